@@ -49,6 +49,13 @@ MOE_STATUS_TIMEOUT = 4
 MOE_WIDE_AUTO = 0
 MOE_WIDE_CUDA_CORES = 1
 MOE_WIDE_TENSOR_CORES = 2
+MOE_T_BF16 = 0
+MOE_T_F32 = 1
+MOE_GATE_NONE = 0
+MOE_GATE_LINEAR = 1
+MOE_GATE_SIGMOID = 2
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 
 
 class moe_cache_desc(C.Structure):
@@ -82,6 +89,7 @@ class moe_views(C.Structure):
 
 
 _vp, _i, _u = C.c_void_p, C.c_int, C.c_uint
+_ll, _fl = C.c_longlong, C.c_float
 _SIGS = {
     "moe_cache_create": [C.POINTER(moe_cache_desc), C.POINTER(C.c_void_p)],
     "moe_cache_destroy": [_vp],
@@ -109,6 +117,15 @@ _SIGS = {
     "moe_lookahead_predict": [_vp, _vp, _vp, _i, _i, _vp, _vp],
     "moe_hybrid_selftest": [_i, _i, _i, _vp, _i, _i, _i, _i, _i, _u, _vp],
     "moe_cpu_experts": [_i, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp],
+    "moe_block_norm": [_vp, _ll, _vp, _ll, _vp, _vp, _ll, _i, _fl, _vp, _fl, _fl, _vp, _ll, _vp,
+                       _ll, _i, _i, _i, _vp],
+    "moe_route": [_vp, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _fl, _vp, _vp, _vp, _vp,
+                  _vp],
+    "moe_route_logits": [_vp, _i, _ll, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _fl, _vp, _vp, _vp],
+    "moe_fp4_quantize": [_i, _vp, _i, _ll, _i, _i, _vp, _vp, _vp, _vp],
+    "moe_fp4_dequantize": [_i, _vp, _vp, _vp, _i, _i, _vp, _i, _ll, _vp],
+    "moe_fp4_global_scale": [_vp, _i, _ll, _i, _i, _vp, _vp],
+    "moe_fp4_linear": [_i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _ll, _vp, _vp],
     "moe_strerror": [_i],
     "moe_last_cuda_error": [],
     "moe_abi_version": [],
@@ -328,6 +345,71 @@ def moe_cpu_experts(wfmt: int, hidden: int, inter: int, blob_ptrs, x_bf16, ids, 
         wfmt, hidden, inter, ptrs.ctypes.data, len(ptrs), x.ctypes.data, ids.ctypes.data,
         slot_ids.ctypes.data, w.ctypes.data, B, k, n_threads, out.ctypes.data))
     return out
+
+
+def moe_block_norm(d_h, d_y, d_post_w, d_gate, d_pre_w, d_h_out, d_x_out, n_rows: int,
+                   hidden: int, *, res_dtype: int = MOE_T_BF16, gate_kind: int = MOE_GATE_NONE,
+                   alpha: float = 1.0, w_offset: float = 0.0, eps: float = 1e-6, h_stride: int = 0,
+                   y_stride: int = 0, gate_stride: int = 0, h_out_stride: int = 0,
+                   x_out_stride: int = 0, stream=None) -> None:
+    """Post-norm, gate, residual add and the next block's pre-norm (see moe_cache.h)."""
+    _check("moe_block_norm", _lib.moe_block_norm(
+        _ptr(d_h), h_stride, _ptr(d_y), y_stride, _ptr(d_post_w), _ptr(d_gate), gate_stride,
+        gate_kind, alpha, _ptr(d_pre_w), w_offset, eps, _ptr(d_h_out), h_out_stride, _ptr(d_x_out),
+        x_out_stride, n_rows, hidden, res_dtype, _stream(stream)))
+
+
+def moe_route(d_x, d_router, d_bias, n_rows: int, hidden: int, n_experts: int, k: int, d_logits,
+              d_ids, d_w, *, score: int = MOE_SCORE_SOFTMAX, n_groups: int = 1,
+              topk_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+              x_stride: int = 0, d_status=None, stream=None) -> None:
+    """Router logits, scores, choice and weights of a step (see moe_cache.h)."""
+    _check("moe_route", _lib.moe_route(
+        _ptr(d_x), x_stride, _ptr(d_router), _ptr(d_bias), n_rows, hidden, n_experts, k, score,
+        n_groups, topk_groups, group_top, int(renorm), scale, _ptr(d_logits), _ptr(d_ids),
+        _ptr(d_w), _ptr(d_status), _stream(stream)))
+
+
+def moe_route_logits(d_logits, dtype: int, d_bias, n_rows: int, n_experts: int, k: int, d_ids, d_w,
+                     *, score: int = MOE_SCORE_SOFTMAX, n_groups: int = 1, topk_groups: int = 1,
+                     group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+                     logits_stride: int = 0, stream=None) -> None:
+    """moe_route's choice from given logits (see moe_cache.h)."""
+    _check("moe_route_logits", _lib.moe_route_logits(
+        _ptr(d_logits), dtype, logits_stride, _ptr(d_bias), n_rows, n_experts, k, score, n_groups,
+        topk_groups, group_top, int(renorm), scale, _ptr(d_ids), _ptr(d_w), _stream(stream)))
+
+
+def moe_fp4_quantize(wfmt: int, d_src, dtype: int, rows: int, cols: int, d_global, d_codes,
+                     d_scales, *, src_stride: int = 0, stream=None) -> None:
+    """One matrix into a blob's code and scale banks (see moe_cache.h)."""
+    _check("moe_fp4_quantize", _lib.moe_fp4_quantize(
+        wfmt, _ptr(d_src), dtype, src_stride, rows, cols, _ptr(d_global), _ptr(d_codes),
+        _ptr(d_scales), _stream(stream)))
+
+
+def moe_fp4_dequantize(wfmt: int, d_codes, d_scales, d_global, rows: int, cols: int, d_dst,
+                       dtype: int, *, dst_stride: int = 0, stream=None) -> None:
+    """The values of a code and a scale bank (see moe_cache.h)."""
+    _check("moe_fp4_dequantize", _lib.moe_fp4_dequantize(
+        wfmt, _ptr(d_codes), _ptr(d_scales), _ptr(d_global), rows, cols, _ptr(d_dst), dtype,
+        dst_stride, _stream(stream)))
+
+
+def moe_fp4_global_scale(d_src, dtype: int, rows: int, cols: int, d_global, *, src_stride: int = 0,
+                         stream=None) -> None:
+    """The NVFP4 global scale of a matrix, into a device float (see moe_cache.h)."""
+    _check("moe_fp4_global_scale", _lib.moe_fp4_global_scale(
+        _ptr(d_src), dtype, src_stride, rows, cols, _ptr(d_global), _stream(stream)))
+
+
+def moe_fp4_linear(wfmt: int, d_x_codes, d_x_scales, d_xg, d_w_codes, d_w_scales, d_wg,
+                   n_rows: int, n: int, k: int, d_out, dtype: int, *, out_stride: int = 0,
+                   d_status=None, stream=None) -> None:
+    """The product of two 4-bit matrices (see moe_cache.h)."""
+    _check("moe_fp4_linear", _lib.moe_fp4_linear(
+        wfmt, _ptr(d_x_codes), _ptr(d_x_scales), _ptr(d_xg), _ptr(d_w_codes), _ptr(d_w_scales),
+        _ptr(d_wg), n_rows, n, k, _ptr(d_out), dtype, out_stride, _ptr(d_status), _stream(stream)))
 
 
 def blob_bytes(wfmt: int, hidden: int, inter: int) -> int:

@@ -57,6 +57,12 @@ int cuda_fail(cudaError_t e, const char* what) {
   return MOE_ERR_CUDA;
 }
 
+}  // namespace
+namespace moe {
+int report_cuda(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+}  // namespace moe
+namespace {
+
 #define CK(call)                                     \
   do {                                               \
     cudaError_t e_ = (call);                         \

@@ -1,0 +1,338 @@
+// route.cu -- the router: logits, scores, grouped choice and weights
+// (formulas in moe_cache.h).
+//
+// Selection: up to 1,024 experts one warp owns a row, lane l the EL consecutive
+// experts from l * EL (EL = 1 .. 32, a power of two), so that a group of experts
+// is a run of lanes.  Choices are compared as unsigned integers in the order of
+// the floats (0 = masked), which makes a pick two warp reductions: the largest
+// key, then the lowest id among its holders.  More experts take one CTA per row
+// with the keys in shared memory.
+#include "block_ops.cuh"
+#include "tile_dot.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ float load_f(const float* p) { return *p; }
+__device__ __forceinline__ float load_f(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// order of floats as unsigned integers; NaN and -inf (masked) are 0
+__device__ __forceinline__ uint32_t choice_key(float c) {
+  if (!(c > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(c + 0.f);  // -0 and +0 tie
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// score numerators: softmax's exp(z - max) or the sigmoid itself
+__device__ __forceinline__ float raw_score(float z, bool softmax, float zmax) {
+  if (!(z > -INFINITY)) return 0.f;
+  if (!softmax) return 1.f / (1.f + expf(-z));
+  if (zmax == INFINITY) return z == INFINITY ? 1.f : 0.f;
+  return expf(z - zmax);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// writes a row's picks: lane r < k holds pick r (id -1: none)
+__device__ __forceinline__ void write_row(const RouteArgs& a, long long b, int lane, int id, float w) {
+  if (lane >= a.k || id < 0) w = 0.f;
+  if (a.renorm) {
+    const float t = warp_sum(w);
+    w = t > 0.f ? w / t : 0.f;
+  }
+  if (lane < a.k) {
+    a.ids[b * a.k + lane] = id;
+    a.w[b * a.k + lane] = w * a.scale;
+  }
+}
+
+template <int EL, typename T>
+__global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a) {
+  const long long b = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (b >= a.rows) return;
+  const int lane = threadIdx.x & 31, e0 = lane * EL;
+  const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  float z[EL], s[EL];
+  uint32_t key[EL];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < EL; ++j) {
+    z[j] = e0 + j < a.E ? load_f(zr + e0 + j) : -INFINITY;
+    mx = fmaxf(mx, z[j]);  // fmaxf drops NaN
+  }
+  if (softmax) mx = warp_max(mx);
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < EL; ++j) sum += s[j] = raw_score(z[j], softmax, mx);
+  if (softmax) {
+    sum = warp_sum(sum);
+#pragma unroll
+    for (int j = 0; j < EL; ++j) s[j] = sum > 0.f ? s[j] / sum : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < EL; ++j) {
+    const bool in = z[j] > -INFINITY;
+    const float c = a.bias ? (in ? s[j] + a.bias[e0 + j] : -INFINITY) : z[j];
+    key[j] = choice_key(c);
+  }
+  if (a.groups > 1) {
+    const int gs = a.E / a.groups;
+    // lane g keeps the scores of groups g and g + 32
+    uint32_t gk[2] = {0u, 0u};
+    for (int g = 0; g < a.groups; ++g) {
+      uint32_t k1 = 0u, k2 = 0u;  // two largest choices
+      float s1 = 0.f, s2 = 0.f;   // two largest scores
+#pragma unroll
+      for (int j = 0; j < EL; ++j) {
+        const int e = e0 + j;
+        if (e < a.E && e / gs == g && key[j]) {
+          const uint32_t kk = key[j];
+          k2 = max(k2, min(k1, kk));
+          k1 = max(k1, kk);
+          s2 = fmaxf(s2, fminf(s1, s[j]));
+          s1 = fmaxf(s1, s[j]);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint32_t q1 = __shfl_xor_sync(kAll, k1, o), q2 = __shfl_xor_sync(kAll, k2, o);
+        const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
+        k2 = max(min(k1, q1), max(k2, q2));
+        k1 = max(k1, q1);
+        s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
+        s1 = fmaxf(s1, t1);
+      }
+      uint32_t sc = k1;
+      if (a.group_top == 2 && k1)
+        sc = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
+      if ((g & 31) == lane) gk[g >> 5] = sc;
+    }
+    unsigned long long keep = 0;
+    for (int t = 0; t < a.topk_groups; ++t) {
+      const uint32_t best = __reduce_max_sync(kAll, max(gk[0], gk[1]));
+      if (!best) break;
+      const unsigned at = gk[0] == best ? lane : gk[1] == best ? lane + 32 : 64;
+      const unsigned g = __reduce_min_sync(kAll, at);
+      keep |= 1ull << g;
+      if ((g & 31) == (unsigned)lane) gk[g >> 5] = 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < EL; ++j)
+      if (e0 + j < a.E && !((keep >> ((e0 + j) / gs)) & 1)) key[j] = 0u;
+  }
+  int my_id = -1;
+  float my_w = 0.f;
+  for (int r = 0; r < a.k; ++r) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int j = 0; j < EL; ++j) top = max(top, key[j]);
+    const uint32_t best = __reduce_max_sync(kAll, top);
+    if (!best) break;
+    unsigned at = 0xffffffffu;
+#pragma unroll
+    for (int j = EL - 1; j >= 0; --j)
+      if (key[j] == best) at = e0 + j;
+    const unsigned id = __reduce_min_sync(kAll, at);
+    float w = 0.f;
+#pragma unroll
+    for (int j = 0; j < EL; ++j)
+      if ((unsigned)(e0 + j) == id) {
+        w = s[j];
+        key[j] = 0u;
+      }
+    w = __shfl_sync(kAll, w, id / EL);
+    if (lane == r) {
+      my_id = (int)id;
+      my_w = w;
+    }
+  }
+  write_row(a, b, lane, my_id, my_w);
+}
+
+constexpr int kBigThreads = 256;
+
+struct BigSmem {
+  float red[kBigThreads / 32];
+  uint32_t key[kBigThreads / 32];
+  unsigned id[kBigThreads / 32];
+  uint32_t gk[64];
+  unsigned long long keep;
+  int pick[32];
+  float w[32];
+};
+
+// more than 1,024 experts: one CTA per row, keys and scores in shared memory
+template <typename T>
+__global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
+  extern __shared__ uint32_t dyn[];
+  __shared__ BigSmem sm;
+  uint32_t* key = dyn;
+  float* s = reinterpret_cast<float*>(dyn + a.E);
+  const long long b = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  float mx = -INFINITY;
+  for (int e = threadIdx.x; e < a.E; e += kBigThreads) mx = fmaxf(mx, load_f(zr + e));
+  mx = warp_max(mx);
+  if (lane == 0) sm.red[warp] = mx;
+  __syncthreads();
+  for (int i = 0; i < kBigThreads / 32; ++i) mx = fmaxf(mx, sm.red[i]);
+  __syncthreads();
+  float sum = 0.f;
+  for (int e = threadIdx.x; e < a.E; e += kBigThreads) sum += raw_score(load_f(zr + e), softmax, mx);
+  sum = warp_sum(sum);
+  if (lane == 0) sm.red[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+  for (int i = 0; i < kBigThreads / 32; ++i) sum += sm.red[i];
+  for (int e = threadIdx.x; e < a.E; e += kBigThreads) {
+    const float z = load_f(zr + e);
+    float sc = raw_score(z, softmax, mx);
+    if (softmax) sc = sum > 0.f ? sc / sum : 0.f;
+    s[e] = sc;
+    key[e] = choice_key(a.bias ? (z > -INFINITY ? sc + a.bias[e] : -INFINITY) : z);
+  }
+  __syncthreads();
+  if (a.groups > 1) {
+    const int gs = a.E / a.groups;
+    for (int g = warp; g < a.groups; g += kBigThreads / 32) {
+      uint32_t k1 = 0u, k2 = 0u;
+      float s1 = 0.f, s2 = 0.f;
+      for (int e = g * gs + lane; e < (g + 1) * gs; e += 32)
+        if (key[e]) {
+          k2 = max(k2, min(k1, key[e]));
+          k1 = max(k1, key[e]);
+          s2 = fmaxf(s2, fminf(s1, s[e]));
+          s1 = fmaxf(s1, s[e]);
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint32_t q1 = __shfl_xor_sync(kAll, k1, o), q2 = __shfl_xor_sync(kAll, k2, o);
+        const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
+        k2 = max(min(k1, q1), max(k2, q2));
+        k1 = max(k1, q1);
+        s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
+        s1 = fmaxf(s1, t1);
+      }
+      uint32_t sc = k1;
+      if (a.group_top == 2 && k1)
+        sc = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
+      if (lane == 0) sm.gk[g] = sc;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unsigned long long keep = 0;
+      for (int t = 0; t < a.topk_groups; ++t) {
+        int at = -1;
+        for (int g = 0; g < a.groups; ++g)
+          if (sm.gk[g] && (at < 0 || sm.gk[g] > sm.gk[at])) at = g;
+        if (at < 0) break;
+        keep |= 1ull << at;
+        sm.gk[at] = 0u;
+      }
+      sm.keep = keep;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kBigThreads)
+      if (!((sm.keep >> (e / gs)) & 1)) key[e] = 0u;
+    __syncthreads();
+  }
+  if (threadIdx.x < 32) sm.pick[threadIdx.x] = -1;
+  for (int r = 0; r < a.k; ++r) {
+    uint32_t top = 0u;
+    unsigned at = 0xffffffffu;
+    for (int e = threadIdx.x; e < a.E; e += kBigThreads)
+      if (key[e] > top) {
+        top = key[e];
+        at = e;
+      }
+    const uint32_t wb = __reduce_max_sync(kAll, top);
+    const unsigned wi = __reduce_min_sync(kAll, top == wb && wb ? at : 0xffffffffu);
+    if (lane == 0) {
+      sm.key[warp] = wb;
+      sm.id[warp] = wi;
+    }
+    __syncthreads();
+    uint32_t best = 0u;
+    unsigned id = 0xffffffffu;
+    for (int i = 0; i < kBigThreads / 32; ++i)
+      if (sm.key[i] > best || (sm.key[i] == best && sm.id[i] < id)) {
+        best = sm.key[i];
+        id = sm.id[i];
+      }
+    if (best && threadIdx.x == 0) {
+      sm.pick[r] = (int)id;
+      sm.w[r] = s[id];
+      key[id] = 0u;
+    }
+    __syncthreads();
+    if (!best) break;
+  }
+  if (warp == 0) write_row(a, b, lane, sm.pick[lane], sm.pick[lane] < 0 ? 0.f : sm.w[lane]);
+}
+
+template <typename T>
+cudaError_t select(const RouteArgs& a, cudaStream_t s) {
+  const unsigned grid = (unsigned)((a.rows + 3LL) / 4);
+  if (a.E <= 32) select_warp_kernel<1, T><<<grid, 128, 0, s>>>(a);
+  else if (a.E <= 64) select_warp_kernel<2, T><<<grid, 128, 0, s>>>(a);
+  else if (a.E <= 128) select_warp_kernel<4, T><<<grid, 128, 0, s>>>(a);
+  else if (a.E <= 256) select_warp_kernel<8, T><<<grid, 128, 0, s>>>(a);
+  else if (a.E <= 512) select_warp_kernel<16, T><<<grid, 128, 0, s>>>(a);
+  else if (a.E <= 1024) select_warp_kernel<32, T><<<grid, 128, 0, s>>>(a);
+  else {
+    static const cudaError_t e = cudaFuncSetAttribute(
+        select_cta_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 8);
+    if (e != cudaSuccess) return e;
+    select_cta_kernel<T><<<a.rows, kBigThreads, (size_t)a.E * 8, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+struct Bf16Rows {
+  const __nv_bfloat16* p;
+  long long stride;
+  __device__ float operator()(int r, int k) const { return __bfloat162float(p[r * stride + k]); }
+};
+struct StoreF32 {
+  float* p;
+  long long stride;
+  __device__ void operator()(int m, int n, float v) const { p[m * stride + n] = v; }
+};
+
+}  // namespace
+
+cudaError_t launch_route_select(const RouteArgs& a, int dtype, cudaStream_t s) {
+  return dtype == MOE_T_F32 ? select<float>(a, s) : select<__nv_bfloat16>(a, s);
+}
+
+cudaError_t launch_route_logits(const __nv_bfloat16* x, long long x_stride,
+                                const __nv_bfloat16* router, int rows, int hidden, int E, float* z,
+                                unsigned long long*, cudaStream_t s) {
+  // rows in slices that keep the grid's y within 65,535
+  for (long long r0 = 0; r0 < rows; r0 += 65535 * 64) {
+    const int n = (int)(rows - r0 < 65535 * 64 ? rows - r0 : 65535 * 64);
+    tile_dot_kernel<<<dim3((E + 63) / 64, (n + 63) / 64), 256, 0, s>>>(
+        Bf16Rows{x + r0 * x_stride, x_stride}, Bf16Rows{router, hidden},
+        StoreF32{z + r0 * E, E}, n, E, hidden);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -517,6 +517,114 @@ MOE_API int moe_routed_experts_noalloc(int wfmt, int hidden, int inter, const vo
                                        int k, void* d_out, unsigned long long* d_status,
                                        void* stream);
 
+/* ---------------------------------------------------------------- around the experts
+ * The operators a decode or prefill step needs next to the cached experts: the
+ * norms before and after a block, the router that makes ids and weights, the
+ * conversions that make 4-bit banks, and the product of 4-bit matrices.  The
+ * pages have no counterpart of these calls; formulas are given with each.
+ * None takes a cache handle, allocates or synchronises: they only enqueue work
+ * on `stream` and may be captured into a CUDA graph.  The first call of each on
+ * a device sets kernel attributes; make it before a capture.  They keep no state
+ * between calls, so calls on different streams may overlap.  Sums and
+ * statistics are fp32 in an order that does not depend on timing: equal inputs
+ * give equal bits.  Row strides count elements; 0 means rows without gaps.
+ * Pointers must be aligned to their element (2 or 4 bytes) where nothing more
+ * is asked; 16-byte aligned rows take the fast paths.  A step of 0 rows is
+ * MOE_OK and enqueues nothing. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 } moe_dtype;
+
+/* The seam between two blocks in one pass over the residual stream:
+ *   z  = y                                                  (d_post_w NULL)
+ *      = y * rsqrt(mean(y^2) + eps) * (w_offset + post_w)   (the block's post-norm)
+ *   h' = h + alpha * act(gate) * z                          (gate_kind NONE: act = 1)
+ *   x' = h' * rsqrt(mean(h'^2) + eps) * (w_offset + pre_w)  (the next block's input)
+ * per row of `hidden` elements (1 .. 32768).  d_h, d_h_out: res_dtype (the residual
+ * stream, bf16 or fp32); d_y, d_x_out, weights and gate: bf16.  d_y NULL: no
+ * block output (h' = h; post_w and gate must be NULL / NONE then).  d_h_out
+ * NULL: h' is not written.  d_pre_w and d_x_out are both given or both NULL.
+ * x' is taken from h' before h' is rounded to res_dtype.  gate: [hidden] used for every row
+ * (gate_stride 0) or one per row (gate_stride >= hidden).  d_h_out may equal
+ * d_h, and d_x_out may equal d_y, with equal strides; no other overlap. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_LINEAR = 1, MOE_GATE_SIGMOID = 2 } moe_gate_kind;
+MOE_API int moe_block_norm(const void* d_h, long long h_stride, const void* d_y, long long y_stride,
+                           const void* d_post_w, const void* d_gate, long long gate_stride,
+                           int gate_kind, float alpha, const void* d_pre_w, float w_offset,
+                           float eps, void* d_h_out, long long h_out_stride, void* d_x_out,
+                           long long x_out_stride, int n_rows, int hidden, int res_dtype,
+                           void* stream);
+
+/* The router.  Logits z[b][e] = sum_h router[e][h] * x[b][h] (bf16 operands,
+ * exact products, fp32 sums), then per row:
+ *   score s = softmax(z) or sigmoid(z);  choice c = s + bias, or z itself where
+ *   d_bias is NULL (the scores' order without their rounding);
+ *   an expert whose logit is NaN or -inf, or whose choice is NaN or -inf, is
+ *   masked: it scores 0 and is never chosen; logits of +inf share a softmax equally;
+ *   groups: experts g*E/G .. (g+1)*E/G - 1 form group g; a group's score is its
+ *   largest choice (group_top 1) or the sum of its two largest (group_top 2; of s where
+ *   d_bias is NULL; a missing second counts 0); the topk_groups groups of largest
+ *   score stay eligible, a tie going to the lower group, groups without an
+ *   unmasked expert never;
+ *   the k experts of largest choice, largest first, a tie going to the lower
+ *   id; weights w = s (never the bias), divided by their sum if renorm, times
+ *   scale (a sum of 0 gives weights 0).  Where fewer than k experts are
+ *   eligible the rest of the row is id -1, weight 0.
+ * d_ids int32 and d_w float32 [n_rows][k] feed moe_decode_layer or moe_admit.
+ * d_logits float32 [n_rows][E], required, receives z.  d_x bf16 (x_stride);
+ * d_router bf16 [E][hidden]; d_bias float32 [E] or NULL.
+ * 1 <= k <= min(32, E), E <= 16384, G <= 64 and a divisor of E (with group_top 2, E/G >= 2).
+ * d_status: device word that receives MOE_STATUS_TIMEOUT if a bounded wait
+ * gives up (NULL = not reported). */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+MOE_API int moe_route(const void* d_x, long long x_stride, const void* d_router,
+                      const float* d_bias, int n_rows, int hidden, int n_experts, int k, int score,
+                      int n_groups, int topk_groups, int group_top, int renorm, float scale,
+                      float* d_logits, int32_t* d_ids, float* d_w, unsigned long long* d_status,
+                      void* stream);
+
+/* The same choice from logits the caller has (dtype bf16 or fp32, logits_stride). */
+MOE_API int moe_route_logits(const void* d_logits, int dtype, long long logits_stride,
+                             const float* d_bias, int n_rows, int n_experts, int k, int score,
+                             int n_groups, int topk_groups, int group_top, int renorm, float scale,
+                             int32_t* d_ids, float* d_w, void* stream);
+
+/* 4-bit conversion of a matrix [rows][cols] (bf16 or fp32) into one code bank
+ * [rows][cols/2] and one scale bank of a blob (wfmt MOE_W_NVFP4 or MOE_W_MXFP4,
+ * layouts as above; cols a multiple of 16 or 32; banks 16-byte aligned), in fp32 operations that round
+ * to nearest even:
+ *   MOE_W_NVFP4, global scale g = *d_global (device; NULL = 1), blocks of 16:
+ *     scale s = e4m3(min(448, amax / (6 * g))), code = e2m1(x / (s * g));
+ *   MOE_W_MXFP4 (d_global must be NULL), blocks of 32:
+ *     scale s = 2^(floor(log2 amax) - 2), within 2^-127 .. 2^127, code = e2m1(x / s).
+ * Magnitudes beyond 6 saturate, the sign of a zero is kept, a scale of 0 gives
+ * codes 0 (a block of zeros takes MXFP4 scale byte 0).  A block that holds a NaN gets a NaN scale
+ * (0x7F, 0xFF): every element reads NaN.  An infinity
+ * takes code 6 under the largest scale (448, 2^126). */
+MOE_API int moe_fp4_quantize(int wfmt, const void* d_src, int dtype, long long src_stride, int rows,
+                             int cols, const float* d_global, uint8_t* d_codes, uint8_t* d_scales,
+                             void* stream);
+
+/* The values the banks stand for: dst = (code * s) * g, rounded to dtype. */
+MOE_API int moe_fp4_dequantize(int wfmt, const uint8_t* d_codes, const uint8_t* d_scales,
+                               const float* d_global, int rows, int cols, void* d_dst, int dtype,
+                               long long dst_stride, void* stream);
+
+/* The global scale that lets a matrix's largest finite magnitude use the whole
+ * NVFP4 range: *d_global = max |x| / 2688 (at least 2^-126; 1 for a matrix
+ * without finite nonzero elements).  Three operations on `stream`. */
+MOE_API int moe_fp4_global_scale(const void* d_src, int dtype, long long src_stride, int rows,
+                                 int cols, float* d_global, void* stream);
+
+/* The product of 4-bit matrices: out[b][i] = g_x * g_w * sum_k x[b][k] w[i][k],
+ * x [n_rows][k] and w [n][k] in the banks moe_fp4_quantize writes (a blob's banks may be passed
+ * where they lie), exact products, fp32 sums; out bf16 or fp32, out_stride.
+ * wfmt MOE_W_NVFP4 or MOE_W_MXFP4 for both; d_xg, d_wg device global scales
+ * (NULL = 1, must be NULL for MXFP4); k a multiple of 32; all four banks
+ * 16-byte aligned.  d_status as moe_route. */
+MOE_API int moe_fp4_linear(int wfmt, const uint8_t* d_x_codes, const uint8_t* d_x_scales,
+                           const float* d_xg, const uint8_t* d_w_codes, const uint8_t* d_w_scales,
+                           const float* d_wg, int n_rows, int n, int k, void* d_out, int dtype,
+                           long long out_stride, unsigned long long* d_status, void* stream);
+
 /* Text of an error code; last CUDA error text seen by this thread. */
 MOE_API const char* moe_strerror(int err);
 MOE_API const char* moe_last_cuda_error(void);
