@@ -10,6 +10,7 @@ There is no fallback: if the shared library is missing this import fails.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -154,9 +155,7 @@ def _check(fn: str, rc: int) -> None:
 
 def _ptr(t) -> int | None:
     """Address of a tensor / array, an int address, or None (NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     if hasattr(t, "data_ptr"):
         return t.data_ptr()
@@ -165,10 +164,20 @@ def _ptr(t) -> int | None:
     raise TypeError(f"cannot take the address of {type(t)}")
 
 
+@functools.lru_cache(maxsize=None)
+def _raw_stream():
+    """torch's function from a device index to its current cudaStream_t, if it has one."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(s) -> int | None:
     """cudaStream_t of a torch stream; None means torch's current stream."""
     if s is None:
         import torch
+        # without a Stream object: 0.2 us of a small call's host time instead of 3 (Grace)
+        if torch.cuda.is_initialized() and _raw_stream():
+            return _raw_stream()(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
