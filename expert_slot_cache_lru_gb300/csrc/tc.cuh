@@ -15,11 +15,6 @@ namespace tc {
 __device__ __forceinline__ uint32_t sa(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
 
 // ---------------------------------------------------------------- mbarriers
 __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t n) {
@@ -43,8 +38,9 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
   return ok != 0;
 }
 
-// A wait longer than this has failed: a whole product takes milliseconds.
-constexpr unsigned long long kWaitNs = 500ull * 1000 * 1000;
+// A wait longer than this (about half a second) has failed: a whole product
+// takes milliseconds.
+constexpr long long kWaitCycles = 1000ll * 1000 * 1000;
 
 __device__ __forceinline__ void raise_abort(int* flag, unsigned long long* status) {
   if (atomicExch(flag, 1) == 0 && status) atomicOr(status, (unsigned long long)MOE_STATUS_TIMEOUT);
@@ -53,34 +49,94 @@ __device__ __forceinline__ void raise_abort(int* flag, unsigned long long* statu
 __device__ __forceinline__ bool wait_bar(uint64_t* b, uint32_t parity, int* flag,
                                          unsigned long long* status) {
   if (mbar_test(b, parity)) return true;
-  const unsigned long long t0 = now_ns();
+  const long long t0 = clock64();
   while (!mbar_test(b, parity)) {
     if (*reinterpret_cast<volatile int*>(flag)) return false;
-    if (now_ns() - t0 > kWaitNs) {
+    if (clock64() - t0 > kWaitCycles) {
       raise_abort(flag, status);
       return false;
     }
   }
   return true;
 }
+// The same for a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int* flag,
+                                          unsigned long long* status) {
+  return __all_sync(0xffffffffu, wait_bar(b, parity, flag, status));
+}
+// One lane of a converged warp.  The tensor-core and TMA instructions take warp-uniform
+// operands: issued under this predicate by a warp that stays together they cost a
+// few cycles, in a branch of lane 0 alone about 70 each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(yes));
+  return yes != 0;
+}
 // Bounded wait that no flag ends: for copies and MMAs in flight before an exit.
 __device__ __forceinline__ void drain_bar(uint64_t* b, uint32_t parity) {
-  const unsigned long long t0 = now_ns();
-  while (!mbar_test(b, parity) && now_ns() - t0 <= kWaitNs) {
+  const long long t0 = clock64();
+  while (!mbar_test(b, parity) && clock64() - t0 <= kWaitCycles) {
   }
 }
 
 // ---------------------------------------------------------------- TMA
+// CG = 2: the copy of either CTA of a pair may signal a barrier of the pair's
+// first CTA; `bar` is then a cluster address.
+template <int CG>
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
-                                         uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3}], [%4];" ::"r"(sa(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(sa(bar))
-      : "memory");
+                                         uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(sa(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(sa(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+
+// `n` bytes of a 16, 8 or 4-byte piece, the rest zeros; counted by the thread's next
+// cp_async_arrive, which arrives at `b` once they are in place.
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int piece, int n) {
+  if (piece == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else if (piece == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(b)) : "memory");
+}
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_peer(uint32_t saddr, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(saddr, rank)) : "memory");
+  return v;
 }
 
 // ---------------------------------------------------------------- tcgen05
@@ -90,73 +146,110 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(where)),
-               "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  if (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(where)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(where)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
 }
+template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
-               : "memory");
+  if (CG == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+                 : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+                 : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar))
-      : "memory");
+// All MMAs issued so far, then one arrival at `bar`; CG = 2: at the barriers of
+// the CTAs in `mask` at that offset.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint16_t mask) {
+  if (CG == 1)
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar))
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(sa(bar)),
+        "h"(mask)
+        : "memory");
 }
-// Shared-memory descriptors: a K-major tile of 128-byte rows, 128-byte swizzle,
-// 8-row groups 1,024 bytes apart; and a block of 32 rows x 16 bytes, no swizzle,
-// 8-row groups 128 bytes apart (scale factors).
+// Shared-memory descriptor of a K-major tile of 128-byte rows, 128-byte swizzle,
+// 8-row groups 1,024 bytes apart.
 __device__ __forceinline__ uint64_t desc_tile(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
-// 512 bytes of scale factors to 4 columns of tensor memory, repeated in each
-// warp's 32 lanes: lane i, column q = bytes 16 i + 4 q .. + 3.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
-// thread t of a warp: lane (its quarter + t), 32 columns from taddr
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+
+// Tensor memory, one warp: thread t holds lane (its quarter + t), column i in r[i].
+#define MOE_TC_R8(r, o) \
+  "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+#define MOE_TC_W8(r, o)                                                                        \
+  "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), \
+      "=r"(r[o + 6]), "=r"(r[o + 7])
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 16 || N == 32, "columns");
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : MOE_TC_W8(r, 0), MOE_TC_W8(r, 8)
+        : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : MOE_TC_W8(r, 0), MOE_TC_W8(r, 8), MOE_TC_W8(r, 16), MOE_TC_W8(r, 24)
+        : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-
-// ---------------------------------------------------------------- clusters
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// r into N columns from taddr, in pieces of 32, 16, 8 and 4
+template <int N, int O = 0>
+__device__ __forceinline__ void tmem_st_all(uint32_t taddr, const uint32_t (&r)[N]) {
+  static_assert((N - O) % 4 == 0, "columns");
+  if constexpr (N - O >= 32) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31};" ::MOE_TC_R8(r, O),
+        MOE_TC_R8(r, O + 8), MOE_TC_R8(r, O + 16), MOE_TC_R8(r, O + 24), "r"(taddr + O)
+        : "memory");
+    tmem_st_all<N, O + 32>(taddr, r);
+  } else if constexpr (N - O >= 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15};" ::MOE_TC_R8(r, O),
+        MOE_TC_R8(r, O + 8), "r"(taddr + O)
+        : "memory");
+    tmem_st_all<N, O + 16>(taddr, r);
+  } else if constexpr (N - O >= 8) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::MOE_TC_R8(r, O),
+        "r"(taddr + O)
+        : "memory");
+    tmem_st_all<N, O + 8>(taddr, r);
+  } else if constexpr (N - O == 4) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[O]),
+                 "r"(r[O + 1]), "r"(r[O + 2]), "r"(r[O + 3]), "r"(taddr + O)
+                 : "memory");
+  }
 }
-__device__ __forceinline__ float ld_peer(uint32_t saddr, int rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- host side

@@ -1,0 +1,591 @@
+// tile_gemm.cuh -- out = P Q^T on the tensor cores for K-major matrices of bf16
+// or block-scaled 4-bit elements: the router's logits and the 4-bit product.
+//
+// A tile is 128 rows of P (256 with a CTA pair, CG = 2) times NT rows of Q;
+// sums are fp32 in tensor memory.  A stage of the pipeline is 128 bytes of every
+// row: 64 bf16 or 256 4-bit elements, four MMAs.  CTAs (or pairs) are persistent
+// and take tiles in turn.  Warps of a CTA:
+//   0..7   epilogue: tensor memory -> registers -> global scales -> out.  Warp w
+//          reads lanes 32 (w % 4) .., half w / 4 of the columns; up to 128 columns two
+//          accumulators alternate, so the next tile's MMAs run beside it;
+//   8..11  block scales (4-bit kinds), shared memory -> tensor memory in the order
+//          the MMA reads.  (tcgen05.cp would copy them too, but measured 52 cycles per 512
+//          bytes in series with the MMAs: 193 us of an 8,192 x 8,192 x 4,096
+//          product against 121 us without any.)
+//   12     TMA loads of the operands;   13   MMAs (issued by the first CTA of a pair);
+//   14..17 block scales, global -> shared memory, 32 bytes of a row at a time: a request
+//          costs a cycle per row it touches, 460 per stage at 16 bytes.
+// A pair halves what each SM takes in of Q, the bound of a lone CTA's 128 x 256
+// tile (48 KB a stage at about 52 bytes per cycle).
+// Scale order: the 32-bit word of row r and K step j belongs in lane r % 32 of
+// every warp's quarter, column r / 32 of block j.  NVFP4: a word is the four
+// scales of one 64-element step; MXFP4: the two scales of two steps, picked by
+// the instruction's scale ids.
+// Where tiles are few, `split` CTAs (pairs) of a cluster share a tile: each sums
+// its part of K and then, through distributed shared memory, its part of the
+// tile's results over the parts in ascending order.
+// Every wait is bounded; on a timeout the CTA reports it, drains its copies and
+// MMAs, frees its tensor memory and returns.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "tc.cuh"
+
+namespace moe {
+namespace tg {
+
+using namespace tc;
+
+enum Kind { kBf16, kNv, kMx };
+
+constexpr int kEpiWarps = 8, kScaleWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kCopyWarp = 14;
+constexpr int kGroups = 3;  // groups of scales in shared memory, 32 bytes of each row
+constexpr int kMaxCluster = 8;
+
+template <Kind KIND, int NT, int CG>
+struct Shape {
+  static constexpr int kQ = NT / CG;                          // Q rows a CTA loads
+  static constexpr int kBlocks = KIND == kNv ? 4 : KIND == kMx ? 2 : 0;  // scale words per row and stage
+  static constexpr int kThreads = 32 * (kBlocks ? 18 : 14);
+  static constexpr int kPer = KIND == kMx ? 2 : 1;            // stages in 16 bytes of a row's scales
+  static constexpr int kQRows = (NT + 31) / 32 * 32;          // Q rows of scales in shared memory
+  static constexpr int kQCols = NT < 128 ? 4 : NT / 32;       // Q columns of a scale block
+  static constexpr int kScaleCols = kBlocks * (4 + kQCols);   // of tensor memory, per stage
+  static constexpr int kStage = 128 * 128 + kQ * 128;
+  static constexpr int kChunk = (128 + kQRows) * 16;          // 16 bytes of every row
+  static constexpr int kScaleSmem = kBlocks ? kGroups * 2 * kChunk : 0;
+  static constexpr int kFit = (226 * 1024 - 1024 - 1024 - kScaleSmem) / kStage;
+  static constexpr int kStages = kFit > 12 ? 12 : kFit;
+  // stages of scales in tensor memory
+  static constexpr int kBufs = !kBlocks ? 1 : 2 * NT + 4 * kScaleCols <= 512 ? 4 : 3;
+  static constexpr int kAcc = 2 * NT + kBufs * kScaleCols <= 512 ? 2 : 1;  // accumulators
+  static constexpr int kUsed = kAcc * NT + kBufs * kScaleCols;
+  static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static constexpr int kSmem = kStages * kStage + kScaleSmem + 1024;
+  static_assert(kUsed <= 512 && kStage % 1024 == 0 && kStages >= kBufs, "tile shape");
+  static_assert(kStages * kStage >= 128 * NT * 4, "room for a partial tile");
+};
+
+struct Args {
+  const uint8_t *ps, *qs;  // scale banks
+  int p_rows, q_rows;
+  int tiles_p, tiles_q;
+  int nk;                  // stages of K
+  int sb;                  // scale bytes per row
+  int piece;               // bytes a row's scales are copied in: 16, 8, 4 or 1
+  int split;               // parts of K
+  const float *g0, *g1;
+  void* out;
+  long long out_stride;
+  int f32, wide;           // wide: 32-byte stores fit the output's alignment
+  unsigned long long* status;
+};
+
+template <int ST>
+struct Ctl {
+  uint64_t full[ST], empty[ST], scaled[4], rows_full[kGroups], rows_empty[kGroups];
+  uint64_t acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int abort_flag, epi_ok[2];  // epi_ok: the epilogue's wait, by tile parity
+};
+
+// tiles in strips of 8 P tiles, so that concurrent CTAs share operands in L2
+__device__ __forceinline__ void tile_at(const Args& a, int t, int& tp, int& tq) {
+  const int per = 8 * a.tiles_q, g = t / per, r = t - g * per;
+  const int n = min(8, a.tiles_p - g * 8);
+  tp = g * 8 + r % n;
+  tq = r / n;
+}
+
+// 16 bytes of a row's scales in smaller pieces, zeros beyond the row
+__device__ __noinline__ void copy_ragged(uint32_t dst, const uint8_t* row, int off, int sb, int piece) {
+  if (piece > 1) {
+    for (int o = 0; o < 16; o += piece) {
+      const bool in = off + o < sb;
+      cp_async(dst + o, row + (in ? off + o : 0), piece, in ? piece : 0);
+    }
+    return;
+  }
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w = 0;
+    for (int j = 0; j < 4; ++j)
+      if (off + 4 * i + j < sb) w |= (uint32_t)__ldg(row + off + 4 * i + j) << (8 * j);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4 * i), "r"(w) : "memory");
+  }
+}
+// bytes off .. off + 15 of a row's scales (row null: zeros)
+__device__ __forceinline__ void copy_scales(uint32_t dst, const uint8_t* row, int off, const Args& a) {
+  if (a.piece == 16 || !row) {
+    const bool in = row && off < a.sb;
+    cp_async(dst, in ? row + off : a.ps, 16, in ? 16 : 0);
+  } else {
+    copy_ragged(dst, row, off, a.sb, a.piece);
+  }
+}
+
+// Instruction descriptors: K-major operands, fp32 sums.  4 bits: e2m1 x e2m1, K 64, scales
+// e4m3 or e8m0, `id` the scale bytes of a word; bf16: K 16.
+template <Kind KIND>
+__device__ __forceinline__ uint32_t idesc(int m, int n, int id) {
+  const uint32_t mn = ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+  if (KIND == kBf16) return mn | (1u << 4) | (1u << 7) | (1u << 10);
+  return mn | ((uint32_t)id << 4) | (1u << 7) | (1u << 10) | (KIND == kNv ? 0u : 1u << 23) |
+         ((uint32_t)id << 29);
+}
+#define MOE_TG_MMA4(cg, kind, vec)                                                              \
+  asm volatile(                                                                                 \
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"                                             \
+      " tcgen05.mma.cta_group::" cg ".kind::" kind ".block_scale.scale_vec::" vec               \
+      " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),                                        \
+      "l"(p), "l"(q), "r"(id), "r"(sp), "r"(sq), "r"(acc)                                       \
+      : "memory")
+#define MOE_TG_MMA16(cg)                                                                        \
+  asm volatile(                                                                                 \
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"                                             \
+      " tcgen05.mma.cta_group::" cg ".kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),            \
+      "l"(p), "l"(q), "r"(id), "r"(acc)                                                         \
+      : "memory")
+template <Kind KIND, int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t p, uint64_t q, uint32_t id, uint32_t sp,
+                                    uint32_t sq, uint32_t acc) {
+  if constexpr (KIND == kBf16) {
+    if constexpr (CG == 1) MOE_TG_MMA16("1");
+    else MOE_TG_MMA16("2");
+  } else if constexpr (KIND == kNv) {
+    if constexpr (CG == 1) MOE_TG_MMA4("1", "mxf4nvf4", "4X");
+    else MOE_TG_MMA4("2", "mxf4nvf4", "4X");
+  } else {
+    if constexpr (CG == 1) MOE_TG_MMA4("1", "mxf4", "2X");
+    else MOE_TG_MMA4("2", "mxf4", "2X");
+  }
+}
+#undef MOE_TG_MMA4
+#undef MOE_TG_MMA16
+
+__device__ __forceinline__ void store_one(const Args& a, long long at, float v) {
+  if (a.f32) static_cast<float*>(a.out)[at] = v;
+  else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ float global_scale(const Args& a) {
+  return (a.g0 ? *a.g0 : 1.f) * (a.g1 ? *a.g1 : 1.f);
+}
+
+// SWAP: out[q][p] (P the weights, Q the tokens); else out[p][q].
+template <Kind KIND, int NT, int CG, bool SWAP>
+__global__ void __launch_bounds__(Shape<KIND, NT, CG>::kThreads, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
+            const Args a) {
+  using T = Shape<KIND, NT, CG>;
+  constexpr int ST = T::kStages, kThreads = T::kThreads;
+  extern __shared__ uint8_t raw[];
+  uint8_t* stg = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sstg = stg + (size_t)ST * T::kStage;
+  __shared__ Ctl<ST> c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // cluster: `split` parts of K, each CG CTAs; a lone CTA's cluster is itself
+  const int crank = CG == 1 && a.split == 1 ? 0 : (int)cluster_rank();
+  const int pair = crank % CG, first = crank - pair, part = crank / CG;
+  const int team = CG * a.split;
+  // a part of K starts at a whole 16 bytes of scales
+  const int nkp = (a.nk + T::kPer - 1) / T::kPer;
+  const int k_lo = nkp * part / a.split * T::kPer,
+            k_hi = min(a.nk, nkp * (part + 1) / a.split * T::kPer), n_k = k_hi - k_lo;
+  const int n_tiles = a.tiles_p * a.tiles_q, tile0 = blockIdx.x / team, step = gridDim.x / team;
+  const uint16_t mask = (uint16_t)(((1 << CG) - 1) << first);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&c.full[i], 1);
+      mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&c.scaled[i], 4 * CG);
+    for (int i = 0; i < kGroups; ++i) {
+      mbar_init(&c.rows_full[i], 128);
+      mbar_init(&c.rows_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.acc_full[i], 1);
+      mbar_init(&c.acc_empty[i], kEpiWarps * CG);
+    }
+    mbar_init(&c.drain, 1);
+    c.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc<CG>(&c.tmem, T::kCols);
+  fence_before();
+  __syncthreads();
+  if (CG > 1) cluster_sync();  // the peer's barriers exist before anything arrives there
+  fence_after();
+  const uint32_t tmem = c.tmem;
+
+  if (warp == kTmaWarp) {
+    int it = 0, s = 0;
+    bool ok = true;
+    for (int t = tile0; t < n_tiles && ok; t += step) {
+      int tp, tq;
+      tile_at(a, t, tp, tq);
+      for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
+        if (it >= ST && !warp_wait(&c.empty[s], (it / ST - 1) & 1, &c.abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* p = stg + (size_t)s * T::kStage;
+          const int x = ks * (KIND == kBf16 ? 64 : 128);
+          // a pair's copies all count on the first CTA's barrier
+          if (pair == 0) mbar_expect(&c.full[s], CG * T::kStage);
+          const uint32_t bar = CG == 1 ? sa(&c.full[s]) : peer_addr(sa(&c.full[s]), first);
+          tma_load<CG>(p, &pmap, x, (tp * CG + pair) * 128, bar);
+          tma_load<CG>(p + 128 * 128, &qmap, x, tq * NT + pair * T::kQ, bar);
+        }
+        __syncwarp();
+        s = s + 1 == ST ? 0 : s + 1;
+      }
+    }
+    if (!ok) {  // the copies in flight land before the CTA ends
+      if (pair == 0)
+        for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_bar(&c.full[i % ST], (i / ST) & 1);
+      else  // their barrier is the peer's: a copy takes microseconds
+        for (const long long t0 = clock64(); clock64() - t0 < 1000 * 1000;) {
+        }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (pair == 0) {
+      int u = 0, s = 0, sbuf = 0;
+      uint32_t full_par = 0, scaled_par = 0;  // parities of this round through the rings
+      bool ok = true;
+      const uint64_t p_base = desc_tile(sa(stg)), q_base = desc_tile(sa(stg) + 128 * 128);
+      for (int t = tile0; t < n_tiles && ok; t += step, ++u) {
+        const int b = u % T::kAcc;
+        if (u >= T::kAcc &&
+            !warp_wait(&c.acc_empty[b], (u / T::kAcc - 1) & 1, &c.abort_flag, a.status))
+          break;
+        const uint32_t d = tmem + b * NT;
+        for (int i = 0; i < n_k; ++i) {
+          if ((T::kBlocks && !warp_wait(&c.scaled[sbuf], scaled_par, &c.abort_flag, a.status)) ||
+              !warp_wait(&c.full[s], full_par, &c.abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          if (elect_one()) {
+            const uint64_t p0 = p_base + (uint64_t)(s * (T::kStage / 16)),
+                           q0 = q_base + (uint64_t)(s * (T::kStage / 16));
+            const uint32_t cp = tmem + T::kAcc * NT + sbuf * T::kScaleCols, cq = cp + 4 * T::kBlocks;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // 32 bytes of every row each
+              const int w = KIND == kMx ? j / 2 : j, id = KIND == kMx ? 2 * (j & 1) : 0;
+              mma<KIND, CG>(d, p0 + 2 * j, q0 + 2 * j, idesc<KIND>(128 * CG, NT, id), cp + 4 * w,
+                            cq + T::kQCols * w, j > 0 || i > 0);
+            }
+            mma_commit<CG>(&c.empty[s], mask);
+          }
+          __syncwarp();
+          if (++s == ST) s = 0, full_par ^= 1;
+          if (++sbuf == T::kBufs) sbuf = 0, scaled_par ^= 1;
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit<CG>(&c.acc_full[b], mask);
+        __syncwarp();
+      }
+      if (elect_one()) mma_commit<CG>(&c.drain, mask);
+      __syncwarp();
+    }
+    drain_bar(&c.drain, 0);  // every MMA has finished before the tensor memory is freed
+    __syncwarp();
+  } else if (warp >= kCopyWarp) {
+    if constexpr (T::kBlocks > 0) {
+      // two threads per row: 16 bytes each of the 32 that a group holds
+      const int tid = threadIdx.x - 32 * kCopyWarp, half = tid & 1, r0 = tid >> 1;
+      const uint32_t base = sa(sstg) + half * T::kChunk;
+      constexpr int PR = 2, QR = (NT + 63) / 64;  // rows per thread, 64 apart
+      int it = 0, slot = 0;
+      bool ok = true;
+      for (int t = tile0; t < n_tiles && ok; t += step) {
+        int tp, tq;
+        tile_at(a, t, tp, tq);
+        const uint8_t *pr[PR], *qr[QR];
+#pragma unroll
+        for (int i = 0; i < PR; ++i) {
+          const long long p = ((long long)tp * CG + pair) * 128 + r0 + 64 * i;
+          pr[i] = p < a.p_rows ? a.ps + p * a.sb : nullptr;
+        }
+#pragma unroll
+        for (int i = 0; i < QR; ++i) {
+          const long long q = (long long)tq * NT + r0 + 64 * i;
+          qr[i] = q < a.q_rows ? a.qs + q * a.sb : nullptr;
+        }
+        // groups start at the first stage of the tile's part of K
+        for (int ks = k_lo; ks < k_hi; ks += 2 * T::kPer, ++it) {
+          if (it >= kGroups &&
+              !warp_wait(&c.rows_empty[slot], (it / kGroups - 1) & 1, &c.abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          const int off = ks * (16 / T::kPer) + 16 * half;
+          const uint32_t dst = base + slot * 2 * T::kChunk + r0 * 16;
+#pragma unroll
+          for (int i = 0; i < PR; ++i) copy_scales(dst + 64 * 16 * i, pr[i], off, a);
+#pragma unroll
+          for (int i = 0; i < QR; ++i)
+            if (r0 + 64 * i < NT) copy_scales(dst + (128 + 64 * i) * 16, qr[i], off, a);
+          if (a.piece > 1) {
+            cp_async_arrive(&c.rows_full[slot]);
+          } else {  // rows without a tile and ragged rows alike
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            mbar_arrive(&c.rows_full[slot]);
+          }
+          slot = slot + 1 == kGroups ? 0 : slot + 1;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    __syncwarp();
+  } else if (warp >= kScaleWarp) {
+    if constexpr (T::kBlocks > 0) {
+      const uint32_t quarter = (uint32_t)(32 * (warp - kScaleWarp)) << 16;
+      int it = 0, group = 0, slot = 0, buf = 0;
+      bool ok = true;
+      for (int t = tile0; t < n_tiles && ok; t += step) {
+        int in_group = 0;
+        for (int i = 0; i < n_k; ++i, ++it) {
+          if (in_group == 0 &&
+              !warp_wait(&c.rows_full[slot], (group / kGroups) & 1, &c.abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          // lane's rows, lane + 32 q: word j of row q belongs in column q of block j
+          const uint8_t* sp = sstg + (slot * 2 + in_group / T::kPer) * T::kChunk + lane * 16 +
+                              (KIND == kMx ? 8 * (in_group & 1) : 0);
+          uint32_t w[T::kScaleCols];
+#pragma unroll
+          for (int q = 0; q < 4 + T::kQCols; ++q) {
+            uint32_t v[4] = {0, 0, 0, 0};
+            if (q < 4 || 32 * (q - 4) < T::kQRows) {
+              if constexpr (KIND == kNv) {
+                const uint4 x = *reinterpret_cast<const uint4*>(sp + 512 * q);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+              } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(sp + 512 * q);
+                v[0] = x.x, v[1] = x.y;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < T::kBlocks; ++j)
+              w[q < 4 ? 4 * j + q : 4 * T::kBlocks + T::kQCols * j + q - 4] = v[j];
+          }
+          if (++in_group == 2 * T::kPer || i + 1 == n_k) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.rows_empty[slot]);
+            in_group = 0;
+            ++group;
+            slot = slot + 1 == kGroups ? 0 : slot + 1;
+          }
+          // a buffer's previous scales have been used once MMA it - kBufs is done
+          if (it >= T::kBufs) {
+            const int was = it - T::kBufs;
+            if (!warp_wait(&c.empty[was % ST], (was / ST) & 1, &c.abort_flag, a.status)) {
+              ok = false;
+              break;
+            }
+          }
+          fence_after();
+          const uint32_t at = tmem + quarter + T::kAcc * NT + buf * T::kScaleCols;
+          tmem_st_all(at, w);
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 1) mbar_arrive(&c.scaled[buf]);
+            else mbar_arrive_at(peer_addr(sa(&c.scaled[buf]), first));
+          }
+          buf = buf + 1 == T::kBufs ? 0 : buf + 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const float g = global_scale(a);
+    constexpr int W = NT < 64 ? 16 : 32;  // columns read at a time
+    int u = 0;
+    for (int t = tile0; t < n_tiles; t += step, ++u) {
+      const int b = u % T::kAcc;
+      int tp, tq;
+      tile_at(a, t, tp, tq);
+      if (threadIdx.x == 0)
+        c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], (u / T::kAcc) & 1, &c.abort_flag, a.status);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (!c.epi_ok[u & 1]) break;
+      fence_after();
+      const int pr = 32 * (warp & 3) + lane;
+      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + b * NT;
+      const long long p = ((long long)tp * CG + pair) * 128 + pr;
+#pragma unroll 1
+      for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
+        const long long q0 = (long long)tq * NT + n0;
+        if (q0 >= a.q_rows) break;
+        uint32_t v[W];
+        tmem_ld(acc + n0, v);
+        tmem_wait_ld();
+        const int nq = (int)(a.q_rows - q0 < W ? a.q_rows - q0 : W);
+        if (a.split > 1) {  // partial sums, [column][row], for the cluster's reduction
+          float* sum = reinterpret_cast<float*>(stg);
+#pragma unroll
+          for (int i = 0; i < W; ++i) sum[(n0 + i) * 128 + pr] = __uint_as_float(v[i]);
+        } else if (SWAP) {
+          if (p < a.p_rows) {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+              if (i < nq) store_one(a, (q0 + i) * a.out_stride + p, __uint_as_float(v[i]) * g);
+          }
+        } else if (p < a.p_rows) {
+          const long long at = p * a.out_stride + q0;
+          if (a.wide && nq == W) {
+            if (a.f32) {
+              float* o = static_cast<float*>(a.out) + at;
+#pragma unroll
+              for (int i = 0; i < W; i += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__uint_as_float(v[i + j]) * g);
+                store32(o + i, w);
+              }
+            } else {
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll
+              for (int i = 0; i < W; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  w[j] = pack2(__uint_as_float(v[i + 2 * j]) * g, __uint_as_float(v[i + 2 * j + 1]) * g);
+                store32(o + i, w);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+              if (i < nq) store_one(a, at + i, __uint_as_float(v[i]) * g);
+          }
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1) mbar_arrive(&c.acc_empty[b]);
+        else mbar_arrive_at(peer_addr(sa(&c.acc_empty[b]), first));
+      }
+    }
+    __syncwarp();
+  }
+  if (CG > 1 || a.split > 1) cluster_sync();
+  if (a.split > 1) {
+    // one tile per cluster: this part's share of its results, summed over the parts
+    int tp, tq;
+    tile_at(a, tile0, tp, tq);
+    const long long left = a.q_rows - (long long)tq * NT;
+    const int cols = (int)(left < NT ? left : NT);
+    const float g = global_scale(a);
+    const uint32_t sums = sa(stg);
+    const int n = cols * 128;
+    for (int i = part * kThreads + threadIdx.x; i < n; i += a.split * kThreads) {
+      // SWAP: neighbouring threads take neighbouring rows (outputs of one token);
+      // else neighbouring columns
+      const int col = SWAP ? i >> 7 : i % cols, row = SWAP ? i & 127 : i / cols;
+      float v = 0.f;
+      for (int k = 0; k < a.split; ++k) v += ld_peer(sums + 4 * (col * 128 + row), k * CG + pair);
+      const long long p = ((long long)tp * CG + pair) * 128 + row, q = (long long)tq * NT + col;
+      if (p < a.p_rows && !c.abort_flag)
+        store_one(a, SWAP ? q * a.out_stride + p : p * a.out_stride + q, v * g);
+    }
+    cluster_sync();  // a peer may still be reading this CTA's sums
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    fence_after();
+    tmem_free<CG>(tmem, T::kCols);
+  }
+}
+
+// What a caller fills in: the matrices and the output.
+struct Problem {
+  const void *p, *q;           // K-major rows; p_stride, q_stride bytes apart
+  long long p_stride, q_stride;
+  int p_rows, q_rows, k;
+  const uint8_t *ps, *qs;      // scale banks (4-bit kinds)
+  const float *g0, *g1;
+  void* out;
+  long long out_stride;
+  bool f32;
+  unsigned long long* status;
+};
+
+// Parts of K that give every SM a CTA where tiles are few.
+inline int split_for(long long tiles, int nk, int cg, int sms) {
+  int s = 1;
+  while (s + 1 <= kMaxCluster / cg && s + 1 <= nk && tiles * cg * (s + 1) <= sms) ++s;
+  return s;
+}
+
+template <Kind KIND, int NT, int CG, bool SWAP>
+cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
+  using T = Shape<KIND, NT, CG>;
+  auto kern = gemm_kernel<KIND, NT, CG, SWAP>;
+  static const cudaError_t set =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  if (set != cudaSuccess) return set;
+  Args a{};
+  a.ps = l.ps;
+  a.qs = l.qs;
+  a.p_rows = l.p_rows;
+  a.q_rows = l.q_rows;
+  a.tiles_p = (l.p_rows + 128 * CG - 1) / (128 * CG);
+  a.tiles_q = (l.q_rows + NT - 1) / NT;
+  const int slab = KIND == kBf16 ? 64 : 256;
+  a.nk = (l.k + slab - 1) / slab;
+  a.sb = KIND == kBf16 ? 0 : l.k / (KIND == kNv ? 16 : 32);
+  a.piece = a.sb % 16 == 0 ? 16 : a.sb % 8 == 0 ? 8 : a.sb % 4 == 0 ? 4 : 1;
+  a.g0 = l.g0;
+  a.g1 = l.g1;
+  a.out = l.out;
+  a.out_stride = l.out_stride;
+  a.f32 = l.f32;
+  a.wide = (reinterpret_cast<uintptr_t>(l.out) & 31) == 0 && l.out_stride % (l.f32 ? 8 : 16) == 0;
+  a.status = l.status;
+  const long long tiles = (long long)a.tiles_p * a.tiles_q;
+  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  a.split = split_for(tiles, (a.nk + T::kPer - 1) / T::kPer, CG, sms);
+  const int team = CG * a.split;
+  CUtensorMap pm, qm;
+  const int elem = KIND == kBf16 ? 2 : 1;
+  const long long width = KIND == kBf16 ? l.k : l.k / 2;
+  cudaError_t e = make_map(&pm, l.p, elem, width, l.p_rows, l.p_stride, 128);
+  if (e == cudaSuccess) e = make_map(&qm, l.q, elem, width, l.q_rows, l.q_stride, T::kQ);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  const long long teams = tiles < sms / team ? tiles : sms / team;
+  cfg.gridDim = dim3((unsigned)(teams * team));
+  cfg.blockDim = dim3(T::kThreads);
+  cfg.dynamicSmemBytes = T::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)team, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, pm, qm, a);
+}
+
+}  // namespace tg
+}  // namespace moe
