@@ -8,13 +8,14 @@
 //   0..7   epilogue: tensor memory -> registers -> global scales -> out.  Warp w
 //          reads lanes 32 (w % 4) .., half w / 4 of the columns; up to 128 columns two
 //          accumulators alternate, so the next tile's MMAs run beside it;
-//   8..11  block scales (4-bit kinds), shared memory -> tensor memory in the order
-//          the MMA reads.  (tcgen05.cp would copy them too, but measured 52 cycles per 512
-//          bytes in series with the MMAs: 193 us of an 8,192 x 8,192 x 4,096
-//          product against 121 us without any.)
-//   12     TMA loads of the operands;   13   MMAs (issued by the first CTA of a pair);
-//   14..17 block scales, global -> shared memory, 32 bytes of a row at a time: a request
-//          costs a cycle per row it touches, 460 per stage at 16 bytes.
+//   8..15  block scales (4-bit kinds), shared memory -> tensor memory in the order
+//          the MMA reads, two groups of four warps on alternate stages (one group alone
+//          left the MMAs of an 8,192 x 8,192 x 4,096 product waiting: 150 us).
+//          (tcgen05.cp would copy them too, but measured 52 cycles per 512 bytes in
+//          series with the MMAs.)
+//   16..19 block scales, global -> shared memory, 32 bytes of a row at a time: a request
+//          costs a cycle per row it touches, 460 per stage at 16 bytes;
+//   then   one warp of TMA loads of the operands, one of MMAs (the first CTA's of a pair).
 // A pair halves what each SM takes in of Q, the bound of a lone CTA's 128 x 256
 // tile (48 KB a stage at about 52 bytes per cycle).
 // Scale order: the 32-bit word of row r and K step j belongs in lane r % 32 of
@@ -39,7 +40,7 @@ using namespace tc;
 
 enum Kind { kBf16, kNv, kMx };
 
-constexpr int kEpiWarps = 8, kScaleWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kCopyWarp = 14;
+constexpr int kEpiWarps = 8, kScaleWarp = 8, kCopyWarp = 16;
 constexpr int kGroups = 3;  // groups of scales in shared memory, 32 bytes of each row
 constexpr int kMaxCluster = 8;
 
@@ -47,7 +48,8 @@ template <Kind KIND, int NT, int CG>
 struct Shape {
   static constexpr int kQ = NT / CG;                          // Q rows a CTA loads
   static constexpr int kBlocks = KIND == kNv ? 4 : KIND == kMx ? 2 : 0;  // scale words per row and stage
-  static constexpr int kThreads = 32 * (kBlocks ? 18 : 14);
+  static constexpr int kTmaWarp = kBlocks ? 20 : kEpiWarps, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kPer = KIND == kMx ? 2 : 1;            // stages in 16 bytes of a row's scales
   static constexpr int kQRows = (NT + 31) / 32 * 32;          // Q rows of scales in shared memory
   static constexpr int kQCols = NT < 128 ? 4 : NT / 32;       // Q columns of a scale block
@@ -211,7 +213,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     for (int i = 0; i < 4; ++i) mbar_init(&c.scaled[i], 4 * CG);
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(&c.rows_full[i], 128);
-      mbar_init(&c.rows_empty[i], 4);
+      mbar_init(&c.rows_empty[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.acc_full[i], 1);
@@ -221,14 +223,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     c.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) tmem_alloc<CG>(&c.tmem, T::kCols);
+  if (warp == T::kMmaWarp) tmem_alloc<CG>(&c.tmem, T::kCols);
   fence_before();
   __syncthreads();
   if (CG > 1) cluster_sync();  // the peer's barriers exist before anything arrives there
   fence_after();
   const uint32_t tmem = c.tmem;
 
-  if (warp == kTmaWarp) {
+  if (warp == T::kTmaWarp) {
     int it = 0, s = 0;
     bool ok = true;
     for (int t = tile0; t < n_tiles && ok; t += step) {
@@ -260,7 +262,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == T::kMmaWarp) {
     if (pair == 0) {
       int u = 0, s = 0, sbuf = 0;
       uint32_t full_par = 0, scaled_par = 0;  // parities of this round through the rings
@@ -354,63 +356,61 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     __syncwarp();
   } else if (warp >= kScaleWarp) {
     if constexpr (T::kBlocks > 0) {
-      const uint32_t quarter = (uint32_t)(32 * (warp - kScaleWarp)) << 16;
-      int it = 0, group = 0, slot = 0, buf = 0;
+      const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+      const unsigned mine = (warp - kScaleWarp) >> 2;  // takes the stages of this parity
+      unsigned it = 0, group = 0;
       bool ok = true;
       for (int t = tile0; t < n_tiles && ok; t += step) {
-        int in_group = 0;
-        for (int i = 0; i < n_k; ++i, ++it) {
-          if (in_group == 0 &&
-              !warp_wait(&c.rows_full[slot], (group / kGroups) & 1, &c.abort_flag, a.status)) {
+        for (int ks = k_lo; ks < k_hi && ok; ks += 2 * T::kPer, ++group) {
+          const unsigned slot = group % kGroups, m = min(2 * T::kPer, k_hi - ks);
+          if (!warp_wait(&c.rows_full[slot], (group / kGroups) & 1, &c.abort_flag, a.status)) {
             ok = false;
             break;
           }
-          // lane's rows, lane + 32 q: word j of row q belongs in column q of block j
-          const uint8_t* sp = sstg + (slot * 2 + in_group / T::kPer) * T::kChunk + lane * 16 +
-                              (KIND == kMx ? 8 * (in_group & 1) : 0);
-          uint32_t w[T::kScaleCols];
+#pragma unroll 1
+          for (unsigned x = (it ^ mine) & 1; x < m; x += 2) {
+            const unsigned n = it + x, buf = n % T::kBufs;
+            // lane's rows, lane + 32 q: word j of row q belongs in column q of block j
+            const uint8_t* sp = sstg + (slot * 2 + x / T::kPer) * T::kChunk + lane * 16 +
+                                (KIND == kMx ? 8 * (x & 1) : 0);
+            uint32_t w[T::kScaleCols];
 #pragma unroll
-          for (int q = 0; q < 4 + T::kQCols; ++q) {
-            uint32_t v[4] = {0, 0, 0, 0};
-            if (q < 4 || 32 * (q - 4) < T::kQRows) {
-              if constexpr (KIND == kNv) {
-                const uint4 x = *reinterpret_cast<const uint4*>(sp + 512 * q);
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-              } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(sp + 512 * q);
-                v[0] = x.x, v[1] = x.y;
+            for (int q = 0; q < 4 + T::kQCols; ++q) {
+              uint32_t v[4] = {0, 0, 0, 0};
+              if (q < 4 || 32 * (q - 4) < T::kQRows) {
+                if constexpr (KIND == kNv) {
+                  const uint4 u = *reinterpret_cast<const uint4*>(sp + 512 * q);
+                  v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+                } else {
+                  const uint2 u = *reinterpret_cast<const uint2*>(sp + 512 * q);
+                  v[0] = u.x, v[1] = u.y;
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < T::kBlocks; ++j)
+                w[q < 4 ? 4 * j + q : 4 * T::kBlocks + T::kQCols * j + q - 4] = v[j];
+            }
+            // a buffer's previous scales have been used once MMA n - kBufs is done
+            if (n >= T::kBufs) {
+              const unsigned was = n - T::kBufs;
+              if (!warp_wait(&c.empty[was % ST], (was / ST) & 1, &c.abort_flag, a.status)) {
+                ok = false;
+                break;
               }
             }
-#pragma unroll
-            for (int j = 0; j < T::kBlocks; ++j)
-              w[q < 4 ? 4 * j + q : 4 * T::kBlocks + T::kQCols * j + q - 4] = v[j];
-          }
-          if (++in_group == 2 * T::kPer || i + 1 == n_k) {
+            fence_after();
+            tmem_st_all(tmem + quarter + T::kAcc * NT + buf * T::kScaleCols, w);
+            tmem_wait_st();
+            fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.rows_empty[slot]);
-            in_group = 0;
-            ++group;
-            slot = slot + 1 == kGroups ? 0 : slot + 1;
-          }
-          // a buffer's previous scales have been used once MMA it - kBufs is done
-          if (it >= T::kBufs) {
-            const int was = it - T::kBufs;
-            if (!warp_wait(&c.empty[was % ST], (was / ST) & 1, &c.abort_flag, a.status)) {
-              ok = false;
-              break;
+            if (lane == 0) {
+              if (CG == 1) mbar_arrive(&c.scaled[buf]);
+              else mbar_arrive_at(peer_addr(sa(&c.scaled[buf]), first));
             }
           }
-          fence_after();
-          const uint32_t at = tmem + quarter + T::kAcc * NT + buf * T::kScaleCols;
-          tmem_st_all(at, w);
-          tmem_wait_st();
-          fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if (CG == 1) mbar_arrive(&c.scaled[buf]);
-            else mbar_arrive_at(peer_addr(sa(&c.scaled[buf]), first));
-          }
-          buf = buf + 1 == T::kBufs ? 0 : buf + 1;
+          if (lane == 0) mbar_arrive(&c.rows_empty[slot]);
+          it += m;
         }
       }
     }
@@ -512,7 +512,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   }
   fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == T::kMmaWarp) {
     fence_after();
     tmem_free<CG>(tmem, T::kCols);
   }
