@@ -31,10 +31,12 @@ cudaError_t by_rows(const Fp4Linear& l, int sms, cudaStream_t s) {
   if (l.rows <= 16) return tg::launch<KIND, 16, 1, true>(p, sms, s);
   if (l.rows <= 32) return tg::launch<KIND, 32, 1, true>(p, sms, s);
   if (l.rows <= 64) return tg::launch<KIND, 64, 1, true>(p, sms, s);
-  // the largest tile that still gives every SM one
-  const long long tp = (l.rows + 127) / 128;
-  if ((tp + 1) / 2 * 2 * ((l.n + 191) / 192) >= sms) return tg::launch<KIND, 192, 2, false>(p, sms, s);
-  if (tp * ((l.n + 127) / 128) >= sms) return tg::launch<KIND, 128, 1, false>(p, sms, s);
+  // the tile that asks least of an SM's intake
+  const long long c64 = tg::intake<KIND, 64, 1>(l.rows, l.n, l.k, sms),
+                  c128 = tg::intake<KIND, 128, 1>(l.rows, l.n, l.k, sms),
+                  c192 = tg::intake<KIND, 192, 2>(l.rows, l.n, l.k, sms);
+  if (c192 <= c128 && c192 <= c64) return tg::launch<KIND, 192, 2, false>(p, sms, s);
+  if (c128 <= c64) return tg::launch<KIND, 128, 1, false>(p, sms, s);
   return tg::launch<KIND, 64, 1, false>(p, sms, s);
 }
 

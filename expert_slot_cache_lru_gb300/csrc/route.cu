@@ -7,8 +7,14 @@
 // the floats (0 = masked), which makes a pick two warp reductions: the largest
 // key, then the lowest id among its holders.  More experts take one CTA per row
 // with the keys in shared memory.
+//
+// Logits: up to kDotRows rows are dot products, one CTA per expert (its router row
+// read once for all rows); more rows are a product on the tensor cores (tile_gemm.cuh),
+// whose operands must start on 16 bytes; other layouts take tile_dot.cuh.  The selection
+// is a second launch that starts while the logits are computed and waits for them.
 #include "block_ops.cuh"
 #include "tile_dot.cuh"
+#include "tile_gemm.cuh"
 
 namespace moe {
 namespace {
@@ -67,6 +73,7 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 31, e0 = lane * EL;
   const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  tc::pdl_wait();
   float z[EL], s[EL];
   uint32_t key[EL];
   float mx = -INFINITY;
@@ -187,6 +194,7 @@ __global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  tc::pdl_wait();
   float mx = -INFINITY;
   for (int e = threadIdx.x; e < a.E; e += kBigThreads) mx = fmaxf(mx, load_f(zr + e));
   mx = warp_max(mx);
@@ -287,22 +295,79 @@ __global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
   if (warp == 0) write_row(a, b, lane, sm.pick[lane], sm.pick[lane] < 0 ? 0.f : sm.w[lane]);
 }
 
+// The selection may start beside the kernel before it in the stream (both
+// kernels wait for its results before they read logits).
+template <typename K>
+cudaError_t launch_after(K kern, unsigned grid, unsigned block, size_t smem, const RouteArgs& a,
+                         cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 template <typename T>
 cudaError_t select(const RouteArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)((a.rows + 3LL) / 4);
-  if (a.E <= 32) select_warp_kernel<1, T><<<grid, 128, 0, s>>>(a);
-  else if (a.E <= 64) select_warp_kernel<2, T><<<grid, 128, 0, s>>>(a);
-  else if (a.E <= 128) select_warp_kernel<4, T><<<grid, 128, 0, s>>>(a);
-  else if (a.E <= 256) select_warp_kernel<8, T><<<grid, 128, 0, s>>>(a);
-  else if (a.E <= 512) select_warp_kernel<16, T><<<grid, 128, 0, s>>>(a);
-  else if (a.E <= 1024) select_warp_kernel<32, T><<<grid, 128, 0, s>>>(a);
-  else {
-    static const cudaError_t e = cudaFuncSetAttribute(
-        select_cta_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 8);
-    if (e != cudaSuccess) return e;
-    select_cta_kernel<T><<<a.rows, kBigThreads, (size_t)a.E * 8, s>>>(a);
+  if (a.E <= 32) return launch_after(select_warp_kernel<1, T>, grid, 128, 0, a, s);
+  if (a.E <= 64) return launch_after(select_warp_kernel<2, T>, grid, 128, 0, a, s);
+  if (a.E <= 128) return launch_after(select_warp_kernel<4, T>, grid, 128, 0, a, s);
+  if (a.E <= 256) return launch_after(select_warp_kernel<8, T>, grid, 128, 0, a, s);
+  if (a.E <= 512) return launch_after(select_warp_kernel<16, T>, grid, 128, 0, a, s);
+  if (a.E <= 1024) return launch_after(select_warp_kernel<32, T>, grid, 128, 0, a, s);
+  static const cudaError_t e = cudaFuncSetAttribute(
+      select_cta_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 8);
+  if (e != cudaSuccess) return e;
+  return launch_after(select_cta_kernel<T>, (unsigned)a.rows, kBigThreads, (size_t)a.E * 8, a, s);
+}
+
+constexpr int kDotRows = 8, kDotWarps = 4;
+
+// z[b][e] for R rows: CTA e, its warps over pieces of 8 elements of K
+template <int R>
+__global__ void __launch_bounds__(32 * kDotWarps)
+dot_kernel(const __nv_bfloat16* __restrict__ x, long long x_stride,
+           const __nv_bfloat16* __restrict__ router, int rows, int hidden, int E,
+           float* __restrict__ z) {
+  __shared__ float red[kDotWarps][R];
+  tc::pdl_trigger();
+  const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint4* w = reinterpret_cast<const uint4*>(router + (size_t)e * hidden);
+  float acc[R] = {};
+#pragma unroll 2
+  for (int i = threadIdx.x; i < hidden / 8; i += 32 * kDotWarps) {
+    const uint4 wq = __ldg(w + i);
+    const uint32_t wv[4] = {wq.x, wq.y, wq.z, wq.w};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= rows) break;
+      const uint4 xq = __ldg(reinterpret_cast<const uint4*>(x + r * x_stride) + i);
+      const uint32_t xv[4] = {xq.x, xq.y, xq.z, xq.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[r] = fmaf(__uint_as_float(wv[j] << 16), __uint_as_float(xv[j] << 16), acc[r]);
+        acc[r] = fmaf(__uint_as_float(wv[j] & 0xffff0000u), __uint_as_float(xv[j] & 0xffff0000u), acc[r]);
+      }
+    }
   }
-  return cudaGetLastError();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float v = warp_sum(acc[r]);
+    if (lane == 0) red[warp][r] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < R && (int)threadIdx.x < rows) {
+    float v = 0.f;
+    for (int i = 0; i < kDotWarps; ++i) v += red[i][threadIdx.x];
+    z[(size_t)threadIdx.x * E + e] = v;
+  }
 }
 
 struct Bf16Rows {
@@ -324,7 +389,39 @@ cudaError_t launch_route_select(const RouteArgs& a, int dtype, cudaStream_t s) {
 
 cudaError_t launch_route_logits(const __nv_bfloat16* x, long long x_stride,
                                 const __nv_bfloat16* router, int rows, int hidden, int E, float* z,
-                                unsigned long long*, cudaStream_t s) {
+                                unsigned long long* status, cudaStream_t s) {
+  const bool whole = hidden % 8 == 0 && x_stride % 8 == 0 &&
+                     ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(router)) & 15) == 0;
+  if (whole && rows <= kDotRows) {
+    auto go = [&](auto kern) {
+      kern<<<E, 32 * kDotWarps, 0, s>>>(x, x_stride, router, rows, hidden, E, z);
+      return cudaGetLastError();
+    };
+    return rows == 1 ? go(dot_kernel<1>) : rows <= 4 ? go(dot_kernel<4>) : go(dot_kernel<kDotRows>);
+  }
+  if (whole) {
+    tc::DeviceInfo d;
+    const cudaError_t e = tc::device_info(&d);
+    if (e != cudaSuccess) return e;
+    tg::Problem p{};
+    p.p = x;
+    p.q = router;
+    p.p_stride = x_stride * 2;
+    p.q_stride = (long long)hidden * 2;
+    p.p_rows = rows;
+    p.q_rows = E;
+    p.k = hidden;
+    p.out = z;
+    p.out_stride = E;
+    p.f32 = true;
+    p.status = status;
+    const long long c64 = tg::intake<tg::kBf16, 64, 1>(rows, E, hidden, d.sms),
+                    c128 = tg::intake<tg::kBf16, 128, 1>(rows, E, hidden, d.sms),
+                    c256 = tg::intake<tg::kBf16, 256, 2>(rows, E, hidden, d.sms);
+    if (c256 <= c128 && c256 <= c64) return tg::launch<tg::kBf16, 256, 2, false>(p, d.sms, s);
+    if (c128 <= c64) return tg::launch<tg::kBf16, 128, 1, false>(p, d.sms, s);
+    return tg::launch<tg::kBf16, 64, 1, false>(p, d.sms, s);
+  }
   // rows in slices that keep the grid's y within 65,535
   for (long long r0 = 0; r0 < rows; r0 += 65535 * 64) {
     const int n = (int)(rows - r0 < 65535 * 64 ? rows - r0 : 65535 * 64);

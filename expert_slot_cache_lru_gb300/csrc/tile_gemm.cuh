@@ -66,7 +66,7 @@ struct Shape {
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static constexpr int kSmem = kStages * kStage + kScaleSmem + 1024;
   static_assert(kUsed <= 512 && kStage % 1024 == 0 && kStages >= kBufs, "tile shape");
-  static_assert(kStages * kStage >= 128 * NT * 4, "room for a partial tile");
+  static_assert(kStages * kStage >= 128 * (NT + 4) * 4, "room for a partial tile");
 };
 
 struct Args {
@@ -101,7 +101,7 @@ __device__ __forceinline__ void tile_at(const Args& a, int t, int& tp, int& tq) 
 }
 
 // 16 bytes of a row's scales in smaller pieces, zeros beyond the row
-__device__ __noinline__ void copy_ragged(uint32_t dst, const uint8_t* row, int off, int sb, int piece) {
+static __device__ __noinline__ void copy_ragged(uint32_t dst, const uint8_t* row, int off, int sb, int piece) {
   if (piece > 1) {
     for (int o = 0; o < 16; o += piece) {
       const bool in = off + o < sb;
@@ -229,6 +229,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   if (CG > 1) cluster_sync();  // the peer's barriers exist before anything arrives there
   fence_after();
   const uint32_t tmem = c.tmem;
+  if (KIND == kBf16) pdl_trigger();  // the router's selection
 
   if (warp == T::kTmaWarp) {
     int it = 0, s = 0;
@@ -439,10 +440,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         tmem_ld(acc + n0, v);
         tmem_wait_ld();
         const int nq = (int)(a.q_rows - q0 < W ? a.q_rows - q0 : W);
-        if (a.split > 1) {  // partial sums, [column][row], for the cluster's reduction
+        if (a.split > 1) {  // partial sums for the cluster's reduction
           float* sum = reinterpret_cast<float*>(stg);
+          if (SWAP) {  // [column][row]
 #pragma unroll
-          for (int i = 0; i < W; ++i) sum[(n0 + i) * 128 + pr] = __uint_as_float(v[i]);
+            for (int i = 0; i < W; ++i) sum[(n0 + i) * 128 + pr] = __uint_as_float(v[i]);
+          } else {  // [row][column], rows 4 floats apart in banks
+#pragma unroll
+            for (int i = 0; i < W; i += 4)
+              *reinterpret_cast<uint4*>(sum + pr * (NT + 4) + n0 + i) =
+                  make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
         } else if (SWAP) {
           if (p < a.p_rows) {
 #pragma unroll
@@ -493,20 +501,38 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     // one tile per cluster: this part's share of its results, summed over the parts
     int tp, tq;
     tile_at(a, tile0, tp, tq);
-    const long long left = a.q_rows - (long long)tq * NT;
-    const int cols = (int)(left < NT ? left : NT);
     const float g = global_scale(a);
     const uint32_t sums = sa(stg);
-    const int n = cols * 128;
-    for (int i = part * kThreads + threadIdx.x; i < n; i += a.split * kThreads) {
-      // SWAP: neighbouring threads take neighbouring rows (outputs of one token);
-      // else neighbouring columns
-      const int col = SWAP ? i >> 7 : i % cols, row = SWAP ? i & 127 : i / cols;
-      float v = 0.f;
-      for (int k = 0; k < a.split; ++k) v += ld_peer(sums + 4 * (col * 128 + row), k * CG + pair);
-      const long long p = ((long long)tp * CG + pair) * 128 + row, q = (long long)tq * NT + col;
-      if (p < a.p_rows && !c.abort_flag)
-        store_one(a, SWAP ? q * a.out_stride + p : p * a.out_stride + q, v * g);
+    // four neighbouring results per thread: rows (outputs of one token) with
+    // SWAP, else columns
+    constexpr int kLine = SWAP ? 128 : NT, kPitch = SWAP ? 128 : NT + 4, kLines = SWAP ? NT : 128;
+    const long long p0 = ((long long)tp * CG + pair) * 128, q0 = (long long)tq * NT;
+    const long long line0 = SWAP ? q0 : p0, at0 = SWAP ? p0 : q0;
+    const long long n_line = SWAP ? a.q_rows : a.p_rows, n_at = SWAP ? a.p_rows : a.q_rows;
+    const int lines = (int)(n_line - line0 < kLines ? n_line - line0 : kLines);
+#pragma unroll 2
+    for (int i = part * kThreads + threadIdx.x; i < lines * (kLine / 4); i += a.split * kThreads) {
+      const int line = i / (kLine / 4), at = i % (kLine / 4) * 4;
+      if (at0 + at >= n_at) continue;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < a.split; ++k) {
+        const float4 u = ld_peer4(sums + 4 * (line * kPitch + at), k * CG + pair);
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
+      if (c.abort_flag) continue;
+      const long long to = (line0 + line) * a.out_stride + at0 + at;
+      const float r[4] = {v.x * g, v.y * g, v.z * g, v.w * g};
+      if (a.wide && at0 + at + 4 <= n_at) {
+        if (a.f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(r[0], r[1], r[2], r[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
+              make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (at0 + at + j < n_at) store_one(a, to + j, r[j]);
+      }
     }
     cluster_sync();  // a peer may still be reading this CTA's sums
   }
@@ -536,6 +562,20 @@ inline int split_for(long long tiles, int nk, int cg, int sms) {
   int s = 1;
   while (s + 1 <= kMaxCluster / cg && s + 1 <= nk && tiles * cg * (s + 1) <= sms) ++s;
   return s;
+}
+
+// What a CTA takes in for its share of the product, in bytes: the measure the tile
+// of a product is chosen by (an SM's intake, about 52 bytes per cycle, bounds all
+// but the largest products), with a split's exchange of partial sums.
+template <Kind KIND, int NT, int CG>
+long long intake(long long p_rows, long long q_rows, int k, int sms) {
+  using T = Shape<KIND, NT, CG>;
+  const long long tiles = (p_rows + 128 * CG - 1) / (128 * CG) * ((q_rows + NT - 1) / NT);
+  const int slab = KIND == kBf16 ? 64 : 256, nk = (k + slab - 1) / slab;
+  const int split = split_for(tiles, (nk + T::kPer - 1) / T::kPer, CG, sms);
+  const long long per = sms / (CG * split), waves = (tiles + per - 1) / per;
+  const long long stage = T::kStage + (T::kBlocks ? T::kBlocks * 4 * (128 + NT) : 0);
+  return waves * ((nk + split - 1) / split * stage + (split > 1 ? 128 * NT * 6 : 0));
 }
 
 template <Kind KIND, int NT, int CG, bool SWAP>
