@@ -133,13 +133,11 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 ld_peer4(uint32_t saddr, int rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(peer_addr(saddr, rank))
+__device__ __forceinline__ void st_peer4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c,
+                                         uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
                : "memory");
-  return v;
 }
 // programmatic launch: let the next kernel of the stream start; wait for the
 // previous one's results
@@ -267,6 +265,9 @@ __device__ __forceinline__ void tmem_wait_st() {
 // bytes (1 or 2).  Outside the matrix a load reads zeros.
 cudaError_t make_map(CUtensorMap* map, const void* base, int elem, long long width,
                      long long rows, long long row_bytes, int box_rows);
+// The same for scale banks: tiles of 64 bytes, 64-byte swizzle.
+cudaError_t make_scale_map(CUtensorMap* map, const void* base, long long row_bytes, long long rows,
+                           int box_rows);
 
 struct DeviceInfo {
   int sms;

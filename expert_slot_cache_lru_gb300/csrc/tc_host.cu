@@ -27,20 +27,33 @@ Encode encoder() {
 
 }  // namespace
 
-cudaError_t make_map(CUtensorMap* map, const void* base, int elem, long long width,
-                     long long rows, long long row_bytes, int box_rows) {
+namespace {
+cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long width,
+                   long long rows, long long row_bytes, int box_width, int box_rows,
+                   CUtensorMapSwizzle swizzle) {
   const Encode f = encoder();
   if (!f) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows};
   const cuuint32_t step[2] = {1, 1};
-  const CUresult r =
-      f(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-        const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = f(map, type, 2, const_cast<void*>(base), dims, strides, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t make_map(CUtensorMap* map, const void* base, int elem, long long width,
+                     long long rows, long long row_bytes, int box_rows) {
+  return encode(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
+                width, rows, row_bytes, 128 / elem, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t make_scale_map(CUtensorMap* map, const void* base, long long row_bytes, long long rows,
+                           int box_rows) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, row_bytes, rows, row_bytes, 64, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 cudaError_t device_info(DeviceInfo* out) {

@@ -13,8 +13,9 @@
 //          left the MMAs of an 8,192 x 8,192 x 4,096 product waiting: 150 us).
 //          (tcgen05.cp would copy them too, but measured 52 cycles per 512 bytes in
 //          series with the MMAs.)
-//   16..19 block scales, global -> shared memory, 32 bytes of a row at a time: a request
-//          costs a cycle per row it touches, 460 per stage at 16 bytes;
+//   16..19 block scales, global -> shared memory, 64 bytes of a row at a time: TMA
+//          where the banks' rows are whole 16-byte pieces, else per-thread copies (which cost
+//          a cycle and more per row and 16 bytes: 550 a stage of 128 + 192 rows);
 //   then   one warp of TMA loads of the operands, one of MMAs (the first CTA's of a pair).
 // A pair halves what each SM takes in of Q, the bound of a lone CTA's 128 x 256
 // tile (48 KB a stage at about 52 bytes per cycle).
@@ -41,8 +42,10 @@ using namespace tc;
 enum Kind { kBf16, kNv, kMx };
 
 constexpr int kEpiWarps = 8, kScaleWarp = 8, kCopyWarp = 16;
-constexpr int kGroups = 3;  // groups of scales in shared memory, 32 bytes of each row
-constexpr int kMaxCluster = 8;
+constexpr int kGroups = 2;  // groups of scales in shared memory, 64 bytes of each row
+// CTAs of a cluster: eights do not all find room at once (128 CTAs in eights
+// started up to 6 us apart)
+constexpr int kMaxCluster = 4;
 
 template <Kind KIND, int NT, int CG>
 struct Shape {
@@ -51,18 +54,23 @@ struct Shape {
   static constexpr int kTmaWarp = kBlocks ? 20 : kEpiWarps, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kPer = KIND == kMx ? 2 : 1;            // stages in 16 bytes of a row's scales
+  static constexpr int kGroupStages = 4 * kPer;
   static constexpr int kQRows = (NT + 31) / 32 * 32;          // Q rows of scales in shared memory
   static constexpr int kQCols = NT < 128 ? 4 : NT / 32;       // Q columns of a scale block
   static constexpr int kScaleCols = kBlocks * (4 + kQCols);   // of tensor memory, per stage
   static constexpr int kStage = 128 * 128 + kQ * 128;
-  static constexpr int kChunk = (128 + kQRows) * 16;          // 16 bytes of every row
-  static constexpr int kScaleSmem = kBlocks ? kGroups * 2 * kChunk : 0;
+  static constexpr int kSlot = (128 + kQRows) * 64;           // a group of scales
+  static constexpr int kScaleSmem = kBlocks ? kGroups * kSlot : 0;
   static constexpr int kFit = (226 * 1024 - 1024 - 1024 - kScaleSmem) / kStage;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   // stages of scales in tensor memory
   static constexpr int kBufs = !kBlocks ? 1 : 2 * NT + 4 * kScaleCols <= 512 ? 4 : 3;
-  static constexpr int kAcc = 2 * NT + kBufs * kScaleCols <= 512 ? 2 : 1;  // accumulators
-  static constexpr int kUsed = kAcc * NT + kBufs * kScaleCols;
+  // Sums of a tile: the tensor cores add with truncation, an error that grows with the
+  // chain of additions, so bf16 tiles use the tensor memory for up to four parts of
+  // K, added up in the epilogue; 4-bit tiles (chains four times shorter) alternate two tiles.
+  static constexpr int kChains = kBlocks ? 1 : 512 / NT < 4 ? 512 / NT : 4;
+  static constexpr int kAcc = kBlocks && 2 * NT + kBufs * kScaleCols <= 512 ? 2 : 1;
+  static constexpr int kUsed = kAcc * kChains * NT + kBufs * kScaleCols;
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static constexpr int kSmem = kStages * kStage + kScaleSmem + 1024;
   static_assert(kUsed <= 512 && kStage % 1024 == 0 && kStages >= kBufs, "tile shape");
@@ -182,10 +190,25 @@ __device__ __forceinline__ float global_scale(const Args& a) {
   return (a.g0 ? *a.g0 : 1.f) * (a.g1 ? *a.g1 : 1.f);
 }
 
+// W columns of the warp's lanes, the sums of n_chains parts of K added up
+template <int NT, int W>
+__device__ __forceinline__ void read_sums(uint32_t at, int n_chains, uint32_t (&v)[W]) {
+  tmem_ld(at, v);
+  tmem_wait_ld();
+  for (int k = 1; k < n_chains; ++k) {
+    uint32_t u[W];
+    tmem_ld(at + k * NT, u);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+  }
+}
+
 // SWAP: out[q][p] (P the weights, Q the tokens); else out[p][q].
 template <Kind KIND, int NT, int CG, bool SWAP>
 __global__ void __launch_bounds__(Shape<KIND, NT, CG>::kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
+            const __grid_constant__ CUtensorMap psmap, const __grid_constant__ CUtensorMap qsmap,
             const Args a) {
   using T = Shape<KIND, NT, CG>;
   constexpr int ST = T::kStages, kThreads = T::kThreads;
@@ -194,6 +217,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   uint8_t* sstg = stg + (size_t)ST * T::kStage;
   __shared__ Ctl<ST> c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int W = NT < 64 ? 16 : 32;  // columns the epilogue reads at a time
   // cluster: `split` parts of K, each CG CTAs; a lone CTA's cluster is itself
   const int crank = CG == 1 && a.split == 1 ? 0 : (int)cluster_rank();
   const int pair = crank % CG, first = crank - pair, part = crank / CG;
@@ -203,6 +227,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   const int k_lo = nkp * part / a.split * T::kPer,
             k_hi = min(a.nk, nkp * (part + 1) / a.split * T::kPer), n_k = k_hi - k_lo;
   const int n_tiles = a.tiles_p * a.tiles_q, tile0 = blockIdx.x / team, step = gridDim.x / team;
+  const int n_chains = min(T::kChains, n_k);
   const uint16_t mask = (uint16_t)(((1 << CG) - 1) << first);
 
   if (threadIdx.x == 0) {
@@ -212,7 +237,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     }
     for (int i = 0; i < 4; ++i) mbar_init(&c.scaled[i], 4 * CG);
     for (int i = 0; i < kGroups; ++i) {
-      mbar_init(&c.rows_full[i], 128);
+      mbar_init(&c.rows_full[i], a.piece == 16 ? 1 : 128);
       mbar_init(&c.rows_empty[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
@@ -274,10 +299,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         if (u >= T::kAcc &&
             !warp_wait(&c.acc_empty[b], (u / T::kAcc - 1) & 1, &c.abort_flag, a.status))
           break;
-        const uint32_t d = tmem + b * NT;
+        uint32_t d = tmem + b * NT;
+        int chain = 0, first_of = 0;  // the part of K being summed, its first stage
         for (int i = 0; i < n_k; ++i) {
-          if ((T::kBlocks && !warp_wait(&c.scaled[sbuf], scaled_par, &c.abort_flag, a.status)) ||
-              !warp_wait(&c.full[s], full_par, &c.abort_flag, a.status)) {
+          if (T::kChains > 1 && i == n_k * (chain + 1) / n_chains) {
+            ++chain;
+            first_of = i;
+            d += NT;
+          }
+          // both at once; one after the other only if one is not there yet
+          const bool there = mbar_test(&c.full[s], full_par) &
+                             (!T::kBlocks || mbar_test(&c.scaled[sbuf], scaled_par));
+          if (!__all_sync(0xffffffffu, there) &&
+              ((T::kBlocks && !warp_wait(&c.scaled[sbuf], scaled_par, &c.abort_flag, a.status)) ||
+               !warp_wait(&c.full[s], full_par, &c.abort_flag, a.status))) {
             ok = false;
             break;
           }
@@ -290,7 +325,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
             for (int j = 0; j < 4; ++j) {  // 32 bytes of every row each
               const int w = KIND == kMx ? j / 2 : j, id = KIND == kMx ? 2 * (j & 1) : 0;
               mma<KIND, CG>(d, p0 + 2 * j, q0 + 2 * j, idesc<KIND>(128 * CG, NT, id), cp + 4 * w,
-                            cq + T::kQCols * w, j > 0 || i > 0);
+                            cq + T::kQCols * w, j > 0 || i > first_of);
             }
             mma_commit<CG>(&c.empty[s], mask);
           }
@@ -309,50 +344,52 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     __syncwarp();
   } else if (warp >= kCopyWarp) {
     if constexpr (T::kBlocks > 0) {
-      // two threads per row: 16 bytes each of the 32 that a group holds
-      const int tid = threadIdx.x - 32 * kCopyWarp, half = tid & 1, r0 = tid >> 1;
-      const uint32_t base = sa(sstg) + half * T::kChunk;
-      constexpr int PR = 2, QR = (NT + 63) / 64;  // rows per thread, 64 apart
-      int it = 0, slot = 0;
-      bool ok = true;
+      const int n_warps = a.piece == 16 ? 1 : 4;  // one lane of TMA, or all 128 threads
+      unsigned group = 0;
+      bool ok = warp - kCopyWarp < n_warps;
       for (int t = tile0; t < n_tiles && ok; t += step) {
         int tp, tq;
         tile_at(a, t, tp, tq);
-        const uint8_t *pr[PR], *qr[QR];
-#pragma unroll
-        for (int i = 0; i < PR; ++i) {
-          const long long p = ((long long)tp * CG + pair) * 128 + r0 + 64 * i;
-          pr[i] = p < a.p_rows ? a.ps + p * a.sb : nullptr;
-        }
-#pragma unroll
-        for (int i = 0; i < QR; ++i) {
-          const long long q = (long long)tq * NT + r0 + 64 * i;
-          qr[i] = q < a.q_rows ? a.qs + q * a.sb : nullptr;
-        }
+        const int p_row = (tp * CG + pair) * 128, q_row = tq * NT;
         // groups start at the first stage of the tile's part of K
-        for (int ks = k_lo; ks < k_hi; ks += 2 * T::kPer, ++it) {
-          if (it >= kGroups &&
-              !warp_wait(&c.rows_empty[slot], (it / kGroups - 1) & 1, &c.abort_flag, a.status)) {
+        for (int ks = k_lo; ks < k_hi; ks += T::kGroupStages, ++group) {
+          const unsigned slot = group % kGroups;
+          if (group >= kGroups && !warp_wait(&c.rows_empty[slot], (group / kGroups - 1) & 1,
+                                             &c.abort_flag, a.status)) {
             ok = false;
             break;
           }
-          const int off = ks * (16 / T::kPer) + 16 * half;
-          const uint32_t dst = base + slot * 2 * T::kChunk + r0 * 16;
-#pragma unroll
-          for (int i = 0; i < PR; ++i) copy_scales(dst + 64 * 16 * i, pr[i], off, a);
-#pragma unroll
-          for (int i = 0; i < QR; ++i)
-            if (r0 + 64 * i < NT) copy_scales(dst + (128 + 64 * i) * 16, qr[i], off, a);
-          if (a.piece > 1) {
-            cp_async_arrive(&c.rows_full[slot]);
-          } else {  // rows without a tile and ragged rows alike
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            mbar_arrive(&c.rows_full[slot]);
+          const int off = ks * (16 / T::kPer);
+          uint8_t* dst = sstg + slot * T::kSlot;
+          if (a.piece == 16) {
+            if (elect_one()) {
+              mbar_expect(&c.rows_full[slot], (128 + NT) * 64);
+              tma_load<1>(dst, &psmap, off, p_row, sa(&c.rows_full[slot]));
+              tma_load<1>(dst + 128 * 64, &qsmap, off, q_row, sa(&c.rows_full[slot]));
+            }
+            __syncwarp();
+          } else {
+            const int tid = threadIdx.x - 32 * kCopyWarp, chunk = tid & 3;
+            for (int r = tid >> 2; r < 128 + NT; r += 32) {
+              const long long row = r < 128 ? (long long)p_row + r : (long long)q_row + r - 128;
+              const bool in = row < (r < 128 ? a.p_rows : a.q_rows);
+              const uint8_t* src = in ? (r < 128 ? a.ps : a.qs) + row * a.sb : nullptr;
+              // the TMA's 64-byte swizzle
+              copy_scales(sa(dst) + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4), src, off + 16 * chunk, a);
+            }
+            if (a.piece > 1) {
+              cp_async_arrive(&c.rows_full[slot]);
+            } else {  // plain stores beside the copies of rows outside the matrix
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              mbar_arrive(&c.rows_full[slot]);
+            }
           }
-          slot = slot + 1 == kGroups ? 0 : slot + 1;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok && warp == kCopyWarp && a.piece == 16)  // copies in flight land before the CTA ends
+        for (unsigned i = group > kGroups ? group - kGroups : 0; i < group; ++i)
+          drain_bar(&c.rows_full[i % kGroups], (i / kGroups) & 1);
     }
     __syncwarp();
   } else if (warp >= kScaleWarp) {
@@ -362,8 +399,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
       unsigned it = 0, group = 0;
       bool ok = true;
       for (int t = tile0; t < n_tiles && ok; t += step) {
-        for (int ks = k_lo; ks < k_hi && ok; ks += 2 * T::kPer, ++group) {
-          const unsigned slot = group % kGroups, m = min(2 * T::kPer, k_hi - ks);
+        for (int ks = k_lo; ks < k_hi && ok; ks += T::kGroupStages, ++group) {
+          const unsigned slot = group % kGroups, m = min(T::kGroupStages, k_hi - ks);
           if (!warp_wait(&c.rows_full[slot], (group / kGroups) & 1, &c.abort_flag, a.status)) {
             ok = false;
             break;
@@ -372,7 +409,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
           for (unsigned x = (it ^ mine) & 1; x < m; x += 2) {
             const unsigned n = it + x, buf = n % T::kBufs;
             // lane's rows, lane + 32 q: word j of row q belongs in column q of block j
-            const uint8_t* sp = sstg + (slot * 2 + x / T::kPer) * T::kChunk + lane * 16 +
+            const uint8_t* sp = sstg + slot * T::kSlot + lane * 64 +
+                                (((x / T::kPer) ^ ((lane >> 1) & 3)) << 4) +
                                 (KIND == kMx ? 8 * (x & 1) : 0);
             uint32_t w[T::kScaleCols];
 #pragma unroll
@@ -380,10 +418,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
               uint32_t v[4] = {0, 0, 0, 0};
               if (q < 4 || 32 * (q - 4) < T::kQRows) {
                 if constexpr (KIND == kNv) {
-                  const uint4 u = *reinterpret_cast<const uint4*>(sp + 512 * q);
+                  const uint4 u = *reinterpret_cast<const uint4*>(sp + 2048 * q);
                   v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
                 } else {
-                  const uint2 u = *reinterpret_cast<const uint2*>(sp + 512 * q);
+                  const uint2 u = *reinterpret_cast<const uint2*>(sp + 2048 * q);
                   v[0] = u.x, v[1] = u.y;
                 }
               }
@@ -418,7 +456,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     __syncwarp();
   } else {
     const float g = global_scale(a);
-    constexpr int W = NT < 64 ? 16 : 32;  // columns read at a time
     int u = 0;
     for (int t = tile0; t < n_tiles; t += step, ++u) {
       const int b = u % T::kAcc;
@@ -427,7 +464,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
       if (threadIdx.x == 0)
         c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], (u / T::kAcc) & 1, &c.abort_flag, a.status);
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (!c.epi_ok[u & 1]) break;
+      if (!c.epi_ok[u & 1] || a.split > 1) break;  // a split's sums are exchanged below
       fence_after();
       const int pr = 32 * (warp & 3) + lane;
       const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + b * NT;
@@ -437,21 +474,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         const long long q0 = (long long)tq * NT + n0;
         if (q0 >= a.q_rows) break;
         uint32_t v[W];
-        tmem_ld(acc + n0, v);
-        tmem_wait_ld();
+        read_sums<NT>(acc + n0, n_chains, v);
         const int nq = (int)(a.q_rows - q0 < W ? a.q_rows - q0 : W);
-        if (a.split > 1) {  // partial sums for the cluster's reduction
-          float* sum = reinterpret_cast<float*>(stg);
-          if (SWAP) {  // [column][row]
-#pragma unroll
-            for (int i = 0; i < W; ++i) sum[(n0 + i) * 128 + pr] = __uint_as_float(v[i]);
-          } else {  // [row][column], rows 4 floats apart in banks
-#pragma unroll
-            for (int i = 0; i < W; i += 4)
-              *reinterpret_cast<uint4*>(sum + pr * (NT + 4) + n0 + i) =
-                  make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          }
-        } else if (SWAP) {
+        if (SWAP) {
           if (p < a.p_rows) {
 #pragma unroll
             for (int i = 0; i < W; ++i)
@@ -498,43 +523,64 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   }
   if (CG > 1 || a.split > 1) cluster_sync();
   if (a.split > 1) {
-    // one tile per cluster: this part's share of its results, summed over the parts
+    // One tile per cluster, its operands done with everywhere.  Every part sends
+    // its sums of a row to the part that adds the row up: [part][row][column].
+    constexpr int kPitch = NT + 4;  // rows 4 banks apart
+    const int rows_per = 128 / a.split;
+    if (warp < kEpiWarps && !c.abort_flag) {
+      fence_after();
+      const int pr = 32 * (warp & 3) + lane, own = pr / rows_per;
+      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      const uint32_t to = peer_addr(sa(stg), own * CG + pair) +
+                          4 * ((part * rows_per + pr - own * rows_per) * kPitch);
+#pragma unroll 1
+      for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
+        uint32_t v[W];
+        read_sums<NT>(acc + n0, n_chains, v);
+#pragma unroll
+        for (int i = 0; i < W; i += 4) st_peer4(to + 4 * (n0 + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+      fence_before();
+    }
+    cluster_sync();
     int tp, tq;
     tile_at(a, tile0, tp, tq);
     const float g = global_scale(a);
-    const uint32_t sums = sa(stg);
-    // four neighbouring results per thread: rows (outputs of one token) with
-    // SWAP, else columns
-    constexpr int kLine = SWAP ? 128 : NT, kPitch = SWAP ? 128 : NT + 4, kLines = SWAP ? NT : 128;
-    const long long p0 = ((long long)tp * CG + pair) * 128, q0 = (long long)tq * NT;
-    const long long line0 = SWAP ? q0 : p0, at0 = SWAP ? p0 : q0;
-    const long long n_line = SWAP ? a.q_rows : a.p_rows, n_at = SWAP ? a.p_rows : a.q_rows;
-    const int lines = (int)(n_line - line0 < kLines ? n_line - line0 : kLines);
-#pragma unroll 2
-    for (int i = part * kThreads + threadIdx.x; i < lines * (kLine / 4); i += a.split * kThreads) {
-      const int line = i / (kLine / 4), at = i % (kLine / 4) * 4;
-      if (at0 + at >= n_at) continue;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < a.split; ++k) {
-        const float4 u = ld_peer4(sums + 4 * (line * kPitch + at), k * CG + pair);
-        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    const float* sums = reinterpret_cast<const float*>(stg);
+    const long long p0 = ((long long)tp * CG + pair) * 128 + part * rows_per, q0 = (long long)tq * NT;
+    const int rows = (int)max(0LL, min((long long)rows_per, a.p_rows - p0));
+    const int cols = (int)min((long long)NT, a.q_rows - q0);
+    if (SWAP) {  // neighbouring threads take neighbouring rows: outputs of one token
+      for (int i = threadIdx.x; i < cols * rows_per; i += kThreads) {
+        const int row = i % rows_per, col = i / rows_per;
+        float v = 0.f;
+        for (int k = 0; k < a.split; ++k) v += sums[(k * rows_per + row) * kPitch + col];
+        if (row < rows && !c.abort_flag) store_one(a, (q0 + col) * a.out_stride + p0 + row, v * g);
       }
-      if (c.abort_flag) continue;
-      const long long to = (line0 + line) * a.out_stride + at0 + at;
-      const float r[4] = {v.x * g, v.y * g, v.z * g, v.w * g};
-      if (a.wide && at0 + at + 4 <= n_at) {
-        if (a.f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(r[0], r[1], r[2], r[3]);
-        else
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
-              make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
-      } else {
+    } else {  // four neighbouring columns per thread
+      for (int i = threadIdx.x; i < rows * (NT / 4); i += kThreads) {
+        const int row = i / (NT / 4), col = i % (NT / 4) * 4;
+        if (col >= cols || c.abort_flag) continue;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < a.split; ++k) {
+          const float4 x = *reinterpret_cast<const float4*>(sums + (k * rows_per + row) * kPitch + col);
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        const long long to = (p0 + row) * a.out_stride + q0 + col;
+        const float r[4] = {v.x * g, v.y * g, v.z * g, v.w * g};
+        if (a.wide && col + 4 <= cols) {
+          if (a.f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(r[0], r[1], r[2], r[3]);
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
+                make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (at0 + at + j < n_at) store_one(a, to + j, r[j]);
+          for (int j = 0; j < 4; ++j)
+            if (col + j < cols) store_one(a, to + j, r[j]);
+        }
       }
     }
-    cluster_sync();  // a peer may still be reading this CTA's sums
   }
   fence_before();
   __syncthreads();
@@ -560,7 +606,7 @@ struct Problem {
 // Parts of K that give every SM a CTA where tiles are few.
 inline int split_for(long long tiles, int nk, int cg, int sms) {
   int s = 1;
-  while (s + 1 <= kMaxCluster / cg && s + 1 <= nk && tiles * cg * (s + 1) <= sms) ++s;
+  while (2 * s <= kMaxCluster / cg && 2 * s <= nk && tiles * cg * 2 * s <= sms) s *= 2;
   return s;
 }
 
@@ -607,11 +653,15 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   a.split = split_for(tiles, (a.nk + T::kPer - 1) / T::kPer, CG, sms);
   const int team = CG * a.split;
-  CUtensorMap pm, qm;
+  CUtensorMap pm, qm, psm{}, qsm{};
   const int elem = KIND == kBf16 ? 2 : 1;
   const long long width = KIND == kBf16 ? l.k : l.k / 2;
   cudaError_t e = make_map(&pm, l.p, elem, width, l.p_rows, l.p_stride, 128);
   if (e == cudaSuccess) e = make_map(&qm, l.q, elem, width, l.q_rows, l.q_stride, T::kQ);
+  if (T::kBlocks && a.piece == 16) {
+    if (e == cudaSuccess) e = make_scale_map(&psm, l.ps, a.sb, l.p_rows, 128);
+    if (e == cudaSuccess) e = make_scale_map(&qsm, l.qs, a.sb, l.q_rows, NT);
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const long long teams = tiles < sms / team ? tiles : sms / team;
@@ -624,7 +674,7 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   attr[0].val.clusterDim = {(unsigned)team, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, pm, qm, a);
+  return cudaLaunchKernelEx(&cfg, kern, pm, qm, psm, qsm, a);
 }
 
 }  // namespace tg
