@@ -1,12 +1,13 @@
 // route.cu -- the router: logits, scores, grouped choice and weights
 // (formulas in moe_cache.h).
 //
-// Selection: up to 1,024 experts one warp owns a row, lane l the EL consecutive
-// experts from l * EL (EL = 1 .. 32, a power of two), so that a group of experts
-// is a run of lanes.  Choices are compared as unsigned integers in the order of
+// Selection: one warp owns a row.  Each of the G groups takes 32 / G lanes, and
+// a lane every (32 / G)-th expert of its group, up to 32 of them in registers: loads are
+// coalesced, and the groups' scores are one reduction over 32 / G lanes for all
+// groups at once.  Choices are compared as unsigned integers in the order of
 // the floats (0 = masked), which makes a pick two warp reductions: the largest
-// key, then the lowest id among its holders.  More experts take one CTA per row
-// with the keys in shared memory.
+// key, then the lowest id among its holders.  Group counts that do not divide 32 and more
+// than 32 experts per lane take one CTA per row with the keys in shared memory.
 //
 // Logits: up to kDotRows rows are dot products, one CTA per expert (its router row
 // read once for all rows); more rows are a product on the tensor cores (tile_gemm.cuh),
@@ -70,101 +71,100 @@ template <int EL, typename T>
 __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a) {
   const long long b = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (b >= a.rows) return;
-  const int lane = threadIdx.x & 31, e0 = lane * EL;
+  const int lane = threadIdx.x & 31;
+  // lane's experts: first + j * lanes, below end
+  const int lanes = 32 / a.groups, gs = a.E / a.groups, group = lane / lanes;
+  const int first = group * gs + lane % lanes, end = (group + 1) * gs;
   const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   tc::pdl_wait();
-  float z[EL], s[EL];
+  float s[EL];
   uint32_t key[EL];
   float mx = -INFINITY;
 #pragma unroll
   for (int j = 0; j < EL; ++j) {
-    z[j] = e0 + j < a.E ? load_f(zr + e0 + j) : -INFINITY;
-    mx = fmaxf(mx, z[j]);  // fmaxf drops NaN
+    s[j] = first + j * lanes < end ? load_f(zr + first + j * lanes) : -INFINITY;
+    mx = fmaxf(mx, s[j]);  // fmaxf drops NaN
   }
   if (softmax) mx = warp_max(mx);
   float sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < EL; ++j) sum += s[j] = raw_score(z[j], softmax, mx);
+  for (int j = 0; j < EL; ++j) {
+    const float z = s[j];
+    key[j] = choice_key(z);  // without a bias the logits rank
+    sum += s[j] = raw_score(z, softmax, mx);
+  }
   if (softmax) {
     sum = warp_sum(sum);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int j = 0; j < EL; ++j) s[j] = sum > 0.f ? s[j] / sum : 0.f;
+    for (int j = 0; j < EL; ++j) s[j] *= inv;
   }
-#pragma unroll
-  for (int j = 0; j < EL; ++j) {
-    const bool in = z[j] > -INFINITY;
-    const float c = a.bias ? (in ? s[j] + a.bias[e0 + j] : -INFINITY) : z[j];
-    key[j] = choice_key(c);
-  }
-  if (a.groups > 1) {
-    const int gs = a.E / a.groups;
-    // lane g keeps the scores of groups g and g + 32
-    uint32_t gk[2] = {0u, 0u};
-    for (int g = 0; g < a.groups; ++g) {
-      uint32_t k1 = 0u, k2 = 0u;  // two largest choices
-      float s1 = 0.f, s2 = 0.f;   // two largest scores
-#pragma unroll
-      for (int j = 0; j < EL; ++j) {
-        const int e = e0 + j;
-        if (e < a.E && e / gs == g && key[j]) {
-          const uint32_t kk = key[j];
-          k2 = max(k2, min(k1, kk));
-          k1 = max(k1, kk);
-          s2 = fmaxf(s2, fminf(s1, s[j]));
-          s1 = fmaxf(s1, s[j]);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint32_t q1 = __shfl_xor_sync(kAll, k1, o), q2 = __shfl_xor_sync(kAll, k2, o);
-        const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
-        k2 = max(min(k1, q1), max(k2, q2));
-        k1 = max(k1, q1);
-        s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
-        s1 = fmaxf(s1, t1);
-      }
-      uint32_t sc = k1;
-      if (a.group_top == 2 && k1)
-        sc = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
-      if ((g & 31) == lane) gk[g >> 5] = sc;
-    }
-    unsigned long long keep = 0;
-    for (int t = 0; t < a.topk_groups; ++t) {
-      const uint32_t best = __reduce_max_sync(kAll, max(gk[0], gk[1]));
-      if (!best) break;
-      const unsigned at = gk[0] == best ? lane : gk[1] == best ? lane + 32 : 64;
-      const unsigned g = __reduce_min_sync(kAll, at);
-      keep |= 1ull << g;
-      if ((g & 31) == (unsigned)lane) gk[g >> 5] = 0u;
-    }
+  if (a.bias) {
 #pragma unroll
     for (int j = 0; j < EL; ++j)
-      if (e0 + j < a.E && !((keep >> ((e0 + j) / gs)) & 1)) key[j] = 0u;
+      if (key[j]) key[j] = choice_key(s[j] + __ldg(a.bias + first + j * lanes));
+  }
+  if (a.groups > 1) {
+    uint32_t k1 = 0u, k2 = 0u;  // the group's two largest choices
+    float s1 = 0.f, s2 = 0.f;   // and scores
+#pragma unroll
+    for (int j = 0; j < EL; ++j) {
+      const float v = key[j] ? s[j] : 0.f;
+      k2 = max(k2, min(k1, key[j]));
+      k1 = max(k1, key[j]);
+      s2 = fmaxf(s2, fminf(s1, v));
+      s1 = fmaxf(s1, v);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      const uint32_t q1 = __shfl_xor_sync(kAll, k1, o), q2 = __shfl_xor_sync(kAll, k2, o);
+      const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
+      k2 = max(min(k1, q1), max(k2, q2));
+      k1 = max(k1, q1);
+      s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
+      s1 = fmaxf(s1, t1);
+    }
+    uint32_t mine = k1;
+    if (a.group_top == 2 && k1)
+      mine = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
+    int rank = 0;  // groups ahead of this one
+    for (int g = 0; g < a.groups; ++g) {
+      const uint32_t other = __shfl_sync(kAll, mine, g * lanes);
+      rank += other > mine || (other == mine && g < group);
+    }
+    if (rank >= a.topk_groups || !mine) {
+#pragma unroll
+      for (int j = 0; j < EL; ++j) key[j] = 0u;
+    }
   }
   int my_id = -1;
   float my_w = 0.f;
   for (int r = 0; r < a.k; ++r) {
-    uint32_t top = 0u;
+    uint32_t top = key[0];
 #pragma unroll
-    for (int j = 0; j < EL; ++j) top = max(top, key[j]);
+    for (int j = 1; j < EL; ++j) top = max(top, key[j]);
     const uint32_t best = __reduce_max_sync(kAll, top);
     if (!best) break;
-    unsigned at = 0xffffffffu;
-#pragma unroll
-    for (int j = EL - 1; j >= 0; --j)
-      if (key[j] == best) at = e0 + j;
-    const unsigned id = __reduce_min_sync(kAll, at);
+    // the lane's lowest id that holds the best key, its score; ids grow with j
+    int at = 0x7fffffff;
     float w = 0.f;
+    if (top == best) {
 #pragma unroll
-    for (int j = 0; j < EL; ++j)
-      if ((unsigned)(e0 + j) == id) {
-        w = s[j];
-        key[j] = 0u;
-      }
-    w = __shfl_sync(kAll, w, id / EL);
+      for (int j = EL - 1; j >= 0; --j)
+        if (key[j] == best) {
+          at = first + j * lanes;
+          w = s[j];
+        }
+    }
+    const int id = __reduce_min_sync(kAll, at);
+    if (at == id) {
+#pragma unroll
+      for (int j = 0; j < EL; ++j)
+        if (first + j * lanes == id) key[j] = 0u;
+    }
+    w = __shfl_sync(kAll, w, __ffs(__ballot_sync(kAll, at == id)) - 1);
     if (lane == r) {
-      my_id = (int)id;
+      my_id = id;
       my_w = w;
     }
   }
@@ -183,7 +183,7 @@ struct BigSmem {
   float w[32];
 };
 
-// more than 1,024 experts: one CTA per row, keys and scores in shared memory
+// one CTA per row, keys and scores in shared memory
 template <typename T>
 __global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
   extern __shared__ uint32_t dyn[];
@@ -316,12 +316,14 @@ cudaError_t launch_after(K kern, unsigned grid, unsigned block, size_t smem, con
 template <typename T>
 cudaError_t select(const RouteArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)((a.rows + 3LL) / 4);
-  if (a.E <= 32) return launch_after(select_warp_kernel<1, T>, grid, 128, 0, a, s);
-  if (a.E <= 64) return launch_after(select_warp_kernel<2, T>, grid, 128, 0, a, s);
-  if (a.E <= 128) return launch_after(select_warp_kernel<4, T>, grid, 128, 0, a, s);
-  if (a.E <= 256) return launch_after(select_warp_kernel<8, T>, grid, 128, 0, a, s);
-  if (a.E <= 512) return launch_after(select_warp_kernel<16, T>, grid, 128, 0, a, s);
-  if (a.E <= 1024) return launch_after(select_warp_kernel<32, T>, grid, 128, 0, a, s);
+  const int lanes = 32 / a.groups;  // per group
+  const int per = 32 % a.groups ? 33 : (a.E / a.groups + lanes - 1) / lanes;
+  if (per <= 1) return launch_after(select_warp_kernel<1, T>, grid, 128, 0, a, s);
+  if (per <= 2) return launch_after(select_warp_kernel<2, T>, grid, 128, 0, a, s);
+  if (per <= 4) return launch_after(select_warp_kernel<4, T>, grid, 128, 0, a, s);
+  if (per <= 8) return launch_after(select_warp_kernel<8, T>, grid, 128, 0, a, s);
+  if (per <= 16) return launch_after(select_warp_kernel<16, T>, grid, 128, 0, a, s);
+  if (per <= 32) return launch_after(select_warp_kernel<32, T>, grid, 128, 0, a, s);
   static const cudaError_t e = cudaFuncSetAttribute(
       select_cta_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 8);
   if (e != cudaSuccess) return e;

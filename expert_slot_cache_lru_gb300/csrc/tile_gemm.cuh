@@ -74,7 +74,7 @@ struct Shape {
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static constexpr int kSmem = kStages * kStage + kScaleSmem + 1024;
   static_assert(kUsed <= 512 && kStage % 1024 == 0 && kStages >= kBufs, "tile shape");
-  static_assert(kStages * kStage >= 128 * (NT + 4) * 4, "room for a partial tile");
+  static_assert(kStages * kStage >= 128 * (NT + 4) * 4 * (CG == 1 ? 7 : 6) / 4, "room for a split's sums");
 };
 
 struct Args {
@@ -95,7 +95,7 @@ struct Args {
 template <int ST>
 struct Ctl {
   uint64_t full[ST], empty[ST], scaled[4], rows_full[kGroups], rows_empty[kGroups];
-  uint64_t acc_full[2], acc_empty[2], drain;
+  uint64_t acc_full[2], acc_empty[2], drain, sums;
   uint32_t tmem;
   int abort_flag, epi_ok[2];  // epi_ok: the epilogue's wait, by tile parity
 };
@@ -245,6 +245,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
       mbar_init(&c.acc_empty[i], kEpiWarps * CG);
     }
     mbar_init(&c.drain, 1);
+    mbar_init(&c.sums, 1);
     c.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -523,30 +524,50 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   }
   if (CG > 1 || a.split > 1) cluster_sync();
   if (a.split > 1) {
-    // One tile per cluster, its operands done with everywhere.  Every part sends
-    // its sums of a row to the part that adds the row up: [part][row][column].
+    // One tile per cluster, its operands done with everywhere.  Every part lays its
+    // sums out in rows and copies each peer the rows that the peer adds up; stores
+    // to the peers one by one took 3,000 cycles of a 128 x 128 tile.
     constexpr int kPitch = NT + 4;  // rows 4 banks apart
-    const int rows_per = 128 / a.split;
-    if (warp < kEpiWarps && !c.abort_flag) {
-      fence_after();
-      const int pr = 32 * (warp & 3) + lane, own = pr / rows_per;
-      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-      const uint32_t to = peer_addr(sa(stg), own * CG + pair) +
-                          4 * ((part * rows_per + pr - own * rows_per) * kPitch);
+    const int rows_per = 128 / a.split, bytes = rows_per * kPitch * 4;
+    float* own = reinterpret_cast<float*>(stg);  // [128][kPitch], then [split - 1][rows_per][kPitch]
+    float* in = own + 128 * kPitch;
+    if (warp < kEpiWarps) {
+      if (!c.abort_flag) {
+        fence_after();
+        const int pr = 32 * (warp & 3) + lane;
+        const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
-      for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
-        uint32_t v[W];
-        read_sums<NT>(acc + n0, n_chains, v);
+        for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
+          uint32_t v[W];
+          read_sums<NT>(acc + n0, n_chains, v);
 #pragma unroll
-        for (int i = 0; i < W; i += 4) st_peer4(to + 4 * (n0 + i), v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int i = 0; i < W; i += 4)
+            *reinterpret_cast<uint4*>(own + pr * kPitch + n0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+        fence_before();
       }
-      fence_before();
+      fence_async_smem();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (warp == 0 && elect_one()) {
+        mbar_expect(&c.sums, (a.split - 1) * bytes);
+        for (int k = 0; k < a.split; ++k) {  // peer k keeps what it gets from part p at p, without itself
+          if (k == part) continue;
+          const int rank = k * CG + pair, at = part < k ? part : part - 1;
+          copy_to_peer(peer_addr(sa(in + at * rows_per * kPitch), rank), own + k * rows_per * kPitch, bytes,
+                       peer_addr(sa(&c.sums), rank));
+        }
+      }
     }
-    cluster_sync();
+    wait_bar(&c.sums, 0, &c.abort_flag, a.status);
+    __syncthreads();
     int tp, tq;
     tile_at(a, tile0, tp, tq);
     const float g = global_scale(a);
-    const float* sums = reinterpret_cast<const float*>(stg);
+    // row r of part k's sums
+    auto sums = [&](int k, int r) {
+      return k == part ? own + (part * rows_per + r) * kPitch
+                       : in + ((k < part ? k : k - 1) * rows_per + r) * kPitch;
+    };
     const long long p0 = ((long long)tp * CG + pair) * 128 + part * rows_per, q0 = (long long)tq * NT;
     const int rows = (int)max(0LL, min((long long)rows_per, a.p_rows - p0));
     const int cols = (int)min((long long)NT, a.q_rows - q0);
@@ -554,7 +575,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
       for (int i = threadIdx.x; i < cols * rows_per; i += kThreads) {
         const int row = i % rows_per, col = i / rows_per;
         float v = 0.f;
-        for (int k = 0; k < a.split; ++k) v += sums[(k * rows_per + row) * kPitch + col];
+        for (int k = 0; k < a.split; ++k) v += sums(k, row)[col];
         if (row < rows && !c.abort_flag) store_one(a, (q0 + col) * a.out_stride + p0 + row, v * g);
       }
     } else {  // four neighbouring columns per thread
@@ -563,7 +584,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         if (col >= cols || c.abort_flag) continue;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < a.split; ++k) {
-          const float4 x = *reinterpret_cast<const float4*>(sums + (k * rows_per + row) * kPitch + col);
+          const float4 x = *reinterpret_cast<const float4*>(sums(k, row) + col);
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
         const long long to = (p0 + row) * a.out_stride + q0 + col;
@@ -581,6 +602,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         }
       }
     }
+    cluster_sync();  // this CTA's copies have left its shared memory
   }
   fence_before();
   __syncthreads();
