@@ -10,7 +10,6 @@ There is no fallback: if the shared library is missing this import fails.
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -155,30 +154,42 @@ def _check(fn: str, rc: int) -> None:
 
 def _ptr(t) -> int | None:
     """Address of a tensor / array, an int address, or None (NULL)."""
-    if t is None or isinstance(t, int):
-        return t
-    if hasattr(t, "data_ptr"):
+    if t is None:
+        return None
+    try:
         return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, int):
+        return t
     if hasattr(t, "ctypes"):
         return t.ctypes.data
     raise TypeError(f"cannot take the address of {type(t)}")
 
 
-@functools.lru_cache(maxsize=None)
-def _raw_stream():
-    """torch's function from a device index to its current cudaStream_t, if it has one."""
+def _public_stream() -> int:
     import torch
-    return getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _current_stream() -> int:
+    """cudaStream_t of torch's current stream.  torch hands it out without a Stream object
+    too: 0.2 us of a small call's host time instead of 3 (Grace)."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        _current_stream = _public_stream
+    elif torch.cuda.is_initialized():  # from here on
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _public_stream()
 
 
 def _stream(s) -> int | None:
     """cudaStream_t of a torch stream; None means torch's current stream."""
     if s is None:
-        import torch
-        # without a Stream object: 0.2 us of a small call's host time instead of 3 (Grace)
-        if torch.cuda.is_initialized() and _raw_stream():
-            return _raw_stream()(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

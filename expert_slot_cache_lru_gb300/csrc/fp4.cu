@@ -13,6 +13,7 @@
 // near the ends of fp32's range divides instead.
 #include "block_ops.cuh"
 #include "fp4.cuh"
+#include "tc.cuh"
 
 namespace moe {
 namespace {
@@ -162,6 +163,8 @@ __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const T* __restrict__ src, long long stride, int rows, long long np,
                 const float* __restrict__ gp, uint8_t* __restrict__ codes,
                 uint8_t* __restrict__ scales) {
+  tc::pdl_trigger();
+  tc::pdl_wait();
   const float g = NV && gp ? __ldg(gp) : 1.f;
   const long long i0 = (long long)blockIdx.x * (kThreads * U) + threadIdx.x;
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
@@ -193,6 +196,8 @@ __global__ void __launch_bounds__(kThreads)
 dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int rows,
                   long long np, const float* __restrict__ gp, T* __restrict__ dst,
                   long long stride) {
+  tc::pdl_trigger();
+  tc::pdl_wait();
   const float g = NV && gp ? __ldg(gp) : 1.f;
   const long long i0 = (long long)blockIdx.x * (kThreads * U) + threadIdx.x;
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
@@ -276,8 +281,7 @@ cudaError_t quantize(const T* src, long long stride, int rows, int cols, const f
   const bool vec = aligned32(src, stride * (long long)sizeof(T));
   const Grid q = grid_for(rows, cols / 16, stride == cols, vec ? kUnits : 1);
   auto go = [&](auto kern) {
-    kern<<<q.grid, kThreads, 0, s>>>(src, stride, q.rows, q.width, g, codes, scales);
-    return cudaGetLastError();
+    return tc::launch_early(kern, q.grid, dim3(kThreads), 0, s, src, stride, q.rows, q.width, g, codes, scales);
   };
   if (!vec) return go(quantize_kernel<NV, T, false, 1>);
   return q.wide ? go(quantize_kernel<NV, T, true, kUnits>) : go(quantize_kernel<NV, T, true, 1>);
@@ -288,8 +292,7 @@ cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, const float*
   const bool vec = aligned32(dst, stride * (long long)sizeof(T));
   const Grid q = grid_for(rows, cols / 16, stride == cols, vec ? kUnits : 1);
   auto go = [&](auto kern) {
-    kern<<<q.grid, kThreads, 0, s>>>(codes, scales, q.rows, q.width, g, dst, stride);
-    return cudaGetLastError();
+    return tc::launch_early(kern, q.grid, dim3(kThreads), 0, s, codes, scales, q.rows, q.width, g, dst, stride);
   };
   if (!vec) return go(dequantize_kernel<NV, T, false, 1>);
   return q.wide ? go(dequantize_kernel<NV, T, true, kUnits>) : go(dequantize_kernel<NV, T, true, 1>);

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a) {
   const int first = group * gs + lane % lanes, end = (group + 1) * gs;
   const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  tc::pdl_trigger();
   tc::pdl_wait();
   float s[EL];
   uint32_t key[EL];
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  tc::pdl_trigger();
   tc::pdl_wait();
   float mx = -INFINITY;
   for (int e = threadIdx.x; e < a.E; e += kBigThreads) mx = fmaxf(mx, load_f(zr + e));
@@ -295,22 +297,10 @@ __global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
   if (warp == 0) write_row(a, b, lane, sm.pick[lane], sm.pick[lane] < 0 ? 0.f : sm.w[lane]);
 }
 
-// The selection may start beside the kernel before it in the stream (both
-// kernels wait for its results before they read logits).
 template <typename K>
 cudaError_t launch_after(K kern, unsigned grid, unsigned block, size_t smem, const RouteArgs& a,
                          cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return tc::launch_early(kern, dim3(grid), dim3(block), smem, s, a);
 }
 
 template <typename T>
@@ -324,8 +314,8 @@ cudaError_t select(const RouteArgs& a, cudaStream_t s) {
   if (per <= 8) return launch_after(select_warp_kernel<8, T>, grid, 128, 0, a, s);
   if (per <= 16) return launch_after(select_warp_kernel<16, T>, grid, 128, 0, a, s);
   if (per <= 32) return launch_after(select_warp_kernel<32, T>, grid, 128, 0, a, s);
-  static const cudaError_t e = cudaFuncSetAttribute(
-      select_cta_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 8);
+  static tc::Once once;
+  const cudaError_t e = tc::raise_smem(once, select_cta_kernel<T>, 16384 * 8);
   if (e != cudaSuccess) return e;
   return launch_after(select_cta_kernel<T>, (unsigned)a.rows, kBigThreads, (size_t)a.E * 8, a, s);
 }
@@ -340,6 +330,7 @@ dot_kernel(const __nv_bfloat16* __restrict__ x, long long x_stride,
            float* __restrict__ z) {
   __shared__ float red[kDotWarps][R];
   tc::pdl_trigger();
+  tc::pdl_wait();
   const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint4* w = reinterpret_cast<const uint4*>(router + (size_t)e * hidden);
   float acc[R] = {};
@@ -396,8 +387,7 @@ cudaError_t launch_route_logits(const __nv_bfloat16* x, long long x_stride,
                      ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(router)) & 15) == 0;
   if (whole && rows <= kDotRows) {
     auto go = [&](auto kern) {
-      kern<<<E, 32 * kDotWarps, 0, s>>>(x, x_stride, router, rows, hidden, E, z);
-      return cudaGetLastError();
+      return tc::launch_early(kern, dim3(E), dim3(32 * kDotWarps), 0, s, x, x_stride, router, rows, hidden, E, z);
     };
     return rows == 1 ? go(dot_kernel<1>) : rows <= 4 ? go(dot_kernel<4>) : go(dot_kernel<kDotRows>);
   }

@@ -2,6 +2,7 @@
 // mbarriers with bounded waits, TMA tile loads, tensor memory, MMA issue.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -146,7 +147,7 @@ __device__ __forceinline__ void copy_to_peer(uint32_t dst, const void* src, uint
       : "memory");
 }
 // programmatic launch: let the next kernel of the stream start; wait for the
-// previous one's results
+// previous one's results (for kernels started by launch_early)
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -280,6 +281,42 @@ struct DeviceInfo {
 };
 // The current device's, read once per device.
 cudaError_t device_info(DeviceInfo* out);
+
+// Launches a kernel that may start while the one before it in the stream ends:
+// it calls pdl_wait before it touches memory, and pdl_trigger first of all, for
+// the next such kernel.  Hides launch and set-up, about a microsecond a call.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+// A kernel's dynamic shared-memory limit, set by its first launch on each device
+// (devices past the 64th set it every time).
+struct Once {
+  std::atomic<unsigned long long> done{0};
+};
+template <typename K>
+cudaError_t raise_smem(Once& once, K kern, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (once.done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) once.done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 }  // namespace tc
 }  // namespace moe

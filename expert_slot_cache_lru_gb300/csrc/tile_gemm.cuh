@@ -230,6 +230,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   const int n_chains = min(T::kChains, n_k);
   const uint16_t mask = (uint16_t)(((1 << CG) - 1) << first);
 
+  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&c.full[i], 1);
@@ -255,7 +256,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   if (CG > 1) cluster_sync();  // the peer's barriers exist before anything arrives there
   fence_after();
   const uint32_t tmem = c.tmem;
-  if (KIND == kBf16) pdl_trigger();  // the router's selection
+  pdl_wait();
 
   if (warp == T::kTmaWarp) {
     int it = 0, s = 0;
@@ -650,9 +651,9 @@ template <Kind KIND, int NT, int CG, bool SWAP>
 cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   using T = Shape<KIND, NT, CG>;
   auto kern = gemm_kernel<KIND, NT, CG, SWAP>;
-  static const cudaError_t set =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
-  if (set != cudaSuccess) return set;
+  static Once once;
+  cudaError_t e = raise_smem(once, kern, T::kSmem);
+  if (e != cudaSuccess) return e;
   Args a{};
   a.ps = l.ps;
   a.qs = l.qs;
@@ -678,7 +679,7 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   CUtensorMap pm, qm, psm{}, qsm{};
   const int elem = KIND == kBf16 ? 2 : 1;
   const long long width = KIND == kBf16 ? l.k : l.k / 2;
-  cudaError_t e = make_map(&pm, l.p, elem, width, l.p_rows, l.p_stride, 128);
+  e = make_map(&pm, l.p, elem, width, l.p_rows, l.p_stride, 128);
   if (e == cudaSuccess) e = make_map(&qm, l.q, elem, width, l.q_rows, l.q_stride, T::kQ);
   if (T::kBlocks && a.piece == 16) {
     if (e == cudaSuccess) e = make_scale_map(&psm, l.ps, a.sb, l.p_rows, 128);
@@ -691,11 +692,13 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   cfg.blockDim = dim3(T::kThreads);
   cfg.dynamicSmemBytes = T::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)team, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, pm, qm, psm, qsm, a);
 }
 

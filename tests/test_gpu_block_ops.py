@@ -106,6 +106,15 @@ def test_norm_many_rows(m):
     norm_case(m, 70000, 24, gate="linear_rows", post=True)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(alias=True), dict(alias=True, gate="sigmoid_rows"), dict(gate="sigmoid", offset=1.0, alpha=0.3),
+    dict(gate="linear", post=False), dict(y=False), dict(pre=False, gate="linear_rows"),
+    dict(h_out=False, pad=8), dict(res="f32", alias=True, gate="linear_rows")])
+@pytest.mark.parametrize("B,H", [(1300, 2048), (500, 8192), (5001, 520), (700, 4104)])
+def test_norm_more_rows_than_fit_at_once(m, kw, B, H):
+    norm_case(m, B, H, **kw)
+
+
 def test_norm_zero_rows_and_extremes(m):
     """A row of zeros stays zero (eps carries the root); a NaN and an infinity
     stay in their own rows."""
