@@ -38,7 +38,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // score numerators: softmax's exp(z - max) or the sigmoid itself
 __device__ __forceinline__ float raw_score(float z, bool softmax, float zmax) {
   if (!(z > -INFINITY)) return 0.f;
-  if (!softmax) return 1.f / (1.f + expf(-z));
+  if (!softmax) return __fdividef(1.f, 1.f + expf(-z));  // 2 ulp; 0 where the quotient is below 2^-126
   if (zmax == INFINITY) return z == INFINITY ? 1.f : 0.f;
   return expf(z - zmax);
 }
@@ -67,70 +67,76 @@ __device__ __forceinline__ void write_row(const RouteArgs& a, long long b, int l
   }
 }
 
+// `shift`: log2 of the lanes per group; gs: experts per group.  A pick's score is
+// made again from its logit, by the lane that writes it, so that no scores move with
+// the picks.
 template <int EL, typename T>
-__global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift, int gs) {
+  tc::pdl_trigger();
   const long long b = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (b >= a.rows) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, lanes = 1 << shift, group = lane >> shift;
   // lane's experts: first + j * lanes, below end
-  const int lanes = 32 / a.groups, gs = a.E / a.groups, group = lane / lanes;
-  const int first = group * gs + lane % lanes, end = (group + 1) * gs;
+  const int first = group * gs + (lane & (lanes - 1)), end = (group + 1) * gs;
   const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
-  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  tc::pdl_trigger();
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX, two = a.groups > 1 && a.group_top == 2;
   tc::pdl_wait();
   float s[EL];
   uint32_t key[EL];
-  float mx = -INFINITY;
+  float mx = -INFINITY, inv = 1.f;
 #pragma unroll
   for (int j = 0; j < EL; ++j) {
-    s[j] = first + j * lanes < end ? load_f(zr + first + j * lanes) : -INFINITY;
+    s[j] = first + (j << shift) < end ? load_f(zr + first + (j << shift)) : -INFINITY;
     mx = fmaxf(mx, s[j]);  // fmaxf drops NaN
   }
+#pragma unroll
+  for (int j = 0; j < EL; ++j) key[j] = choice_key(s[j]);  // without a bias the logits rank
   if (softmax) mx = warp_max(mx);
-  float sum = 0.f;
+  if (softmax || a.bias || two) {
+    float sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < EL; ++j) {
-    const float z = s[j];
-    key[j] = choice_key(z);  // without a bias the logits rank
-    sum += s[j] = raw_score(z, softmax, mx);
-  }
-  if (softmax) {
-    sum = warp_sum(sum);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    for (int j = 0; j < EL; ++j) sum += s[j] = raw_score(s[j], softmax, mx);
+    if (softmax) {
+      sum = warp_sum(sum);
+      inv = sum > 0.f ? 1.f / sum : 0.f;
+    }
+    if (a.bias) {
 #pragma unroll
-    for (int j = 0; j < EL; ++j) s[j] *= inv;
-  }
-  if (a.bias) {
-#pragma unroll
-    for (int j = 0; j < EL; ++j)
-      if (key[j]) key[j] = choice_key(s[j] + __ldg(a.bias + first + j * lanes));
+      for (int j = 0; j < EL; ++j)
+        if (key[j]) key[j] = choice_key(fmaf(s[j], inv, __ldg(a.bias + first + (j << shift))));
+    }
   }
   if (a.groups > 1) {
     uint32_t k1 = 0u, k2 = 0u;  // the group's two largest choices
-    float s1 = 0.f, s2 = 0.f;   // and scores
+    float s1 = 0.f, s2 = 0.f;   // without a bias: its two largest scores
 #pragma unroll
     for (int j = 0; j < EL; ++j) {
-      const float v = key[j] ? s[j] : 0.f;
       k2 = max(k2, min(k1, key[j]));
       k1 = max(k1, key[j]);
-      s2 = fmaxf(s2, fminf(s1, v));
-      s1 = fmaxf(s1, v);
+    }
+    if (two && !a.bias) {
+#pragma unroll
+      for (int j = 0; j < EL; ++j) {
+        const float v = key[j] ? s[j] * inv : 0.f;
+        s2 = fmaxf(s2, fminf(s1, v));
+        s1 = fmaxf(s1, v);
+      }
     }
     for (int o = lanes >> 1; o > 0; o >>= 1) {
       const uint32_t q1 = __shfl_xor_sync(kAll, k1, o), q2 = __shfl_xor_sync(kAll, k2, o);
-      const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
       k2 = max(min(k1, q1), max(k2, q2));
       k1 = max(k1, q1);
-      s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
-      s1 = fmaxf(s1, t1);
+      if (two && !a.bias) {
+        const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
+        s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
+        s1 = fmaxf(s1, t1);
+      }
     }
     uint32_t mine = k1;
-    if (a.group_top == 2 && k1)
-      mine = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
+    if (two && k1) mine = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
     int rank = 0;  // groups ahead of this one
     for (int g = 0; g < a.groups; ++g) {
-      const uint32_t other = __shfl_sync(kAll, mine, g * lanes);
+      const uint32_t other = __shfl_sync(kAll, mine, g << shift);
       rank += other > mine || (other == mine && g < group);
     }
     if (rank >= a.topk_groups || !mine) {
@@ -139,37 +145,29 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a) {
     }
   }
   int my_id = -1;
-  float my_w = 0.f;
   for (int r = 0; r < a.k; ++r) {
     uint32_t top = key[0];
 #pragma unroll
     for (int j = 1; j < EL; ++j) top = max(top, key[j]);
     const uint32_t best = __reduce_max_sync(kAll, top);
     if (!best) break;
-    // the lane's lowest id that holds the best key, its score; ids grow with j
-    int at = 0x7fffffff;
-    float w = 0.f;
+    // the lane's lowest id that holds the best key; ids grow with j
+    int at = EL;
     if (top == best) {
 #pragma unroll
       for (int j = EL - 1; j >= 0; --j)
-        if (key[j] == best) {
-          at = first + j * lanes;
-          w = s[j];
-        }
+        if (key[j] == best) at = j;
     }
-    const int id = __reduce_min_sync(kAll, at);
-    if (at == id) {
+    const int cand = at < EL ? first + (at << shift) : 0x7fffffff;
+    const int id = __reduce_min_sync(kAll, cand);
+    if (cand == id) {
 #pragma unroll
       for (int j = 0; j < EL; ++j)
-        if (first + j * lanes == id) key[j] = 0u;
+        if (j == at) key[j] = 0u;
     }
-    w = __shfl_sync(kAll, w, __ffs(__ballot_sync(kAll, at == id)) - 1);
-    if (lane == r) {
-      my_id = id;
-      my_w = w;
-    }
+    if (lane == r) my_id = id;
   }
-  write_row(a, b, lane, my_id, my_w);
+  write_row(a, b, lane, my_id, my_id < 0 ? 0.f : raw_score(load_f(zr + my_id), softmax, mx) * inv);
 }
 
 constexpr int kBigThreads = 256;
@@ -297,27 +295,25 @@ __global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
   if (warp == 0) write_row(a, b, lane, sm.pick[lane], sm.pick[lane] < 0 ? 0.f : sm.w[lane]);
 }
 
-template <typename K>
-cudaError_t launch_after(K kern, unsigned grid, unsigned block, size_t smem, const RouteArgs& a,
-                         cudaStream_t s) {
-  return tc::launch_early(kern, dim3(grid), dim3(block), smem, s, a);
-}
-
 template <typename T>
 cudaError_t select(const RouteArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)((a.rows + 3LL) / 4);
-  const int lanes = 32 / a.groups;  // per group
-  const int per = 32 % a.groups ? 33 : (a.E / a.groups + lanes - 1) / lanes;
-  if (per <= 1) return launch_after(select_warp_kernel<1, T>, grid, 128, 0, a, s);
-  if (per <= 2) return launch_after(select_warp_kernel<2, T>, grid, 128, 0, a, s);
-  if (per <= 4) return launch_after(select_warp_kernel<4, T>, grid, 128, 0, a, s);
-  if (per <= 8) return launch_after(select_warp_kernel<8, T>, grid, 128, 0, a, s);
-  if (per <= 16) return launch_after(select_warp_kernel<16, T>, grid, 128, 0, a, s);
-  if (per <= 32) return launch_after(select_warp_kernel<32, T>, grid, 128, 0, a, s);
+  const int gs = a.E / a.groups;
+  int shift = 5;  // lanes per group: 32 / groups
+  while (shift > 0 && a.groups << shift > 32) --shift;
+  const int per = a.groups << shift == 32 ? (gs + (1 << shift) - 1) >> shift : 33;
+  auto go = [&](auto kern) {
+    return tc::launch_early(kern, dim3((unsigned)((a.rows + 3LL) / 4)), dim3(128), 0, s, a, shift, gs);
+  };
+  if (per <= 1) return go(select_warp_kernel<1, T>);
+  if (per <= 2) return go(select_warp_kernel<2, T>);
+  if (per <= 4) return go(select_warp_kernel<4, T>);
+  if (per <= 8) return go(select_warp_kernel<8, T>);
+  if (per <= 16) return go(select_warp_kernel<16, T>);
+  if (per <= 32) return go(select_warp_kernel<32, T>);
   static tc::Once once;
   const cudaError_t e = tc::raise_smem(once, select_cta_kernel<T>, 16384 * 8);
   if (e != cudaSuccess) return e;
-  return launch_after(select_cta_kernel<T>, (unsigned)a.rows, kBigThreads, (size_t)a.E * 8, a, s);
+  return tc::launch_early(select_cta_kernel<T>, dim3((unsigned)a.rows), dim3(kBigThreads), (size_t)a.E * 8, s, a);
 }
 
 constexpr int kDotRows = 8, kDotWarps = 4;

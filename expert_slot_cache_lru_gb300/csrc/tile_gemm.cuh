@@ -580,6 +580,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         if (row < rows && !c.abort_flag) store_one(a, (q0 + col) * a.out_stride + p0 + row, v * g);
       }
     } else {  // four neighbouring columns per thread
+#pragma unroll 4
       for (int i = threadIdx.x; i < rows * (NT / 4); i += kThreads) {
         const int row = i / (NT / 4), col = i % (NT / 4) * 4;
         if (col >= cols || c.abort_flag) continue;
