@@ -190,17 +190,62 @@ __device__ __forceinline__ float global_scale(const Args& a) {
   return (a.g0 ? *a.g0 : 1.f) * (a.g1 ? *a.g1 : 1.f);
 }
 
-// W columns of the warp's lanes, the sums of n_chains parts of K added up
+// W columns of the warp's lanes, the sums of n_chains parts of K added up in order
 template <int NT, int W>
 __device__ __forceinline__ void read_sums(uint32_t at, int n_chains, uint32_t (&v)[W]) {
+  uint32_t u[W];
   tmem_ld(at, v);
+  if (n_chains > 1) tmem_ld(at + NT, u);
   tmem_wait_ld();
   for (int k = 1; k < n_chains; ++k) {
-    uint32_t u[W];
-    tmem_ld(at + k * NT, u);
-    tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+    if (k + 1 < n_chains) {
+      tmem_ld(at + (k + 1) * NT, u);
+      tmem_wait_ld();
+    }
+  }
+}
+
+// The end of a split tile: `rows` rows of this part and `cols` columns, S parts' sums of
+// each added up in order and stored, four neighbouring columns per thread; several
+// loads in flight, since little else hides their latency here.
+// own: this part's sums [128][pitch]; in: the other parts' [S - 1][rows_per][pitch].
+template <int NT, int S>
+__device__ __forceinline__ void add_parts(const Args& a, uint32_t own, uint32_t in, int part, int rows,
+                                          int cols, long long to0, float g, int threads) {
+  constexpr int kPitch = NT + 4, kRows = 128 / S, U = 8 / S;
+  for (int i0 = threadIdx.x; i0 < rows * (NT / 4); i0 += U * threads) {
+    float4 x[U][S];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u * threads, rows * (NT / 4) - 1), row = i / (NT / 4), col = i % (NT / 4) * 4;
+#pragma unroll
+      for (int k = 0; k < S; ++k)
+        x[u][k] = lds4(k == part ? own + 4 * ((part * kRows + row) * kPitch + col)
+                                 : in + 4 * (((k < part ? k : k - 1) * kRows + row) * kPitch + col));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * threads, row = i / (NT / 4), col = i % (NT / 4) * 4;
+      if (i >= rows * (NT / 4) || col >= cols) continue;
+      float4 v = x[u][0];
+#pragma unroll
+      for (int k = 1; k < S; ++k) v.x += x[u][k].x, v.y += x[u][k].y, v.z += x[u][k].z, v.w += x[u][k].w;
+      const long long to = to0 + row * a.out_stride + col;
+      const float r[4] = {v.x * g, v.y * g, v.z * g, v.w * g};
+      if (a.wide && col + 4 <= cols) {
+        if (a.f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(r[0], r[1], r[2], r[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
+              make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < cols) store_one(a, to + j, r[j]);
+      }
+    }
   }
 }
 
@@ -561,50 +606,30 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     }
     wait_bar(&c.sums, 0, &c.abort_flag, a.status);
     __syncthreads();
+    cluster_arrive();  // what the peers copied here has left their shared memory
     int tp, tq;
     tile_at(a, tile0, tp, tq);
     const float g = global_scale(a);
-    // row r of part k's sums
-    auto sums = [&](int k, int r) {
-      return k == part ? own + (part * rows_per + r) * kPitch
-                       : in + ((k < part ? k : k - 1) * rows_per + r) * kPitch;
-    };
     const long long p0 = ((long long)tp * CG + pair) * 128 + part * rows_per, q0 = (long long)tq * NT;
     const int rows = (int)max(0LL, min((long long)rows_per, a.p_rows - p0));
     const int cols = (int)min((long long)NT, a.q_rows - q0);
-    if (SWAP) {  // neighbouring threads take neighbouring rows: outputs of one token
+    if (c.abort_flag) {
+    } else if (SWAP) {  // neighbouring threads take neighbouring rows: outputs of one token
       for (int i = threadIdx.x; i < cols * rows_per; i += kThreads) {
         const int row = i % rows_per, col = i / rows_per;
         float v = 0.f;
-        for (int k = 0; k < a.split; ++k) v += sums(k, row)[col];
-        if (row < rows && !c.abort_flag) store_one(a, (q0 + col) * a.out_stride + p0 + row, v * g);
+        for (int k = 0; k < a.split; ++k)
+          v += k == part ? own[(part * rows_per + row) * kPitch + col]
+                         : in[((k < part ? k : k - 1) * rows_per + row) * kPitch + col];
+        if (row < rows) store_one(a, (q0 + col) * a.out_stride + p0 + row, v * g);
       }
-    } else {  // four neighbouring columns per thread
-#pragma unroll 4
-      for (int i = threadIdx.x; i < rows * (NT / 4); i += kThreads) {
-        const int row = i / (NT / 4), col = i % (NT / 4) * 4;
-        if (col >= cols || c.abort_flag) continue;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < a.split; ++k) {
-          const float4 x = *reinterpret_cast<const float4*>(sums(k, row) + col);
-          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        }
-        const long long to = (p0 + row) * a.out_stride + q0 + col;
-        const float r[4] = {v.x * g, v.y * g, v.z * g, v.w * g};
-        if (a.wide && col + 4 <= cols) {
-          if (a.f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(r[0], r[1], r[2], r[3]);
-          else
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
-                make_uint2(pack2(r[0], r[1]), pack2(r[2], r[3]));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (col + j < cols) store_one(a, to + j, r[j]);
-        }
-      }
+    } else if (a.split == 2) {
+      add_parts<NT, 2>(a, sa(own), sa(in), part, rows, cols, p0 * a.out_stride + q0, g, kThreads);
+    } else {
+      add_parts<NT, 4>(a, sa(own), sa(in), part, rows, cols, p0 * a.out_stride + q0, g, kThreads);
     }
-    cluster_sync();  // this CTA's copies have left its shared memory
+    __syncwarp();
+    cluster_wait();  // this CTA's copies have left its shared memory
   }
   fence_before();
   __syncthreads();
