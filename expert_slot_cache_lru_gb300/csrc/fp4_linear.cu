@@ -31,10 +31,10 @@ cudaError_t by_rows(const Fp4Linear& l, int sms, cudaStream_t s) {
   if (l.rows <= 16) return tg::launch<KIND, 16, 1, true>(p, sms, s);
   if (l.rows <= 32) return tg::launch<KIND, 32, 1, true>(p, sms, s);
   if (l.rows <= 64) return tg::launch<KIND, 64, 1, true>(p, sms, s);
-  // the tile that asks least of an SM's intake
-  const long long c64 = tg::intake<KIND, 64, 1>(l.rows, l.n, l.k, sms),
-                  c128 = tg::intake<KIND, 128, 1>(l.rows, l.n, l.k, sms),
-                  c192 = tg::intake<KIND, 192, 2>(l.rows, l.n, l.k, sms);
+  // the tile estimated to take least
+  const long long c64 = tg::cycles<KIND, 64, 1>(l.rows, l.n, l.k, sms),
+                  c128 = tg::cycles<KIND, 128, 1>(l.rows, l.n, l.k, sms),
+                  c192 = tg::cycles<KIND, 192, 2>(l.rows, l.n, l.k, sms);
   if (c192 <= c128 && c192 <= c64) return tg::launch<KIND, 192, 2, false>(p, sms, s);
   if (c128 <= c64) return tg::launch<KIND, 128, 1, false>(p, sms, s);
   return tg::launch<KIND, 64, 1, false>(p, sms, s);

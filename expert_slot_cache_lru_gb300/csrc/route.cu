@@ -403,9 +403,9 @@ cudaError_t launch_route_logits(const __nv_bfloat16* x, long long x_stride,
     p.out_stride = E;
     p.f32 = true;
     p.status = status;
-    const long long c64 = tg::intake<tg::kBf16, 64, 1>(rows, E, hidden, d.sms),
-                    c128 = tg::intake<tg::kBf16, 128, 1>(rows, E, hidden, d.sms),
-                    c256 = tg::intake<tg::kBf16, 256, 2>(rows, E, hidden, d.sms);
+    const long long c64 = tg::cycles<tg::kBf16, 64, 1>(rows, E, hidden, d.sms),
+                    c128 = tg::cycles<tg::kBf16, 128, 1>(rows, E, hidden, d.sms),
+                    c256 = tg::cycles<tg::kBf16, 256, 2>(rows, E, hidden, d.sms);
     if (c256 <= c128 && c256 <= c64) return tg::launch<tg::kBf16, 256, 2, false>(p, d.sms, s);
     if (c128 <= c64) return tg::launch<tg::kBf16, 128, 1, false>(p, d.sms, s);
     return tg::launch<tg::kBf16, 64, 1, false>(p, d.sms, s);

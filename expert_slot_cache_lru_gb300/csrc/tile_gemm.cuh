@@ -659,18 +659,20 @@ inline int split_for(long long tiles, int nk, int cg, int sms) {
   return s;
 }
 
-// What a CTA takes in for its share of the product, in bytes: the measure the tile
-// of a product is chosen by (an SM's intake, about 52 bytes per cycle, bounds all
-// but the largest products), with a split's exchange of partial sums.
+// Estimated cycles of a product with this tile, the measure the tile is chosen by:
+// stages times the cycles one was measured to take when nothing else bounds it (an SM
+// takes in about 64 bytes per cycle; a stage of 4-bit rows has its scales to move), and a
+// split's exchange of partial sums (2,500 cycles and 18 bytes per cycle).
 template <Kind KIND, int NT, int CG>
-long long intake(long long p_rows, long long q_rows, int k, int sms) {
+long long cycles(long long p_rows, long long q_rows, int k, int sms) {
   using T = Shape<KIND, NT, CG>;
+  constexpr int kStageCycles = KIND == kBf16 ? (NT <= 64 ? 450 : NT <= 128 ? 494 : 520)
+                                             : (NT <= 64 ? 480 : NT <= 128 ? 600 : 630);
   const long long tiles = (p_rows + 128 * CG - 1) / (128 * CG) * ((q_rows + NT - 1) / NT);
   const int slab = KIND == kBf16 ? 64 : 256, nk = (k + slab - 1) / slab;
   const int split = split_for(tiles, (nk + T::kPer - 1) / T::kPer, CG, sms);
   const long long per = sms / (CG * split), waves = (tiles + per - 1) / per;
-  const long long stage = T::kStage + (T::kBlocks ? T::kBlocks * 4 * (128 + NT) : 0);
-  return waves * ((nk + split - 1) / split * stage + (split > 1 ? 128 * NT * 6 : 0));
+  return waves * ((nk + split - 1) / split * kStageCycles) + (split > 1 ? 2500 + 128 * NT * 4 / 18 : 0);
 }
 
 template <Kind KIND, int NT, int CG, bool SWAP>
