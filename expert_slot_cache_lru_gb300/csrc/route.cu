@@ -35,12 +35,14 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// score numerators: softmax's exp(z - max) or the sigmoid itself
+// Score numerators: softmax's exp(z - max) or the sigmoid itself.  The fast
+// exponential's relative error, about |argument| 2^-24, is that of a score that is itself
+// e^-|argument| of the largest.
 __device__ __forceinline__ float raw_score(float z, bool softmax, float zmax) {
   if (!(z > -INFINITY)) return 0.f;
-  if (!softmax) return __fdividef(1.f, 1.f + expf(-z));  // 2 ulp; 0 where the quotient is below 2^-126
+  if (!softmax) return __fdividef(1.f, 1.f + __expf(-z));  // 0 where the quotient is below 2^-126
   if (zmax == INFINITY) return z == INFINITY ? 1.f : 0.f;
-  return expf(z - zmax);
+  return __expf(z - zmax);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -90,7 +92,8 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
     mx = fmaxf(mx, s[j]);  // fmaxf drops NaN
   }
 #pragma unroll
-  for (int j = 0; j < EL; ++j) key[j] = choice_key(s[j]);  // without a bias the logits rank
+  for (int j = 0; j < EL; ++j)  // without a bias the logits rank
+    key[j] = a.bias ? s[j] > -INFINITY : choice_key(s[j]);
   if (softmax) mx = warp_max(mx);
   if (softmax || a.bias || two) {
     float sum = 0.f;

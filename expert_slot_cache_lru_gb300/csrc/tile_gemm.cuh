@@ -56,7 +56,7 @@ struct Shape {
   static constexpr int kPer = KIND == kMx ? 2 : 1;            // stages in 16 bytes of a row's scales
   static constexpr int kGroupStages = 4 * kPer;
   static constexpr int kQRows = (NT + 31) / 32 * 32;          // Q rows of scales in shared memory
-  static constexpr int kQCols = NT < 128 ? 4 : NT / 32;       // Q columns of a scale block
+  static constexpr int kQCols = NT < 128 ? 4 : (NT + 31) / 32;  // Q columns of a scale block
   static constexpr int kScaleCols = kBlocks * (4 + kQCols);   // of tensor memory, per stage
   static constexpr int kStage = 128 * 128 + kQ * 128;
   static constexpr int kSlot = (128 + kQRows) * 64;           // a group of scales
