@@ -115,6 +115,23 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* b) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(b)) : "memory");
 }
 
+// A tile from shared memory to the matrix of `map`, clipped at its edges; commit, and
+// waits of the thread that issued it: until all but N copies have been read, or
+// are done.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(sa(src))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -288,6 +305,11 @@ cudaError_t make_map(CUtensorMap* map, const void* base, int elem, long long wid
 // The same for scale banks: tiles of 64 bytes, 64-byte swizzle.
 cudaError_t make_scale_map(CUtensorMap* map, const void* base, long long row_bytes, long long rows,
                            int box_rows);
+
+// A map of an output matrix of bf16 or fp32 in tiles of 32 x 32, 64- or 128-byte
+// swizzle (rows a multiple of 16 bytes apart; base 16-byte aligned).
+cudaError_t make_out_map(CUtensorMap* map, void* base, bool f32, long long width, long long rows,
+                         long long row_bytes);
 
 struct DeviceInfo {
   int sms;

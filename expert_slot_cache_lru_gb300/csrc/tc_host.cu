@@ -56,6 +56,12 @@ cudaError_t make_scale_map(CUtensorMap* map, const void* base, long long row_byt
                 CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+cudaError_t make_out_map(CUtensorMap* map, void* base, bool f32, long long width, long long rows,
+                         long long row_bytes) {
+  return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, width,
+                rows, row_bytes, 32, 32, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 cudaError_t device_info(DeviceInfo* out) {
   constexpr int kMax = 64;
   static std::atomic<int> sms[kMax];

@@ -61,7 +61,8 @@ struct Shape {
   static constexpr int kStage = 128 * 128 + kQ * 128;
   static constexpr int kSlot = (128 + kQRows) * 64;           // a group of scales
   static constexpr int kScaleSmem = kBlocks ? kGroups * kSlot : 0;
-  static constexpr int kFit = (226 * 1024 - 1024 - 1024 - kScaleSmem) / kStage;
+  static constexpr int kOut = NT < 64 ? 0 : kEpiWarps * 4096;  // results on their way out
+  static constexpr int kFit = (226 * 1024 - 1024 - 1024 - kScaleSmem - kOut) / kStage;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   // stages of scales in tensor memory
   static constexpr int kBufs = !kBlocks ? 1 : 2 * NT + 4 * kScaleCols <= 512 ? 4 : 3;
@@ -72,9 +73,9 @@ struct Shape {
   static constexpr int kAcc = kBlocks && 2 * NT + kBufs * kScaleCols <= 512 ? 2 : 1;
   static constexpr int kUsed = kAcc * kChains * NT + kBufs * kScaleCols;
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static constexpr int kSmem = kStages * kStage + kScaleSmem + 1024;
+  static constexpr int kSmem = kStages * kStage + kOut + kScaleSmem + 1024;
   static_assert(kUsed <= 512 && kStage % 1024 == 0 && kStages >= kBufs, "tile shape");
-  static_assert(kStages * kStage >= 128 * (NT + 4) * 4 * (CG == 1 ? 7 : 6) / 4, "room for a split's sums");
+  static_assert(kStages * kStage + kOut >= 128 * (NT + 4) * 4 * (CG == 1 ? 7 : 6) / 4, "room for a split's sums");
 };
 
 struct Args {
@@ -88,7 +89,8 @@ struct Args {
   const float *g0, *g1;
   void* out;
   long long out_stride;
-  int f32, wide;           // wide: 32-byte stores fit the output's alignment
+  int f32;
+  int wide;                // the output's rows are whole 16-byte pieces
   unsigned long long* status;
 };
 
@@ -181,11 +183,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 __device__ __forceinline__ float global_scale(const Args& a) {
   return (a.g0 ? *a.g0 : 1.f) * (a.g1 ? *a.g1 : 1.f);
 }
@@ -254,12 +251,13 @@ template <Kind KIND, int NT, int CG, bool SWAP>
 __global__ void __launch_bounds__(Shape<KIND, NT, CG>::kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
             const __grid_constant__ CUtensorMap psmap, const __grid_constant__ CUtensorMap qsmap,
-            const Args a) {
+            const __grid_constant__ CUtensorMap omap, const Args a) {
   using T = Shape<KIND, NT, CG>;
   constexpr int ST = T::kStages, kThreads = T::kThreads;
   extern __shared__ uint8_t raw[];
   uint8_t* stg = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sstg = stg + (size_t)ST * T::kStage;
+  uint8_t* ostg = stg + (size_t)ST * T::kStage;
+  uint8_t* sstg = ostg + T::kOut;
   __shared__ Ctl<ST> c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int W = NT < 64 ? 16 : 32;  // columns the epilogue reads at a time
@@ -503,7 +501,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     __syncwarp();
   } else {
     const float g = global_scale(a);
-    int u = 0;
+    int u = 0, piece = 0;
     for (int t = tile0; t < n_tiles; t += step, ++u) {
       const int b = u % T::kAcc;
       int tp, tq;
@@ -529,34 +527,44 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
             for (int i = 0; i < W; ++i)
               if (i < nq) store_one(a, (q0 + i) * a.out_stride + p, __uint_as_float(v[i]) * g);
           }
-        } else if (p < a.p_rows) {
-          const long long at = p * a.out_stride + q0;
-          if (a.wide && nq == W) {
+        } else if (a.wide) {
+          // through shared memory (the copy's swizzle) and out by TMA, 32 rows x 32
+          // columns per warp: lanes that store their own rows touch 32 lines a store and
+          // keep the block scales waiting (8,192 x 8,192 x 4,096: 100 us, so 94)
+          if constexpr (!SWAP) {
+            uint8_t* o = ostg + warp * 4096 + (a.f32 ? 0 : (piece & 1) * 2048);
+            if (lane == 0) {  // what this buffer held has been read
+              if (a.f32) store_wait_read<0>();
+              else store_wait_read<1>();
+            }
+            __syncwarp();
             if (a.f32) {
-              float* o = static_cast<float*>(a.out) + at;
 #pragma unroll
-              for (int i = 0; i < W; i += 8) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__uint_as_float(v[i + j]) * g);
-                store32(o + i, w);
-              }
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(o + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                    make_float4(__uint_as_float(v[4 * i]) * g, __uint_as_float(v[4 * i + 1]) * g,
+                                __uint_as_float(v[4 * i + 2]) * g, __uint_as_float(v[4 * i + 3]) * g);
             } else {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
 #pragma unroll
-              for (int i = 0; i < W; i += 16) {
-                uint32_t w[8];
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  w[j] = pack2(__uint_as_float(v[i + 2 * j]) * g, __uint_as_float(v[i + 2 * j + 1]) * g);
-                store32(o + i, w);
+                for (int j = 0; j < 4; ++j)
+                  w[j] = pack2(__uint_as_float(v[8 * i + 2 * j]) * g, __uint_as_float(v[8 * i + 2 * j + 1]) * g);
+                *reinterpret_cast<uint4*>(o + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-              if (i < nq) store_one(a, at + i, __uint_as_float(v[i]) * g);
+            fence_async_smem();
+            __syncwarp();
+            // rows past the matrix are not written (a warp's rows may all be)
+            if (lane == 0 && p < a.p_rows) tma_store(&omap, o, (int)q0, (int)p);
+            ++piece;
           }
+        } else if (p < a.p_rows) {
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            if (i < nq) store_one(a, p * a.out_stride + q0 + i, __uint_as_float(v[i]) * g);
         }
       }
       fence_before();
@@ -566,6 +574,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         else mbar_arrive_at(peer_addr(sa(&c.acc_empty[b]), first));
       }
     }
+    if (lane == 0) store_wait_done();
     __syncwarp();
   }
   if (CG > 1 || a.split > 1) cluster_sync();
@@ -698,13 +707,13 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   a.out = l.out;
   a.out_stride = l.out_stride;
   a.f32 = l.f32;
-  a.wide = (reinterpret_cast<uintptr_t>(l.out) & 31) == 0 && l.out_stride % (l.f32 ? 8 : 16) == 0;
+  a.wide = (reinterpret_cast<uintptr_t>(l.out) & 15) == 0 && l.out_stride % (l.f32 ? 4 : 8) == 0;
   a.status = l.status;
   const long long tiles = (long long)a.tiles_p * a.tiles_q;
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   a.split = split_for(tiles, (a.nk + T::kPer - 1) / T::kPer, CG, sms);
   const int team = CG * a.split;
-  CUtensorMap pm, qm, psm{}, qsm{};
+  CUtensorMap pm, qm, psm{}, qsm{}, om{};
   const int elem = KIND == kBf16 ? 2 : 1;
   const long long width = KIND == kBf16 ? l.k : l.k / 2;
   e = make_map(&pm, l.p, elem, width, l.p_rows, l.p_stride, 128);
@@ -713,6 +722,8 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
     if (e == cudaSuccess) e = make_scale_map(&psm, l.ps, a.sb, l.p_rows, 128);
     if (e == cudaSuccess) e = make_scale_map(&qsm, l.qs, a.sb, l.q_rows, NT);
   }
+  if (e == cudaSuccess && !SWAP && a.wide && a.split == 1)
+    e = make_out_map(&om, l.out, l.f32, l.q_rows, l.p_rows, l.out_stride * (l.f32 ? 4 : 2));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const long long teams = tiles < sms / team ? tiles : sms / team;
@@ -727,7 +738,7 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, pm, qm, psm, qsm, a);
+  return cudaLaunchKernelEx(&cfg, kern, pm, qm, psm, qsm, om, a);
 }
 
 }  // namespace tg
