@@ -72,7 +72,7 @@ __device__ __forceinline__ void write_row(const RouteArgs& a, long long b, int l
 // `shift`: log2 of the lanes per group; gs: experts per group.  A pick's score is
 // made again from its logit, by the lane that writes it, so that no scores move with
 // the picks.
-template <int EL, typename T>
+template <int EL, bool BIAS, typename T>
 __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift, int gs) {
   tc::pdl_trigger();
   const long long b = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -86,6 +86,12 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
   float s[EL];
   uint32_t key[EL];
   float mx = -INFINITY, inv = 1.f;
+  float b_e[BIAS ? EL : 1];  // loaded before the first use: behind a condition they came one by one
+  if (BIAS) {
+#pragma unroll
+    for (int j = 0; j < EL; ++j)
+      b_e[j] = first + (j << shift) < end ? __ldg(a.bias + first + (j << shift)) : 0.f;
+  }
 #pragma unroll
   for (int j = 0; j < EL; ++j) {
     s[j] = first + (j << shift) < end ? load_f(zr + first + (j << shift)) : -INFINITY;
@@ -93,9 +99,9 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
   }
 #pragma unroll
   for (int j = 0; j < EL; ++j)  // without a bias the logits rank
-    key[j] = a.bias ? s[j] > -INFINITY : choice_key(s[j]);
+    key[j] = BIAS ? s[j] > -INFINITY : choice_key(s[j]);
   if (softmax) mx = warp_max(mx);
-  if (softmax || a.bias || two) {
+  if (softmax || BIAS || two) {
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < EL; ++j) sum += s[j] = raw_score(s[j], softmax, mx);
@@ -103,10 +109,12 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
       sum = warp_sum(sum);
       inv = sum > 0.f ? 1.f / sum : 0.f;
     }
-    if (a.bias) {
+    if (BIAS) {
 #pragma unroll
-      for (int j = 0; j < EL; ++j)
-        if (key[j]) key[j] = choice_key(fmaf(s[j], inv, __ldg(a.bias + first + (j << shift))));
+      for (int j = 0; j < EL; ++j) {
+        const uint32_t c = choice_key(fmaf(s[j], inv, b_e[j]));
+        key[j] = key[j] ? c : 0u;
+      }
     }
   }
   if (a.groups > 1) {
@@ -117,7 +125,7 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
       k2 = max(k2, min(k1, key[j]));
       k1 = max(k1, key[j]);
     }
-    if (two && !a.bias) {
+    if (two && !BIAS) {
 #pragma unroll
       for (int j = 0; j < EL; ++j) {
         const float v = key[j] ? s[j] * inv : 0.f;
@@ -129,14 +137,14 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
       const uint32_t q1 = __shfl_xor_sync(kAll, k1, o), q2 = __shfl_xor_sync(kAll, k2, o);
       k2 = max(min(k1, q1), max(k2, q2));
       k1 = max(k1, q1);
-      if (two && !a.bias) {
+      if (two && !BIAS) {
         const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
         s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
         s1 = fmaxf(s1, t1);
       }
     }
     uint32_t mine = k1;
-    if (two && k1) mine = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
+    if (two && k1) mine = choice_key(BIAS ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
     int rank = 0;  // groups ahead of this one
     for (int g = 0; g < a.groups; ++g) {
       const uint32_t other = __shfl_sync(kAll, mine, g << shift);
@@ -307,12 +315,12 @@ cudaError_t select(const RouteArgs& a, cudaStream_t s) {
   auto go = [&](auto kern) {
     return tc::launch_early(kern, dim3((unsigned)((a.rows + 3LL) / 4)), dim3(128), 0, s, a, shift, gs);
   };
-  if (per <= 1) return go(select_warp_kernel<1, T>);
-  if (per <= 2) return go(select_warp_kernel<2, T>);
-  if (per <= 4) return go(select_warp_kernel<4, T>);
-  if (per <= 8) return go(select_warp_kernel<8, T>);
-  if (per <= 16) return go(select_warp_kernel<16, T>);
-  if (per <= 32) return go(select_warp_kernel<32, T>);
+  if (per <= 1) return a.bias ? go(select_warp_kernel<1, true, T>) : go(select_warp_kernel<1, false, T>);
+  if (per <= 2) return a.bias ? go(select_warp_kernel<2, true, T>) : go(select_warp_kernel<2, false, T>);
+  if (per <= 4) return a.bias ? go(select_warp_kernel<4, true, T>) : go(select_warp_kernel<4, false, T>);
+  if (per <= 8) return a.bias ? go(select_warp_kernel<8, true, T>) : go(select_warp_kernel<8, false, T>);
+  if (per <= 16) return a.bias ? go(select_warp_kernel<16, true, T>) : go(select_warp_kernel<16, false, T>);
+  if (per <= 32) return a.bias ? go(select_warp_kernel<32, true, T>) : go(select_warp_kernel<32, false, T>);
   static tc::Once once;
   const cudaError_t e = tc::raise_smem(once, select_cta_kernel<T>, 16384 * 8);
   if (e != cudaSuccess) return e;
