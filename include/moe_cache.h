@@ -618,7 +618,7 @@ MOE_API int moe_fp4_global_scale(const void* d_src, int dtype, long long src_str
  * x [n_rows][k] and w [n][k] in the banks moe_fp4_quantize writes (a blob's banks may be passed
  * where they lie), exact products, fp32 sums; out bf16 or fp32, out_stride.
  * wfmt MOE_W_NVFP4 or MOE_W_MXFP4 for both; d_xg, d_wg device global scales
- * (NULL = 1, must be NULL for MXFP4); k a multiple of 32; all four banks
+ * (NULL = 1, must be NULL for MXFP4); scales without sign; k a multiple of 32; all four banks
  * 16-byte aligned.  d_status as moe_route. */
 MOE_API int moe_fp4_linear(int wfmt, const uint8_t* d_x_codes, const uint8_t* d_x_scales,
                            const float* d_xg, const uint8_t* d_w_codes, const uint8_t* d_w_scales,
