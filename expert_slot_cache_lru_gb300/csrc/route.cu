@@ -69,9 +69,30 @@ __device__ __forceinline__ void write_row(const RouteArgs& a, long long b, int l
   }
 }
 
-// `shift`: log2 of the lanes per group; gs: experts per group.  A pick's score is
-// made again from its logit, by the lane that writes it, so that no scores move with
-// the picks.
+// a lane's two largest keys and their places j, the lower place first among equals
+struct Top2 {
+  uint32_t k1, k2;
+  int i1, i2;
+};
+template <int EL>
+__device__ __forceinline__ Top2 top2(const uint32_t (&key)[EL], uint32_t gone) {
+  Top2 t{0u, 0u, 0, 0};
+#pragma unroll
+  for (int j = 0; j < EL; ++j) {
+    const uint32_t k = (gone >> j) & 1 ? 0u : key[j];
+    const bool first = k > t.k1, second = k > t.k2;
+    t.i2 = first ? t.i1 : second ? j : t.i2;
+    t.k2 = first ? t.k1 : second ? k : t.k2;
+    t.i1 = first ? j : t.i1;
+    t.k1 = first ? k : t.k1;
+  }
+  return t;
+}
+
+// `shift`: log2 of the lanes per group; gs: experts per group.  Each lane keeps its two
+// best keys, which serve its first two picks and its group's score; a lane that is
+// picked from twice looks through its keys again.  A pick's score is made again from
+// its logit, by the lane that writes it, so that no scores move with the picks.
 template <int EL, bool BIAS, typename T>
 __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift, int gs) {
   tc::pdl_trigger();
@@ -81,7 +102,7 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
   // lane's experts: first + j * lanes, below end
   const int first = group * gs + (lane & (lanes - 1)), end = (group + 1) * gs;
   const T* zr = static_cast<const T*>(a.logits) + b * a.stride;
-  const bool softmax = a.score == MOE_SCORE_SOFTMAX, two = a.groups > 1 && a.group_top == 2;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   tc::pdl_wait();
   float s[EL];
   uint32_t key[EL];
@@ -101,7 +122,7 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
   for (int j = 0; j < EL; ++j)  // without a bias the logits rank
     key[j] = BIAS ? s[j] > -INFINITY : choice_key(s[j]);
   if (softmax) mx = warp_max(mx);
-  if (softmax || BIAS || two) {
+  if (softmax || BIAS) {
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < EL; ++j) sum += s[j] = raw_score(s[j], softmax, mx);
@@ -117,64 +138,50 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
       }
     }
   }
+  Top2 t = top2(key, 0u);
   if (a.groups > 1) {
-    uint32_t k1 = 0u, k2 = 0u;  // the group's two largest choices
-    float s1 = 0.f, s2 = 0.f;   // without a bias: its two largest scores
-#pragma unroll
-    for (int j = 0; j < EL; ++j) {
-      k2 = max(k2, min(k1, key[j]));
-      k1 = max(k1, key[j]);
-    }
-    if (two && !BIAS) {
-#pragma unroll
-      for (int j = 0; j < EL; ++j) {
-        const float v = key[j] ? s[j] * inv : 0.f;
-        s2 = fmaxf(s2, fminf(s1, v));
-        s1 = fmaxf(s1, v);
-      }
-    }
+    uint32_t k1 = t.k1, k2 = t.k2;  // the group's two largest choices
     for (int o = lanes >> 1; o > 0; o >>= 1) {
       const uint32_t q1 = __shfl_xor_sync(kAll, k1, o), q2 = __shfl_xor_sync(kAll, k2, o);
       k2 = max(min(k1, q1), max(k2, q2));
       k1 = max(k1, q1);
-      if (two && !BIAS) {
-        const float t1 = __shfl_xor_sync(kAll, s1, o), t2 = __shfl_xor_sync(kAll, s2, o);
-        s2 = fmaxf(fminf(s1, t1), fmaxf(s2, t2));
-        s1 = fmaxf(s1, t1);
-      }
     }
     uint32_t mine = k1;
-    if (two && k1) mine = choice_key(BIAS ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
+    if (a.group_top == 2 && k1) {  // their sum, or of their scores
+      float v1 = key_value(k1), v2 = k2 ? key_value(k2) : 0.f;
+      if (!BIAS) {
+        v1 = raw_score(v1, softmax, mx) * inv;
+        v2 = k2 ? raw_score(v2, softmax, mx) * inv : 0.f;
+      }
+      mine = choice_key(v1 + v2);
+    }
     int rank = 0;  // groups ahead of this one
     for (int g = 0; g < a.groups; ++g) {
       const uint32_t other = __shfl_sync(kAll, mine, g << shift);
       rank += other > mine || (other == mine && g < group);
     }
-    if (rank >= a.topk_groups || !mine) {
-#pragma unroll
-      for (int j = 0; j < EL; ++j) key[j] = 0u;
-    }
+    if (rank >= a.topk_groups || !mine) t.k1 = t.k2 = 0u;
   }
-  int my_id = -1;
+  int my_id = -1, left = 2;  // left: best keys at hand
+  uint32_t gone = 0u;        // places picked from
   for (int r = 0; r < a.k; ++r) {
-    uint32_t top = key[0];
-#pragma unroll
-    for (int j = 1; j < EL; ++j) top = max(top, key[j]);
-    const uint32_t best = __reduce_max_sync(kAll, top);
+    const uint32_t best = __reduce_max_sync(kAll, t.k1);
     if (!best) break;
-    // the lane's lowest id that holds the best key; ids grow with j
-    int at = EL;
-    if (top == best) {
-#pragma unroll
-      for (int j = EL - 1; j >= 0; --j)
-        if (key[j] == best) at = j;
-    }
-    const int cand = at < EL ? first + (at << shift) : 0x7fffffff;
-    const int id = __reduce_min_sync(kAll, cand);
+    const int cand = t.k1 == best ? first + (t.i1 << shift) : 0x7fffffff;
+    const int id = __reduce_min_sync(kAll, cand);  // the lowest of its holders
     if (cand == id) {
-#pragma unroll
-      for (int j = 0; j < EL; ++j)
-        if (j == at) key[j] = 0u;
+      gone |= 1u << t.i1;
+      t.k1 = t.k2;
+      t.i1 = t.i2;
+      t.k2 = 0u;
+      --left;
+    }
+    if (__any_sync(kAll, left == 0)) {
+      const Top2 again = top2(key, gone);
+      if (left == 0) {
+        t = again;
+        left = 2;
+      }
     }
     if (lane == r) my_id = id;
   }
