@@ -6,8 +6,8 @@
 // row: 64 bf16 or 256 4-bit elements, four MMAs.  CTAs (or pairs) are persistent
 // and take tiles in turn.  Warps of a CTA:
 //   0..7   epilogue: tensor memory -> registers -> global scales -> out.  Warp w
-//          reads lanes 32 (w % 4) .., half w / 4 of the columns; up to 128 columns two
-//          accumulators alternate, so the next tile's MMAs run beside it;
+//          reads lanes 32 (w % 4) .., half w / 4 of the columns; 4-bit kinds alternate
+//          two accumulators, so the next tile's MMAs run beside it;
 //   8..15  block scales (4-bit kinds), shared memory -> tensor memory in the order
 //          the MMA reads, two groups of four warps on alternate stages (one group alone
 //          left the MMAs of an 8,192 x 8,192 x 4,096 product waiting: 150 us).
@@ -17,8 +17,8 @@
 //          where the banks' rows are whole 16-byte pieces, else per-thread copies (which cost
 //          a cycle and more per row and 16 bytes: 550 a stage of 128 + 192 rows);
 //   then   one warp of TMA loads of the operands, one of MMAs (the first CTA's of a pair).
-// A pair halves what each SM takes in of Q, the bound of a lone CTA's 128 x 256
-// tile (48 KB a stage at about 52 bytes per cycle).
+// A pair halves what each SM takes in of Q: an SM takes in about 64 bytes per
+// cycle, which bounds the bf16 tiles and a lone CTA's 4-bit ones.
 // Scale order: the 32-bit word of row r and K step j belongs in lane r % 32 of
 // every warp's quarter, column r / 32 of block j.  NVFP4: a word is the four
 // scales of one 64-element step; MXFP4: the two scales of two steps, picked by

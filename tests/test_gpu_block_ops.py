@@ -283,6 +283,23 @@ def test_route(m, B, H, E, k, pad):
     assert (np.abs(f64(w) - want_w)[same] <= 64 * U * np.abs(want_w)[same] + 1e-37).all()
 
 
+@pytest.mark.parametrize("B,H,E", [(20500, 256, 256), (40000, 128, 100), (30001, 72, 64), (20000, 512, 700)])
+def test_route_more_tiles_than_sms(m, B, H, E):
+    """Every logit of products whose CTAs take several tiles each, and each row's best expert."""
+    r = np.random.default_rng([B, H, E])
+    x = dev(r.normal(0, 1, (B, H)), torch.bfloat16)
+    wr = dev(r.normal(0, H ** -0.5, (E, H)), torch.bfloat16)
+    z = torch.full((B, E), float("nan"), device="cuda")
+    ids = torch.empty(B, 1, dtype=torch.int32, device="cuda")
+    w = torch.empty(B, 1, device="cuda")
+    m.moe_route(x, wr, None, B, H, E, 1, z, ids, w, renorm=False)
+    want = x.double() @ wr.double().T
+    assert ((z.double() - want).abs() <= (H / 16 + 40) * 2 * U * (x.double().abs() @ wr.double().abs().T)).all()
+    assert torch.equal(z.gather(1, ids.long()), z.max(1, keepdim=True).values)
+    p = torch.softmax(z.double(), 1).gather(1, ids.long())
+    assert ((w.double() - p).abs() <= 64 * U * p).all()
+
+
 def test_route_twice_the_same_and_in_a_graph(m):
     r = np.random.default_rng(5)
     for B, H, E, k in [(1, 2048, 256, 8), (40, 2048, 256, 8), (600, 2048, 1024, 2)]:
@@ -420,7 +437,7 @@ LINEAR = [(1, 16, 32), (1, 130, 64), (1, 4096, 2048), (2, 1000, 512), (5, 257, 2
           (16, 2048, 96), (17, 384, 1024), (33, 4097, 256), (64, 1536, 2048), (100, 640, 288),
           (128, 128, 256), (129, 255, 2080), (200, 2048, 512), (255, 300, 320), (256, 256, 4096),
           (600, 1536, 2048), (513, 1030, 544), (1000, 8, 64), (2048, 2048, 2048), (1930, 2000, 544),
-          (700, 7001, 96)]
+          (700, 7001, 96), (5000, 5000, 160), (20, 70000, 64), (3000, 2500, 64)]
 
 
 def linear_case(m, nv, B, N, K, dtype, pad=0, seed=0, g=True):
