@@ -1,9 +1,11 @@
 // fp4_linear.cu -- the product of two 4-bit matrices (formulas in moe_cache.h):
 // block-scaled tcgen05 MMAs over packed e2m1, tile_gemm.cuh.
 //
-// With up to 64 tokens P are the weights and Q the tokens (NT = 16, 32 or 64:
-// the weights stream from HBM once, and an MMA costs no more than its Q rows);
-// with more, P are the tokens and Q the weights.
+// P are the tokens and Q the weights, or, with up to 64 tokens, the other way round
+// (NT = 16, 32 or 64: a tile's MMAs cost no more than its Q rows): the tile is the one
+// estimated to take least.  The weights as P where their 128-row tiles fill the SMs
+// (64 x 70,000 x 2,048: 17.2 us, as Q 21.8) or K is long enough to split (32 x 4,096 x
+// 4,096: 6.6 and 8.0), as Q between (64 x 8,192 x 2,048: 5.9 us, as P 8.3).
 #include "block_ops.cuh"
 #include "tile_gemm.cuh"
 
@@ -12,7 +14,15 @@ namespace {
 
 template <tg::Kind KIND>
 cudaError_t by_rows(const Fp4Linear& l, int sms, cudaStream_t s) {
-  const bool swap = l.rows <= 64;
+  const long long c64 = tg::cycles<KIND, 64, 1>(l.rows, l.n, l.k, sms),
+                  c128 = tg::cycles<KIND, 128, 1>(l.rows, l.n, l.k, sms),
+                  c192 = tg::cycles<KIND, 192, 2>(l.rows, l.n, l.k, sms);
+  long long best = c64 < c128 ? c64 : c128;
+  best = c192 < best ? c192 : best;
+  const long long turned = l.rows <= 16   ? tg::cycles<KIND, 16, 1>(l.n, l.rows, l.k, sms)
+                           : l.rows <= 32 ? tg::cycles<KIND, 32, 1>(l.n, l.rows, l.k, sms)
+                                          : tg::cycles<KIND, 64, 1>(l.n, l.rows, l.k, sms);
+  const bool swap = l.rows <= 64 && turned <= best;
   tg::Problem p{};
   p.p = swap ? l.wc : l.xc;
   p.q = swap ? l.xc : l.wc;
@@ -28,15 +38,13 @@ cudaError_t by_rows(const Fp4Linear& l, int sms, cudaStream_t s) {
   p.out_stride = l.out_stride;
   p.f32 = l.f32;
   p.status = l.status;
-  if (l.rows <= 16) return tg::launch<KIND, 16, 1, true>(p, sms, s);
-  if (l.rows <= 32) return tg::launch<KIND, 32, 1, true>(p, sms, s);
-  if (l.rows <= 64) return tg::launch<KIND, 64, 1, true>(p, sms, s);
-  // the tile estimated to take least
-  const long long c64 = tg::cycles<KIND, 64, 1>(l.rows, l.n, l.k, sms),
-                  c128 = tg::cycles<KIND, 128, 1>(l.rows, l.n, l.k, sms),
-                  c192 = tg::cycles<KIND, 192, 2>(l.rows, l.n, l.k, sms);
-  if (c192 <= c128 && c192 <= c64) return tg::launch<KIND, 192, 2, false>(p, sms, s);
-  if (c128 <= c64) return tg::launch<KIND, 128, 1, false>(p, sms, s);
+  if (swap) {
+    if (l.rows <= 16) return tg::launch<KIND, 16, 1, true>(p, sms, s);
+    if (l.rows <= 32) return tg::launch<KIND, 32, 1, true>(p, sms, s);
+    return tg::launch<KIND, 64, 1, true>(p, sms, s);
+  }
+  if (c192 == best) return tg::launch<KIND, 192, 2, false>(p, sms, s);
+  if (c128 == best) return tg::launch<KIND, 128, 1, false>(p, sms, s);
   return tg::launch<KIND, 64, 1, false>(p, sms, s);
 }
 

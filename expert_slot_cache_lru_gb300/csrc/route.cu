@@ -10,7 +10,8 @@
 // than 32 experts per lane take one CTA per row with the keys in shared memory.
 //
 // Logits: up to kDotRows rows are dot products, one CTA per expert (its router row
-// read once for all rows); more rows are a product on the tensor cores (tile_gemm.cuh),
+// read once for all rows; with the selection 6.3 us for 8 rows x 2,048 x 256 and 9.4
+// for 16, on the tensor cores 8.3 and 8.5); more rows are a product on the tensor cores (tile_gemm.cuh),
 // whose operands must start on 16 bytes; other layouts take tile_dot.cuh.  The selection
 // is a second launch that starts while the logits are computed and waits for them.
 #include "block_ops.cuh"

@@ -437,7 +437,8 @@ LINEAR = [(1, 16, 32), (1, 130, 64), (1, 4096, 2048), (2, 1000, 512), (5, 257, 2
           (16, 2048, 96), (17, 384, 1024), (33, 4097, 256), (64, 1536, 2048), (100, 640, 288),
           (128, 128, 256), (129, 255, 2080), (200, 2048, 512), (255, 300, 320), (256, 256, 4096),
           (600, 1536, 2048), (513, 1030, 544), (1000, 8, 64), (2048, 2048, 2048), (1930, 2000, 544),
-          (700, 7001, 96), (5000, 5000, 160), (20, 70000, 64), (3000, 2500, 64)]
+          (700, 7001, 96), (5000, 5000, 160), (20, 70000, 64), (3000, 2500, 64),
+          (40, 20000, 320), (64, 19500, 512)]
 
 
 def linear_case(m, nv, B, N, K, dtype, pad=0, seed=0, g=True):
