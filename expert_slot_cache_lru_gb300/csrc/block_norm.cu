@@ -10,8 +10,9 @@
 // memory (cp.async), so loads stay in flight across the two sums of a row; what a thread
 // reads it has copied itself, so the ring needs no barrier.  The arithmetic is on
 // pairs of floats: issue slots come second to memory.
-// row_kernel, everything else: one CTA per row, N pieces of VEC elements per thread,
-// T pieces apart (VEC = 8 for aligned rows, 1 for other layouts).
+// row_kernel: one CTA per row, N pieces of VEC elements per thread, T pieces apart (VEC
+// = 8 for aligned rows, 1 for layouts nothing else takes).
+// flat_kernel: rows without gaps that are not whole 16-byte pieces, in aligned pieces.
 // Measured, ring / row: 8,192 x 4,096 bf16 with a gate per channel 43.9 us (6.1 TB/s) /
 // 56.9; 8,192 x 2,048 bf16 with a gate per row 28.9 / 32.6; but with an fp32 residual, whose
 // rows put half as many bytes again in flight, 40.8 / 31.2 (6.5 TB/s) for 8,192 x 2,048
@@ -310,6 +311,131 @@ row_kernel(NormArgs a) {
     }
 }
 
+// 8 bf16 that start S elements before the second of two neighbouring words
+template <int S>
+__device__ __forceinline__ uint4 join(uint4 a, uint4 b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = (8 - S) / 2 + i;
+    o[i] = S & 1 ? __funnelshift_r(w[k], w[k + 1 < 8 ? k + 1 : 7], 16) : w[k];
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Rows without gaps that are not whole 16-byte pieces: the matrices are taken as flat
+// arrays in aligned pieces of 8, of which a row's first and last may be shared with
+// its neighbours; every array is `off` = row * hidden % 8 elements off the weights,
+// which are read as two pieces and shifted.  One piece per thread, 32 registers: a few
+// spills cost less than half the threads (8,192 x 4,095 bf16 with a gate 87 us, 107 with
+// 44 registers, 126 element by element in row_kernel).
+template <typename R, int GATE>
+__global__ void __launch_bounds__(1024, 2) flat_kernel(NormArgs a) {
+  __shared__ float red[2][32];
+  tc::pdl_trigger();
+  tc::pdl_wait();
+  const int H = a.hidden, tid = threadIdx.x;
+  const long long o = (long long)blockIdx.x * H, at = ((o >> 3) + tid) * 8;
+  const int off = (int)(o & 7);
+  // elements lo .. hi - 1 of this piece are the row's
+  const int lo = tid == 0 ? off : 0, hi = (int)min(8LL, max(0LL, o + H - at));
+  const bool mine = lo < hi, whole = at + 8 <= (long long)a.rows * H;
+  const float inv_h = 1.f / (float)H;
+  auto read = [&](auto* p, Piece<8>& v) {
+    if (mine && whole) {
+      load<8>(p + at, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v.v[j] = j >= lo && j < hi ? v.v[j] : 0.f;
+    } else {  // past the last row there may be no more memory
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        Piece<1> e{{0.f}};
+        if (j >= lo && j < hi) load<1>(p + at + j, e);
+        v.v[j] = e.v[0];
+      }
+    }
+  };
+  auto write = [&](auto* p, const Piece<8>& v) {
+    if (lo == 0 && hi == 8) {
+      store<8>(p + at, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const Piece<1> e{{v.v[j]}};
+        if (j >= lo && j < hi) store<1>(p + at + j, e);
+      }
+    }
+  };
+  // the weights of this piece: elements 8 tid - off ..
+  auto weights = [&](const B* p, Piece<8>& v) {
+    if (tid > 0 && 8 * tid + 8 <= H) {
+      const uint4 hi_w = __ldg(reinterpret_cast<const uint4*>(p) + tid);
+      const uint4 lo_w = off ? __ldg(reinterpret_cast<const uint4*>(p) + tid - 1) : hi_w;
+      uint4 q = hi_w;
+      switch (off) {
+        case 1: q = join<1>(lo_w, hi_w); break;
+        case 2: q = join<2>(lo_w, hi_w); break;
+        case 3: q = join<3>(lo_w, hi_w); break;
+        case 4: q = join<4>(lo_w, hi_w); break;
+        case 5: q = join<5>(lo_w, hi_w); break;
+        case 6: q = join<6>(lo_w, hi_w); break;
+        case 7: q = join<7>(lo_w, hi_w); break;
+      }
+      load<8>(reinterpret_cast<const B*>(&q), v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        Piece<1> e{{0.f}};
+        if (j >= lo && j < hi) load<1>(p + 8 * tid - off + j, e);
+        v.v[j] = e.v[0];
+      }
+    }
+  };
+  Piece<8> h, z, w;
+  read(static_cast<const R*>(a.h), h);
+  if (a.y) {
+    read(a.y, z);
+    float inv = 1.f;
+    if (a.post_w) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fmaf(z.v[j], z.v[j], s);
+      inv = rsqrtf(cta_sum(s, red[0]) * inv_h + a.eps);
+      weights(a.post_w, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z.v[j] *= inv * (a.w_offset + w.v[j]);
+    }
+    if (GATE != MOE_GATE_NONE) {
+      if (a.gate_stride) read(a.gate, w);
+      else weights(a.gate, w);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h.v[j] = fmaf(a.alpha, gated<GATE>(z.v[j], w.v[j]), h.v[j]);
+  }
+  if (a.h_out) write(static_cast<R*>(a.h_out), h);
+  if (!a.pre_w) return;
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s = j >= lo && j < hi ? fmaf(h.v[j], h.v[j], s) : s;
+  const float inv = rsqrtf(cta_sum(s, red[1]) * inv_h + a.eps);
+  weights(a.pre_w, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w.v[j] = h.v[j] * inv * (a.w_offset + w.v[j]);
+  write(a.x_out, w);
+}
+
+// flat_kernel's layouts: no gaps, every array 16-byte aligned, at most 1,024 pieces a row
+bool flat(const NormArgs& a) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.h) | reinterpret_cast<uintptr_t>(a.h_out) |
+                        reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.post_w) |
+                        reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.pre_w) |
+                        reinterpret_cast<uintptr_t>(a.x_out);
+  const long long H = a.hidden;
+  return a.h_stride == H && (!a.y || a.y_stride == H) && (!a.gate_stride || a.gate_stride == H) &&
+         (!a.h_out || a.ho_stride == H) && (!a.x_out || a.xo_stride == H) && (all & 15) == 0 && H <= 8176;
+}
+
 // every row of every operand starts on a VEC = 8 boundary
 template <typename R>
 bool vectors(const NormArgs& a) {
@@ -329,6 +455,7 @@ cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
   };
   if (vectors<R>(a))
     return a.hidden <= 8192 ? go(row_kernel<R, 8, 1, GATE>, a.hidden / 8, 1) : go(row_kernel<R, 8, 4, GATE>, a.hidden / 8, 4);
+  if (flat(a)) return go(flat_kernel<R, GATE>, a.hidden / 8 + 2, 1);
   if (a.hidden <= 1024) return go(row_kernel<R, 1, 4, GATE>, a.hidden, 4);
   if (a.hidden <= 4096) return go(row_kernel<R, 1, 8, GATE>, a.hidden, 8);
   if (a.hidden <= 8192) return go(row_kernel<R, 1, 16, GATE>, a.hidden, 16);

@@ -110,7 +110,8 @@ def test_norm_many_rows(m):
     dict(alias=True), dict(alias=True, gate="sigmoid_rows"), dict(gate="sigmoid", offset=1.0, alpha=0.3),
     dict(gate="linear", post=False), dict(y=False), dict(pre=False, gate="linear_rows"),
     dict(h_out=False, pad=8), dict(res="f32", alias=True, gate="linear_rows")])
-@pytest.mark.parametrize("B,H", [(1300, 2048), (500, 8192), (5001, 520), (700, 4104)])
+@pytest.mark.parametrize("B,H", [(1300, 2048), (500, 8192), (5001, 520), (700, 4104), (33, 2047), (19, 8175),
+                                 (50, 1002), (9, 13), (17, 8177)])
 def test_norm_more_rows_than_fit_at_once(m, kw, B, H):
     norm_case(m, B, H, **kw)
 
