@@ -101,20 +101,6 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
-// `n` bytes of a 16, 8 or 4-byte piece, the rest zeros; counted by the thread's next
-// cp_async_arrive, which arrives at `b` once they are in place.
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int piece, int n) {
-  if (piece == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else if (piece == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t* b) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(b)) : "memory");
-}
-
 // A tile from shared memory to the matrix of `map`, clipped at its edges; commit, and
 // waits of the thread that issued it: until all but N copies have been read, or
 // are done.

@@ -14,8 +14,8 @@
 //          (tcgen05.cp would copy them too, but measured 52 cycles per 512 bytes in
 //          series with the MMAs.)
 //   16..19 block scales, global -> shared memory, 64 bytes of a row at a time: TMA
-//          where the banks' rows are whole 16-byte pieces, else per-thread copies (which cost
-//          a cycle and more per row and 16 bytes: 550 a stage of 128 + 192 rows);
+//          where the banks' rows are whole 16-byte pieces (K a multiple of 256 or 512),
+//          else aligned loads, shifted;
 //   then   one warp of TMA loads of the operands, one of MMAs (the first CTA's of a pair).
 // A pair halves what each SM takes in of Q: an SM takes in about 64 bytes per
 // cycle, which bounds the bf16 tiles and a lone CTA's 4-bit ones.
@@ -84,7 +84,7 @@ struct Args {
   int tiles_p, tiles_q;
   int nk;                  // stages of K
   int sb;                  // scale bytes per row
-  int piece;               // bytes a row's scales are copied in: 16, 8, 4 or 1
+  int tma_scales;          // the scale banks' rows are whole 16-byte pieces
   int split;               // parts of K
   const float *g0, *g1;
   void* out;
@@ -110,29 +110,67 @@ __device__ __forceinline__ void tile_at(const Args& a, int t, int& tp, int& tq) 
   tq = r / n;
 }
 
-// 16 bytes of a row's scales in smaller pieces, zeros beyond the row
-static __device__ __noinline__ void copy_ragged(uint32_t dst, const uint8_t* row, int off, int sb, int piece) {
-  if (piece > 1) {
-    for (int o = 0; o < 16; o += piece) {
-      const bool in = off + o < sb;
-      cp_async(dst + o, row + (in ? off + o : 0), piece, in ? piece : 0);
-    }
-    return;
-  }
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w = 0;
-    for (int j = 0; j < 4; ++j)
-      if (off + 4 * i + j < sb) w |= (uint32_t)__ldg(row + off + 4 * i + j) << (8 * j);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4 * i), "r"(w) : "memory");
-  }
+// 16 aligned bytes of a bank of `bytes` bytes (nothing past its end is read)
+__device__ __forceinline__ uint4 bank_word(const uint8_t* bank, long long bytes, long long word) {
+  if ((word + 1) * 16 <= bytes) return __ldg(reinterpret_cast<const uint4*>(bank) + word);
+  uint32_t w[4] = {0, 0, 0, 0};
+  for (int j = 0; j < 16 && word * 16 + j < bytes; ++j)
+    w[j >> 2] |= (uint32_t)__ldg(bank + word * 16 + j) << (8 * (j & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// bytes off .. off + 15 of a row's scales (row null: zeros)
-__device__ __forceinline__ void copy_scales(uint32_t dst, const uint8_t* row, int off, const Args& a) {
-  if (a.piece == 16 || !row) {
-    const bool in = row && off < a.sb;
-    cp_async(dst, in ? row + off : a.ps, 16, in ? 16 : 0);
-  } else {
-    copy_ragged(dst, row, off, a.sb, a.piece);
+// bytes sh .. sh + 15 of two neighbouring words, those from `n` on zero
+__device__ __forceinline__ uint4 cut(uint4 a, uint4 b, int sh, int n) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (sh & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (sh & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = __funnelshift_r(w[i], w[i + 1], 8 * (sh & 3));
+    const int left = n - 4 * i;  // bytes to keep
+    o[i] = left >= 4 ? o[i] : left <= 0 ? 0u : o[i] & (0xffffffffu >> (32 - 8 * left));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// A group of block scales of a tile into shared memory where the banks' rows are not
+// whole 16-byte pieces: 64 bytes from `off` of 128 P rows and NT Q rows, zeros beyond the
+// matrix, in the 64-byte swizzle of a TMA copy.  128 threads, four per row; U rows'
+// loads in flight per thread.
+template <int NT>
+__device__ __forceinline__ void copy_rows(const Args& a, uint8_t* dst, int p_row, int q_row, int off, int tid) {
+  constexpr int U = 4;
+  const int chunk = tid & 3, at = off + 16 * chunk, n = min(16, a.sb - at);
+  const long long p_bytes = (long long)a.p_rows * a.sb, q_bytes = (long long)a.q_rows * a.sb;
+#pragma unroll 1
+  for (int r0 = tid >> 2; r0 < 128 + NT; r0 += 32 * U) {
+    uint4 w0[U], w1[U];
+    int sh[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + 32 * u;
+      const bool is_p = r < 128;
+      const long long row = is_p ? (long long)p_row + r : (long long)q_row + r - 128;
+      const uint8_t* bank = is_p ? a.ps : a.qs;
+      const long long bytes = is_p ? p_bytes : q_bytes, byte = row * a.sb + at;
+      w0[u] = w1[u] = make_uint4(0, 0, 0, 0);
+      sh[u] = (int)(byte & 15);
+      if (r < 128 + NT && row < (is_p ? a.p_rows : a.q_rows) && n > 0) {
+        w0[u] = bank_word(bank, bytes, byte >> 4);
+        if (sh[u] + n > 16) w1[u] = bank_word(bank, bytes, (byte >> 4) + 1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + 32 * u;
+      if (r < 128 + NT)
+        *reinterpret_cast<uint4*>(dst + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4)) = cut(w0[u], w1[u], sh[u], n);
+    }
   }
 }
 
@@ -281,7 +319,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     }
     for (int i = 0; i < 4; ++i) mbar_init(&c.scaled[i], 4 * CG);
     for (int i = 0; i < kGroups; ++i) {
-      mbar_init(&c.rows_full[i], a.piece == 16 ? 1 : 128);
+      mbar_init(&c.rows_full[i], a.tma_scales ? 1 : 128);
       mbar_init(&c.rows_empty[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
@@ -389,7 +427,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     __syncwarp();
   } else if (warp >= kCopyWarp) {
     if constexpr (T::kBlocks > 0) {
-      const int n_warps = a.piece == 16 ? 1 : 4;  // one lane of TMA, or all 128 threads
+      const int n_warps = a.tma_scales ? 1 : 4;  // one lane of TMA, or all 128 threads
       unsigned group = 0;
       bool ok = warp - kCopyWarp < n_warps;
       for (int t = tile0; t < n_tiles && ok; t += step) {
@@ -406,7 +444,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
           }
           const int off = ks * (16 / T::kPer);
           uint8_t* dst = sstg + slot * T::kSlot;
-          if (a.piece == 16) {
+          if (a.tma_scales) {
             if (elect_one()) {
               mbar_expect(&c.rows_full[slot], (128 + NT) * 64);
               tma_load<1>(dst, &psmap, off, p_row, sa(&c.rows_full[slot]));
@@ -414,25 +452,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
             }
             __syncwarp();
           } else {
-            const int tid = threadIdx.x - 32 * kCopyWarp, chunk = tid & 3;
-            for (int r = tid >> 2; r < 128 + NT; r += 32) {
-              const long long row = r < 128 ? (long long)p_row + r : (long long)q_row + r - 128;
-              const bool in = row < (r < 128 ? a.p_rows : a.q_rows);
-              const uint8_t* src = in ? (r < 128 ? a.ps : a.qs) + row * a.sb : nullptr;
-              // the TMA's 64-byte swizzle
-              copy_scales(sa(dst) + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4), src, off + 16 * chunk, a);
-            }
-            if (a.piece > 1) {
-              cp_async_arrive(&c.rows_full[slot]);
-            } else {  // plain stores beside the copies of rows outside the matrix
-              asm volatile("cp.async.wait_all;" ::: "memory");
-              mbar_arrive(&c.rows_full[slot]);
-            }
+            copy_rows<NT>(a, dst, p_row, q_row, off, threadIdx.x - 32 * kCopyWarp);
+            mbar_arrive(&c.rows_full[slot]);
           }
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (!ok && warp == kCopyWarp && a.piece == 16)  // copies in flight land before the CTA ends
+      if (!ok && warp == kCopyWarp && a.tma_scales)  // copies in flight land before the CTA ends
         for (unsigned i = group > kGroups ? group - kGroups : 0; i < group; ++i)
           drain_bar(&c.rows_full[i % kGroups], (i / kGroups) & 1);
     }
@@ -701,7 +726,7 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   const int slab = KIND == kBf16 ? 64 : 256;
   a.nk = (l.k + slab - 1) / slab;
   a.sb = KIND == kBf16 ? 0 : l.k / (KIND == kNv ? 16 : 32);
-  a.piece = a.sb % 16 == 0 ? 16 : a.sb % 8 == 0 ? 8 : a.sb % 4 == 0 ? 4 : 1;
+  a.tma_scales = a.sb % 16 == 0;
   a.g0 = l.g0;
   a.g1 = l.g1;
   a.out = l.out;
@@ -718,7 +743,7 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   const long long width = KIND == kBf16 ? l.k : l.k / 2;
   e = make_map(&pm, l.p, elem, width, l.p_rows, l.p_stride, 128);
   if (e == cudaSuccess) e = make_map(&qm, l.q, elem, width, l.q_rows, l.q_stride, T::kQ);
-  if (T::kBlocks && a.piece == 16) {
+  if (T::kBlocks && a.tma_scales) {
     if (e == cudaSuccess) e = make_scale_map(&psm, l.ps, a.sb, l.p_rows, 128);
     if (e == cudaSuccess) e = make_scale_map(&qsm, l.qs, a.sb, l.q_rows, NT);
   }
