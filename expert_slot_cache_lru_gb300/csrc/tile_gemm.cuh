@@ -13,7 +13,7 @@
 //          left the MMAs of an 8,192 x 8,192 x 4,096 product waiting: 150 us).
 //          (tcgen05.cp would copy them too, but measured 52 cycles per 512 bytes in
 //          series with the MMAs.)
-//   16..19 block scales, global -> shared memory, 64 bytes of a row at a time: TMA
+//   16..23 block scales, global -> shared memory, 64 bytes of a row at a time: TMA
 //          where the banks' rows are whole 16-byte pieces (K a multiple of 256 or 512),
 //          else aligned loads, shifted;
 //   then   one warp of TMA loads of the operands, one of MMAs (the first CTA's of a pair).
@@ -51,7 +51,7 @@ template <Kind KIND, int NT, int CG>
 struct Shape {
   static constexpr int kQ = NT / CG;                          // Q rows a CTA loads
   static constexpr int kBlocks = KIND == kNv ? 4 : KIND == kMx ? 2 : 0;  // scale words per row and stage
-  static constexpr int kTmaWarp = kBlocks ? 20 : kEpiWarps, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kTmaWarp = kBlocks ? 24 : kEpiWarps, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   static constexpr int kPer = KIND == kMx ? 2 : 1;            // stages in 16 bytes of a row's scales
   static constexpr int kGroupStages = 4 * kPer;
@@ -110,9 +110,8 @@ __device__ __forceinline__ void tile_at(const Args& a, int t, int& tp, int& tq) 
   tq = r / n;
 }
 
-// 16 aligned bytes of a bank of `bytes` bytes (nothing past its end is read)
-__device__ __forceinline__ uint4 bank_word(const uint8_t* bank, long long bytes, long long word) {
-  if ((word + 1) * 16 <= bytes) return __ldg(reinterpret_cast<const uint4*>(bank) + word);
+// 16 aligned bytes at the end of a bank of `bytes` bytes (nothing past it is read)
+static __device__ __noinline__ uint4 bank_word(const uint8_t* bank, long long bytes, long long word) {
   uint32_t w[4] = {0, 0, 0, 0};
   for (int j = 0; j < 16 && word * 16 + j < bytes; ++j)
     w[j >> 2] |= (uint32_t)__ldg(bank + word * 16 + j) << (8 * (j & 3));
@@ -140,37 +139,37 @@ __device__ __forceinline__ uint4 cut(uint4 a, uint4 b, int sh, int n) {
 }
 // A group of block scales of a tile into shared memory where the banks' rows are not
 // whole 16-byte pieces: 64 bytes from `off` of 128 P rows and NT Q rows, zeros beyond the
-// matrix, in the 64-byte swizzle of a TMA copy.  128 threads, four per row; U rows'
-// loads in flight per thread.
+// matrix, in the 64-byte swizzle of a TMA copy.  256 threads, four per row, all of a
+// thread's loads in flight at once.
 template <int NT>
 __device__ __forceinline__ void copy_rows(const Args& a, uint8_t* dst, int p_row, int q_row, int off, int tid) {
-  constexpr int U = 4;
-  const int chunk = tid & 3, at = off + 16 * chunk, n = min(16, a.sb - at);
-  const long long p_bytes = (long long)a.p_rows * a.sb, q_bytes = (long long)a.q_rows * a.sb;
-#pragma unroll 1
-  for (int r0 = tid >> 2; r0 < 128 + NT; r0 += 32 * U) {
-    uint4 w0[U], w1[U];
-    int sh[U];
+  constexpr int PR = 2, QR = (NT + 63) / 64;  // rows per thread, 64 apart
+  const int chunk = tid & 3, at = off + 16 * chunk, n = min(16, a.sb - at), r0 = tid >> 2;
+  uint4 w0[PR + QR], w1[PR + QR];
+  int sh[PR + QR];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + 32 * u;
-      const bool is_p = r < 128;
-      const long long row = is_p ? (long long)p_row + r : (long long)q_row + r - 128;
-      const uint8_t* bank = is_p ? a.ps : a.qs;
-      const long long bytes = is_p ? p_bytes : q_bytes, byte = row * a.sb + at;
-      w0[u] = w1[u] = make_uint4(0, 0, 0, 0);
-      sh[u] = (int)(byte & 15);
-      if (r < 128 + NT && row < (is_p ? a.p_rows : a.q_rows) && n > 0) {
+  for (int u = 0; u < PR + QR; ++u) {
+    const bool is_p = u < PR;
+    const int rows = is_p ? a.p_rows : a.q_rows, row = (is_p ? p_row + 64 * u : q_row + 64 * (u - PR)) + r0;
+    const uint8_t* bank = is_p ? a.ps : a.qs;
+    const long long bytes = (long long)rows * a.sb, byte = (long long)row * a.sb + at;
+    w0[u] = w1[u] = make_uint4(0, 0, 0, 0);
+    sh[u] = (int)(byte & 15);
+    if (row < rows && n > 0 && (is_p || r0 + 64 * (u - PR) < NT)) {
+      if (((byte >> 4) + 2) * 16 <= bytes) {  // else at the bank's end
+        w0[u] = __ldg(reinterpret_cast<const uint4*>(bank) + (byte >> 4));
+        w1[u] = __ldg(reinterpret_cast<const uint4*>(bank) + (byte >> 4) + 1);
+      } else {
         w0[u] = bank_word(bank, bytes, byte >> 4);
-        if (sh[u] + n > 16) w1[u] = bank_word(bank, bytes, (byte >> 4) + 1);
+        w1[u] = bank_word(bank, bytes, (byte >> 4) + 1);
       }
     }
+  }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + 32 * u;
-      if (r < 128 + NT)
-        *reinterpret_cast<uint4*>(dst + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4)) = cut(w0[u], w1[u], sh[u], n);
-    }
+  for (int u = 0; u < PR + QR; ++u) {
+    const int r = u < PR ? r0 + 64 * u : 128 + r0 + 64 * (u - PR);
+    if (r < 128 + NT)
+      *reinterpret_cast<uint4*>(dst + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4)) = cut(w0[u], w1[u], sh[u], n);
   }
 }
 
@@ -319,7 +318,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     }
     for (int i = 0; i < 4; ++i) mbar_init(&c.scaled[i], 4 * CG);
     for (int i = 0; i < kGroups; ++i) {
-      mbar_init(&c.rows_full[i], a.tma_scales ? 1 : 128);
+      mbar_init(&c.rows_full[i], a.tma_scales ? 1 : 256);
       mbar_init(&c.rows_empty[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
@@ -427,7 +426,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     __syncwarp();
   } else if (warp >= kCopyWarp) {
     if constexpr (T::kBlocks > 0) {
-      const int n_warps = a.tma_scales ? 1 : 4;  // one lane of TMA, or all 128 threads
+      const int n_warps = a.tma_scales ? 1 : 8;  // one lane of TMA, or all 256 threads
       unsigned group = 0;
       bool ok = warp - kCopyWarp < n_warps;
       for (int t = tile0; t < n_tiles && ok; t += step) {
