@@ -139,14 +139,20 @@ __device__ __forceinline__ uint4 cut(uint4 a, uint4 b, int sh, int n) {
 }
 // A group of block scales of a tile into shared memory where the banks' rows are not
 // whole 16-byte pieces: 64 bytes from `off` of 128 P rows and NT Q rows, zeros beyond the
-// matrix, in the 64-byte swizzle of a TMA copy.  256 threads, four per row, all of a
-// thread's loads in flight at once.
+// matrix, in the 64-byte swizzle of a TMA copy.  256 threads, four per row; the loads
+// wait in registers for the slot they go to.
 template <int NT>
-__device__ __forceinline__ void copy_rows(const Args& a, uint8_t* dst, int p_row, int q_row, int off, int tid) {
-  constexpr int PR = 2, QR = (NT + 63) / 64;  // rows per thread, 64 apart
-  const int chunk = tid & 3, at = off + 16 * chunk, n = min(16, a.sb - at), r0 = tid >> 2;
+struct ScaleRows {
+  static constexpr int PR = 2, QR = (NT + 63) / 64;  // rows per thread, 64 apart
   uint4 w0[PR + QR], w1[PR + QR];
-  int sh[PR + QR];
+  int sh[PR + QR], n;
+  __device__ __forceinline__ void load(const Args& a, int p_row, int q_row, int off, int tid);
+  __device__ __forceinline__ void store(uint8_t* dst, int tid) const;
+};
+template <int NT>
+__device__ __forceinline__ void ScaleRows<NT>::load(const Args& a, int p_row, int q_row, int off, int tid) {
+  const int at = off + 16 * (tid & 3), r0 = tid >> 2;
+  n = min(16, a.sb - at);
 #pragma unroll
   for (int u = 0; u < PR + QR; ++u) {
     const bool is_p = u < PR;
@@ -165,6 +171,10 @@ __device__ __forceinline__ void copy_rows(const Args& a, uint8_t* dst, int p_row
       }
     }
   }
+}
+template <int NT>
+__device__ __forceinline__ void ScaleRows<NT>::store(uint8_t* dst, int tid) const {
+  const int chunk = tid & 3, r0 = tid >> 2;
 #pragma unroll
   for (int u = 0; u < PR + QR; ++u) {
     const int r = u < PR ? r0 + 64 * u : 128 + r0 + 64 * (u - PR);
@@ -436,12 +446,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         // groups start at the first stage of the tile's part of K
         for (int ks = k_lo; ks < k_hi; ks += T::kGroupStages, ++group) {
           const unsigned slot = group % kGroups;
+          const int off = ks * (16 / T::kPer), tid = threadIdx.x - 32 * kCopyWarp;
+          ScaleRows<NT> rows;
+          if (!a.tma_scales) rows.load(a, p_row, q_row, off, tid);
           if (group >= kGroups && !warp_wait(&c.rows_empty[slot], (group / kGroups - 1) & 1,
                                              &c.abort_flag, a.status)) {
             ok = false;
             break;
           }
-          const int off = ks * (16 / T::kPer);
           uint8_t* dst = sstg + slot * T::kSlot;
           if (a.tma_scales) {
             if (elect_one()) {
@@ -451,7 +463,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
             }
             __syncwarp();
           } else {
-            copy_rows<NT>(a, dst, p_row, q_row, off, threadIdx.x - 32 * kCopyWarp);
+            rows.store(dst, tid);
             mbar_arrive(&c.rows_full[slot]);
           }
         }
