@@ -597,10 +597,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
             if (lane == 0 && p < a.p_rows) tma_store(&omap, o, (int)q0, (int)p);
             ++piece;
           }
-        } else if (p < a.p_rows) {
+        } else {  // other row lengths: turned in shared memory, so that a row's lanes are neighbours
+          if constexpr (!SWAP) {
+            float* o = reinterpret_cast<float*>(ostg + warp * 4096);
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < W; ++i)
-            if (i < nq) store_one(a, p * a.out_stride + q0 + i, __uint_as_float(v[i]) * g);
+            for (int i = 0; i < W; ++i) o[lane * 32 + (i ^ lane)] = __uint_as_float(v[i]) * g;
+            __syncwarp();
+            const int rows = (int)min(32LL, a.p_rows - (p - lane));
+            for (int r = 0; r < rows; ++r)
+              if (lane < nq) store_one(a, (p - lane + r) * a.out_stride + q0 + lane, o[r * 32 + (lane ^ r)]);
+          }
         }
       }
       fence_before();
