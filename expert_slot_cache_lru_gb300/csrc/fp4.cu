@@ -11,6 +11,8 @@
 // per block, q = x r, q' = q + r (x - q d) with r the correctly rounded 1 / d
 // (Markstein, IBM J. Res. Dev. 34, 1990); a block whose divisor or maximum is
 // near the ends of fp32's range divides instead.
+#include <type_traits>
+
 #include "block_ops.cuh"
 #include "fp4.cuh"
 #include "tc.cuh"
@@ -230,19 +232,27 @@ dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
 }
 
 // ---------------------------------------------------------------- global scale
-// the bits of the largest finite magnitude (nonnegative floats order as integers)
-template <typename T>
+// the bits of the largest finite magnitude (nonnegative floats order as integers);
+// VEC: pieces of 16 elements, else single ones
+__device__ __forceinline__ unsigned finite_bits(float v) {
+  const unsigned u = __float_as_uint(v) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-amax_kernel(const T* src, long long stride, int rows, long long cols, unsigned* out) {
+amax_kernel(const T* __restrict__ src, long long stride, int rows, long long cols, unsigned* out) {
   unsigned m = 0;
   for (int row = blockIdx.y; row < rows; row += gridDim.y)
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < cols;
          i += (long long)gridDim.x * kThreads) {
-      const T v = src[row * stride + i];
-      unsigned u;
-      if constexpr (sizeof(T) == 4) u = __float_as_uint(v) & 0x7fffffffu;
-      else u = (unsigned)(__bfloat16_as_ushort(v) & 0x7fffu) << 16;
-      if (u < 0x7f800000u) m = max(m, u);
+      if constexpr (VEC) {
+        Raw<T> x;
+        load16<true>(src + row * stride + i * 16, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max(m, finite_bits(elem(x, j)));
+      } else {
+        m = max(m, finite_bits((float)src[row * stride + i]));
+      }
     }
   m = __reduce_max_sync(0xffffffffu, m);
   if ((threadIdx.x & 31) == 0 && m) atomicMax(out, m);
@@ -330,16 +340,19 @@ cudaError_t launch_fp4_global_scale(const void* src, int dtype, long long stride
                                     int cols, float* g, cudaStream_t s) {
   const cudaError_t e = cudaMemsetAsync(g, 0, sizeof(float), s);
   if (e != cudaSuccess) return e;
-  Grid q = grid_for(rows, cols, stride == cols, 1);
-  const unsigned most = q.rows > 8 ? 152 * 8 / 8 : 152 * 8;  // CTAs loop over what is left
-  if (q.grid.x > most) q.grid.x = most;
-  if (q.grid.y > 1024) q.grid.y = 1024;
   unsigned* u = reinterpret_cast<unsigned*>(g);
-  if (dtype == MOE_T_F32)
-    amax_kernel<<<q.grid, kThreads, 0, s>>>(static_cast<const float*>(src), stride, q.rows, q.width, u);
-  else
-    amax_kernel<<<q.grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(src), stride, q.rows,
-                                            q.width, u);
+  auto go = [&](auto* p) {
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    const bool vec = cols % 16 == 0 && aligned32(src, stride * (long long)sizeof(T));
+    Grid q = grid_for(rows, vec ? cols / 16 : cols, stride == cols, 1);
+    const unsigned most = q.rows > 8 ? 152 : 152 * 8;  // CTAs loop over what is left
+    if (q.grid.x > most) q.grid.x = most;
+    if (q.grid.y > 1024) q.grid.y = 1024;
+    if (vec) amax_kernel<T, true><<<q.grid, kThreads, 0, s>>>(p, stride, q.rows, q.width, u);
+    else amax_kernel<T, false><<<q.grid, kThreads, 0, s>>>(p, stride, q.rows, q.width, u);
+  };
+  if (dtype == MOE_T_F32) go(static_cast<const float*>(src));
+  else go(static_cast<const __nv_bfloat16*>(src));
   global_kernel<<<1, 1, 0, s>>>(g);
   return cudaGetLastError();
 }
