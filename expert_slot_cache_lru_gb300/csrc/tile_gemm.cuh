@@ -550,8 +550,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
       const int pr = 32 * (warp & 3) + lane;
       const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + b * NT;
       const long long p = ((long long)tp * CG + pair) * 128 + pr;
+      // a warp whose rows are all past the matrix has nothing to stage: its output buffers
+      // may still be under a copy, which a piece without a copy of its own would not wait for
+      const int n_end = p - lane < a.p_rows ? NT : 0;
 #pragma unroll 1
-      for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
+      for (int n0 = (warp >> 2) * W; n0 < n_end; n0 += 2 * W) {
         const long long q0 = (long long)tq * NT + n0;
         if (q0 >= a.q_rows) break;
         uint32_t v[W];
@@ -569,7 +572,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
           // keep the block scales waiting (8,192 x 8,192 x 4,096: 100 us, so 94)
           if constexpr (!SWAP) {
             uint8_t* o = ostg + warp * 4096 + (a.f32 ? 0 : (piece & 1) * 2048);
-            if (lane == 0) {  // what this buffer held has been read
+            if (lane == 0) {  // what this buffer held has been read (bf16: two buffers in turn)
               if (a.f32) store_wait_read<0>();
               else store_wait_read<1>();
             }
@@ -593,9 +596,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
             }
             fence_async_smem();
             __syncwarp();
-            // rows past the matrix are not written (a warp's rows may all be)
-            if (lane == 0 && p < a.p_rows) tma_store(&omap, o, (int)q0, (int)p);
-            ++piece;
+            if (lane == 0) tma_store(&omap, o, (int)q0, (int)p);  // rows past the matrix are not written
+            ++piece;  // one copy each: the waits above count copies
           }
         } else {  // other row lengths: turned in shared memory, so that a row's lanes are neighbours
           if constexpr (!SWAP) {
