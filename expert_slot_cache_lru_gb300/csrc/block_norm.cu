@@ -165,12 +165,12 @@ __global__ void __launch_bounds__(512, N == 1 ? 2 : 1) ring_kernel(NormArgs a) {
     if (at >= n) break;
     float2 w[4];
     if (a.post_w) {
-      unpack(__ldg(reinterpret_cast<const uint4*>(a.post_w) + at), w);
+      unpack(reinterpret_cast<const uint4*>(a.post_w)[at], w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[i][j] = __fmul2_rn(f[i][j], __fadd2_rn(offset, w[j]));
     }
     if (GATE == MOE_GATE_NONE && a.gate) {
-      unpack(__ldg(reinterpret_cast<const uint4*>(a.gate) + at), w);
+      unpack(reinterpret_cast<const uint4*>(a.gate)[at], w);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         f[i][j] = a.gate_kind == MOE_GATE_LINEAR
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(512, N == 1 ? 2 : 1) ring_kernel(NormArgs a) {
                       : make_float2(gated<MOE_GATE_SIGMOID>(f[i][j].x, w[j].x),
                                     gated<MOE_GATE_SIGMOID>(f[i][j].y, w[j].y));
     }
-    if (a.pre_w) qw[i] = __ldg(reinterpret_cast<const uint4*>(a.pre_w) + at);
+    if (a.pre_w) qw[i] = reinterpret_cast<const uint4*>(a.pre_w)[at];
   }
   const float inv_h = 1.f / (float)a.hidden;
   int d = 0, odd = 0;
@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(1024, 2) flat_kernel(NormArgs a) {
   // the weights of this piece: elements 8 tid - off ..
   auto weights = [&](const B* p, Piece<8>& v) {
     if (tid > 0 && 8 * tid + 8 <= H) {
-      const uint4 hi_w = __ldg(reinterpret_cast<const uint4*>(p) + tid);
-      const uint4 lo_w = off ? __ldg(reinterpret_cast<const uint4*>(p) + tid - 1) : hi_w;
+      const uint4 hi_w = reinterpret_cast<const uint4*>(p)[tid];
+      const uint4 lo_w = off ? reinterpret_cast<const uint4*>(p)[tid - 1] : hi_w;
       uint4 q = hi_w;
       switch (off) {
         case 1: q = join<1>(lo_w, hi_w); break;

@@ -25,7 +25,7 @@ constexpr int kUnits = 4;
 
 // ---------------------------------------------------------------- loads and stores
 __device__ __forceinline__ void ld32(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
       : "l"(p));
 }
@@ -55,7 +55,7 @@ __device__ __forceinline__ void load16(const float* p, Raw<float>& r) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r.w[i] = __float_as_uint(__ldg(p + i));
+    for (int i = 0; i < 16; ++i) r.w[i] = __float_as_uint(p[i]);
   }
 }
 template <bool VEC>
@@ -65,7 +65,7 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, Raw<__nv_bfloat16
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i] = __ldg(h + 2 * i) | (uint32_t)__ldg(h + 2 * i + 1) << 16;
+    for (int i = 0; i < 8; ++i) r.w[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
   }
 }
 __device__ __forceinline__ float elem(const Raw<float>& r, int i) { return __uint_as_float(r.w[i]); }
@@ -162,12 +162,11 @@ __device__ __forceinline__ uint2 quantize16(const Raw<T>& x, float g, uint32_t& 
 // np pieces of 16 per row; rows without gaps arrive as one long row
 template <bool NV, typename T, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads)
-quantize_kernel(const T* __restrict__ src, long long stride, int rows, long long np,
-                const float* __restrict__ gp, uint8_t* __restrict__ codes,
-                uint8_t* __restrict__ scales) {
+quantize_kernel(const T* src, long long stride, int rows, long long np, const float* gp,
+                uint8_t* codes, uint8_t* scales) {
   tc::pdl_trigger();
   tc::pdl_wait();
-  const float g = NV && gp ? __ldg(gp) : 1.f;
+  const float g = NV && gp ? *gp : 1.f;
   const long long i0 = (long long)blockIdx.x * (kThreads * U) + threadIdx.x;
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const T* p = src + row * stride;
@@ -195,12 +194,11 @@ quantize_kernel(const T* __restrict__ src, long long stride, int rows, long long
 // ---------------------------------------------------------------- dequantize
 template <bool NV, typename T, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads)
-dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int rows,
-                  long long np, const float* __restrict__ gp, T* __restrict__ dst,
-                  long long stride) {
+dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int rows, long long np,
+                  const float* gp, T* dst, long long stride) {
   tc::pdl_trigger();
   tc::pdl_wait();
-  const float g = NV && gp ? __ldg(gp) : 1.f;
+  const float g = NV && gp ? *gp : 1.f;
   const long long i0 = (long long)blockIdx.x * (kThreads * U) + threadIdx.x;
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     T* p = dst + row * stride;
@@ -210,8 +208,8 @@ dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__
     for (int u = 0; u < U; ++u) {
       const long long i = i0 + u * kThreads, at = row * np + i;
       if (i < np) {
-        c[u] = __ldg(reinterpret_cast<const uint2*>(codes + at * 8));
-        sb[u] = __ldg(scales + (NV ? at : at / 2));
+        c[u] = *reinterpret_cast<const uint2*>(codes + at * 8);
+        sb[u] = scales[NV ? at : at / 2];
       }
     }
 #pragma unroll
@@ -240,7 +238,7 @@ __device__ __forceinline__ unsigned finite_bits(float v) {
 }
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-amax_kernel(const T* __restrict__ src, long long stride, int rows, long long cols, unsigned* out) {
+amax_kernel(const T* src, long long stride, int rows, long long cols, unsigned* out) {
   unsigned m = 0;
   for (int row = blockIdx.y; row < rows; row += gridDim.y)
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < cols;

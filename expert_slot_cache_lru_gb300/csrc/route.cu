@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
   if (BIAS) {
 #pragma unroll
     for (int j = 0; j < EL; ++j)
-      b_e[j] = first + (j << shift) < end ? __ldg(a.bias + first + (j << shift)) : 0.f;
+      b_e[j] = first + (j << shift) < end ? a.bias[first + (j << shift)] : 0.f;
   }
 #pragma unroll
   for (int j = 0; j < EL; ++j) {
@@ -340,9 +340,8 @@ constexpr int kDotRows = 8, kDotWarps = 4;
 // z[b][e] for R rows: CTA e, its warps over pieces of 8 elements of K
 template <int R>
 __global__ void __launch_bounds__(32 * kDotWarps)
-dot_kernel(const __nv_bfloat16* __restrict__ x, long long x_stride,
-           const __nv_bfloat16* __restrict__ router, int rows, int hidden, int E,
-           float* __restrict__ z) {
+dot_kernel(const __nv_bfloat16* x, long long x_stride, const __nv_bfloat16* router, int rows,
+           int hidden, int E, float* z) {
   __shared__ float red[kDotWarps][R];
   tc::pdl_trigger();
   tc::pdl_wait();
@@ -351,12 +350,12 @@ dot_kernel(const __nv_bfloat16* __restrict__ x, long long x_stride,
   float acc[R] = {};
 #pragma unroll 2
   for (int i = threadIdx.x; i < hidden / 8; i += 32 * kDotWarps) {
-    const uint4 wq = __ldg(w + i);
+    const uint4 wq = w[i];
     const uint32_t wv[4] = {wq.x, wq.y, wq.z, wq.w};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (r >= rows) break;
-      const uint4 xq = __ldg(reinterpret_cast<const uint4*>(x + r * x_stride) + i);
+      const uint4 xq = reinterpret_cast<const uint4*>(x + r * x_stride)[i];
       const uint32_t xv[4] = {xq.x, xq.y, xq.z, xq.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

@@ -306,6 +306,10 @@ cudaError_t device_info(DeviceInfo* out);
 // Launches a kernel that may start while the one before it in the stream ends:
 // it calls pdl_wait before it touches memory, and pdl_trigger first of all, for
 // the next such kernel.  Hides launch and set-up, about a microsecond a call.
+// Memory may still be written while such a kernel is already resident, so it reads with
+// ordinary loads alone: non-coherent ones (__ldg, ld.global.nc, and what the compiler
+// makes of const __restrict__ pointers) want data that stays as it is for a kernel's whole
+// life, and may be moved above pdl_wait.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                          const A&... args) {

@@ -114,7 +114,7 @@ __device__ __forceinline__ void tile_at(const Args& a, int t, int& tp, int& tq) 
 static __device__ __noinline__ uint4 bank_word(const uint8_t* bank, long long bytes, long long word) {
   uint32_t w[4] = {0, 0, 0, 0};
   for (int j = 0; j < 16 && word * 16 + j < bytes; ++j)
-    w[j >> 2] |= (uint32_t)__ldg(bank + word * 16 + j) << (8 * (j & 3));
+    w[j >> 2] |= (uint32_t)bank[word * 16 + j] << (8 * (j & 3));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // bytes sh .. sh + 15 of two neighbouring words, those from `n` on zero
@@ -163,8 +163,8 @@ __device__ __forceinline__ void ScaleRows<NT>::load(const Args& a, int p_row, in
     sh[u] = (int)(byte & 15);
     if (row < rows && n > 0 && (is_p || r0 + 64 * (u - PR) < NT)) {
       if (((byte >> 4) + 2) * 16 <= bytes) {  // else at the bank's end
-        w0[u] = __ldg(reinterpret_cast<const uint4*>(bank) + (byte >> 4));
-        w1[u] = __ldg(reinterpret_cast<const uint4*>(bank) + (byte >> 4) + 1);
+        w0[u] = reinterpret_cast<const uint4*>(bank)[byte >> 4];
+        w1[u] = reinterpret_cast<const uint4*>(bank)[(byte >> 4) + 1];
       } else {
         w0[u] = bank_word(bank, bytes, byte >> 4);
         w1[u] = bank_word(bank, bytes, (byte >> 4) + 1);

@@ -38,3 +38,93 @@ def test_linear_bf16_tiles_with_warps_past_the_last_row(m, nv, B, N, K):  # noqa
         out = torch.full((B, N), float("nan"), dtype=torch.bfloat16, device="cuda")
         m.moe_fp4_linear(fmt_of(m, nv), xc, xs, None, wc, ws, None, B, N, K, out, m.MOE_T_BF16)
         assert torch.equal(out, f32.bfloat16())
+
+
+# ------------------------------------------------------------------ chains without a stop
+
+def chain(step, n, sources):
+    """step(source) runs calls that go through one set of buffers and returns fresh
+    outputs; n rounds over the sources in turn, enqueued without a stop, give what each
+    source gives alone."""
+    want = []
+    for s in sources:
+        torch.cuda.synchronize()
+        want.append(step(s))
+        torch.cuda.synchronize()
+    got = [step(sources[i % len(sources)]) for i in range(n)]
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for a, b in zip(outs, want[i % len(sources)]):
+            assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("nv", [True, False])
+@pytest.mark.parametrize("B,K,pad", [(1, 512, 0), (64, 2048, 0), (64, 2048, 1), (600, 2080, 0), (4096, 1024, 0)])
+def test_banks_rewritten_between_calls(m, nv, B, K, pad):  # noqa: F811
+    """Two sources in turn through one code bank: bf16 to fp32 and back."""
+    r = np.random.default_rng([B, K])
+    src = [dev(r.normal(0, s, (B, K + pad)), torch.bfloat16) for s in (1.0, 3.0)]
+    codes = torch.empty(B, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(B, K // (16 if nv else 32), dtype=torch.uint8, device="cuda")
+    f = fmt_of(m, nv)
+
+    def step(x):
+        v, back = torch.empty(B, K, device="cuda"), torch.empty(B, K, dtype=torch.bfloat16, device="cuda")
+        m.moe_fp4_quantize(f, x, m.MOE_T_BF16, B, K, None, codes, scales, src_stride=K + pad)
+        m.moe_fp4_dequantize(f, codes, scales, None, B, K, v, m.MOE_T_F32)
+        m.moe_fp4_quantize(f, v, m.MOE_T_F32, B, K, None, codes, scales)
+        m.moe_fp4_dequantize(f, codes, scales, None, B, K, back, m.MOE_T_BF16)
+        return v, back
+
+    chain(step, 40, src)
+
+
+@pytest.mark.parametrize("B,H,E", [(1, 2048, 256), (3, 520, 60), (8, 4096, 64), (40, 2048, 256), (600, 1000, 128),
+                                   (5, 2047, 30)])
+def test_activations_rewritten_between_calls(m, B, H, E):  # noqa: F811
+    """Norm, router, quantise and the 4-bit product through one x and one pair of banks."""
+    r = np.random.default_rng([B, H, E])
+    bf = torch.bfloat16
+    src = [(dev(r.normal(0, 2, (B, H)), bf), dev(r.normal(0, 1, (B, H)), bf)) for _ in range(2)]
+    w, router = dev(r.normal(1, 0.1, H), bf), dev(r.normal(0, H ** -0.5, (E, H)), bf)
+    bias = dev((r.integers(-60, 61, E) * 0.001).astype(np.float32))
+    K = H // 32 * 32
+    wc, ws = banks(r, True, 96, K)
+    x = torch.empty(B, H, dtype=bf, device="cuda")
+    xc = torch.empty(B, K // 2, dtype=torch.uint8, device="cuda")
+    xs = torch.empty(B, K // 16, dtype=torch.uint8, device="cuda")
+
+    def step(s):
+        z, wt, out = (torch.empty(B, n, device="cuda") for n in (E, 4, 96))
+        ids = torch.empty(B, 4, dtype=torch.int32, device="cuda")
+        m.moe_block_norm(s[0], s[1], w, None, w, None, x, B, H)
+        m.moe_route(x, router, bias, B, H, E, 4, z, ids, wt, score=m.MOE_SCORE_SIGMOID)
+        m.moe_fp4_quantize(m.MOE_W_NVFP4, x, m.MOE_T_BF16, B, K, None, xc, xs, src_stride=H)
+        m.moe_fp4_linear(m.MOE_W_NVFP4, xc, xs, None, wc, ws, None, B, 96, K, out, m.MOE_T_F32)
+        return z, ids, wt, out
+
+    chain(step, 40, src)
+
+
+def test_router_made_by_the_call_before(m):  # noqa: F811
+    """Weights that another call has just written: two routers from 4 bits, in turn."""
+    r = np.random.default_rng(11)
+    H, E = 512, 64
+    src = [banks(r, True, E, H) for _ in range(2)]
+    router = torch.empty(E, H, dtype=torch.bfloat16, device="cuda")
+    norm_w = router.view(-1)[:H]
+    x = {B: dev(r.normal(0, 1, (B, H)), torch.bfloat16) for B in (2, 700)}
+
+    def step(s):
+        outs = []
+        for B in (2, 700):
+            z, w = torch.empty(B, E, device="cuda"), torch.empty(B, 2, device="cuda")
+            ids, n = torch.empty(B, 2, dtype=torch.int32, device="cuda"), torch.empty_like(x[B])
+            m.moe_fp4_dequantize(m.MOE_W_NVFP4, *s, None, E, H, router, m.MOE_T_BF16)
+            m.moe_route(x[B], router, None, B, H, E, 2, z, ids, w)
+            m.moe_fp4_dequantize(m.MOE_W_NVFP4, *s, None, E, H, router, m.MOE_T_BF16)
+            m.moe_block_norm(x[B], None, None, None, norm_w, None, n, B, H)
+            outs += [z, ids, w, n]
+        return outs
+
+    chain(step, 40, src)
