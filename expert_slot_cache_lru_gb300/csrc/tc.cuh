@@ -40,8 +40,14 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
 }
 
 // A wait longer than this (about half a second) has failed: a whole product
-// takes milliseconds.
-constexpr long long kWaitCycles = 1000ll * 1000 * 1000;
+// takes milliseconds.  Waits for copies and MMAs in flight keep that limit where
+// the others are built with a shorter one, to see what follows a timeout.
+constexpr long long kDrainCycles = 1000ll * 1000 * 1000;
+#ifdef MOE_TC_WAIT_CYCLES
+constexpr long long kWaitCycles = MOE_TC_WAIT_CYCLES;
+#else
+constexpr long long kWaitCycles = kDrainCycles;
+#endif
 
 __device__ __forceinline__ void raise_abort(int* flag, unsigned long long* status) {
   if (atomicExch(flag, 1) == 0 && status) atomicOr(status, (unsigned long long)MOE_STATUS_TIMEOUT);
@@ -74,11 +80,12 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(yes));
   return yes != 0;
 }
-// Bounded wait that no flag ends: for copies and MMAs in flight before an exit.
-__device__ __forceinline__ void drain_bar(uint64_t* b, uint32_t parity) {
+// Bounded wait that no flag ends, for copies and MMAs in flight; false on timeout.
+__device__ __forceinline__ bool drain_bar(uint64_t* b, uint32_t parity) {
   const long long t0 = clock64();
-  while (!mbar_test(b, parity) && clock64() - t0 <= kWaitCycles) {
-  }
+  while (!mbar_test(b, parity))
+    if (clock64() - t0 > kDrainCycles) return false;
+  return true;
 }
 
 // ---------------------------------------------------------------- TMA
@@ -142,6 +149,9 @@ __device__ __forceinline__ void cluster_wait() {
 __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();
+}
+__device__ __forceinline__ void store_at(uint32_t cluster_addr, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ float4 lds4(uint32_t saddr) {
   float4 v;

@@ -344,6 +344,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   fence_before();
   __syncthreads();
   if (CG > 1) cluster_sync();  // the peer's barriers exist before anything arrives there
+  else if (a.split > 1) cluster_arrive();  // waited for before anything goes to a peer
   fence_after();
   const uint32_t tmem = c.tmem;
   pdl_wait();
@@ -372,13 +373,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         s = s + 1 == ST ? 0 : s + 1;
       }
     }
-    if (!ok) {  // the copies in flight land before the CTA ends
-      if (pair == 0)
-        for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_bar(&c.full[i % ST], (i / ST) & 1);
-      else  // their barrier is the peer's: a copy takes microseconds
-        for (const long long t0 = clock64(); clock64() - t0 < 1000 * 1000;) {
-        }
-    }
+    // the copies in flight land before the CTA ends, whichever warp may have given up
+    if (pair == 0)
+      for (int i = it > ST ? it - ST : 0; i < it; ++i)
+        if (!drain_bar(&c.full[i % ST], (i / ST) & 1)) break;
     __syncwarp();
   } else if (warp == T::kMmaWarp) {
     if (pair == 0) {
@@ -468,9 +466,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
           }
         }
       }
-      if (!ok && warp == kCopyWarp && a.tma_scales)  // copies in flight land before the CTA ends
+      if (warp == kCopyWarp && a.tma_scales)  // as the operands' copies
         for (unsigned i = group > kGroups ? group - kGroups : 0; i < group; ++i)
-          drain_bar(&c.rows_full[i % kGroups], (i / kGroups) & 1);
+          if (!drain_bar(&c.rows_full[i % kGroups], (i / kGroups) & 1)) break;
     }
     __syncwarp();
   } else if (warp >= kScaleWarp) {
@@ -622,7 +620,23 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     if (lane == 0) store_wait_done();
     __syncwarp();
   }
-  if (CG > 1 || a.split > 1) cluster_sync();
+  bool failed = false;
+  if (CG > 1 || a.split > 1) {
+    // a CTA that has given up tells its cluster; every thread that raised the flag passes here
+    if (CG == 1) cluster_wait();
+    if (*reinterpret_cast<volatile int*>(&c.abort_flag))
+      for (int k = 0; k < team; ++k) store_at(peer_addr(sa(&c.abort_flag), k), 1);
+    __syncwarp();
+    cluster_sync();
+    failed = *reinterpret_cast<volatile int*>(&c.abort_flag);
+    // a pair's copies count on its first CTA's barriers, which may have been left by then:
+    // a copy takes microseconds, so both CTAs stay half a millisecond
+    if (CG > 1 && failed) {
+      for (const long long t0 = clock64(); clock64() - t0 < 1000 * 1000;) {
+      }
+      cluster_sync();
+    }
+  }
   if (a.split > 1) {
     // One tile per cluster, its operands done with everywhere.  Every part lays its
     // sums out in rows and copies each peer the rows that the peer adds up; stores
