@@ -27,7 +27,8 @@
 // its part of K and then, through distributed shared memory, its part of the
 // tile's results over the parts in ascending order.
 // Every wait is bounded; on a timeout the CTA reports it, drains its copies and
-// MMAs, frees its tensor memory and returns.
+// MMAs, frees its tensor memory and returns.  A cluster gives a split tile up as one:
+// a tile is stored whole and right or not at all.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -622,7 +623,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
   }
   bool failed = false;
   if (CG > 1 || a.split > 1) {
-    // a CTA that has given up tells its cluster; every thread that raised the flag passes here
+    // a CTA that has given up tells its cluster, which gives the tile up as one; every
+    // thread that raised the flag passes here, and nothing raises it from here on
     if (CG == 1) cluster_wait();
     if (*reinterpret_cast<volatile int*>(&c.abort_flag))
       for (int k = 0; k < team; ++k) store_at(peer_addr(sa(&c.abort_flag), k), 1);
@@ -637,7 +639,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
       cluster_sync();
     }
   }
-  if (a.split > 1) {
+  if (a.split > 1 && !failed) {
     // One tile per cluster, its operands done with everywhere.  Every part lays its
     // sums out in rows and copies each peer the rows that the peer adds up; stores
     // to the peers one by one took 3,000 cycles of a 128 x 128 tile.
@@ -646,20 +648,18 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     float* own = reinterpret_cast<float*>(stg);  // [128][kPitch], then [split - 1][rows_per][kPitch]
     float* in = own + 128 * kPitch;
     if (warp < kEpiWarps) {
-      if (!c.abort_flag) {
-        fence_after();
-        const int pr = 32 * (warp & 3) + lane;
-        const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      fence_after();
+      const int pr = 32 * (warp & 3) + lane;
+      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
-        for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
-          uint32_t v[W];
-          read_sums<NT>(acc + n0, n_chains, v);
+      for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
+        uint32_t v[W];
+        read_sums<NT>(acc + n0, n_chains, v);
 #pragma unroll
-          for (int i = 0; i < W; i += 4)
-            *reinterpret_cast<uint4*>(own + pr * kPitch + n0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        }
-        fence_before();
+        for (int i = 0; i < W; i += 4)
+          *reinterpret_cast<uint4*>(own + pr * kPitch + n0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
+      fence_before();
       fence_async_smem();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (warp == 0 && elect_one()) {
@@ -672,7 +672,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
         }
       }
     }
-    wait_bar(&c.sums, 0, &c.abort_flag, a.status);
+    // the peers' copies are under way to this CTA: no flag ends this wait
+    const bool here = drain_bar(&c.sums, 0);
+    if (!here && a.status) atomicOr(a.status, (unsigned long long)MOE_STATUS_TIMEOUT);
     __syncthreads();
     cluster_arrive();  // what the peers copied here has left their shared memory
     int tp, tq;
@@ -681,7 +683,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CU
     const long long p0 = ((long long)tp * CG + pair) * 128 + part * rows_per, q0 = (long long)tq * NT;
     const int rows = (int)max(0LL, min((long long)rows_per, a.p_rows - p0));
     const int cols = (int)min((long long)NT, a.q_rows - q0);
-    if (c.abort_flag) {
+    if (!here) {
     } else if (SWAP) {  // neighbouring threads take neighbouring rows: outputs of one token
       for (int i = threadIdx.x; i < cols * rows_per; i += kThreads) {
         const int row = i % rows_per, col = i / rows_per;

@@ -49,10 +49,13 @@ def impatient(request, tmp_path_factory):
 # one CTA a tile, pairs, tokens as columns, scales by shifted loads; a few tiles or many each
 WHOLE = [(1, 131072, 256), (128, 40000, 256), (600, 20000, 64), (2048, 8192, 4096), (8192, 2048, 512),
          (300, 40000, 544), (4000, 4000, 2080)]
+# K in two or four parts, on a cluster: rows as rows or as columns, pairs, shifted scales
+SPLIT = [(1, 4096, 4096), (16, 2048, 2048), (64, 1536, 2048), (100, 640, 4096), (128, 128, 8192), (200, 2048, 544),
+         (600, 1536, 2048), (512, 3000, 4096)]
 
 
 @pytest.mark.parametrize("nv", [True, False])
-@pytest.mark.parametrize("B,N,K", WHOLE)
+@pytest.mark.parametrize("B,N,K", WHOLE + SPLIT)
 def test_a_wait_that_runs_out(m, impatient, nv, B, N, K):  # noqa: F811
     r = np.random.default_rng([B, N, K])
     lo, hi, blk = (0x20, 0x40, 16) if nv else (118, 130, 32)
