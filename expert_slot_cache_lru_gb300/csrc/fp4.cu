@@ -159,7 +159,9 @@ __device__ __forceinline__ uint2 quantize16(const Raw<T>& x, float g, uint32_t& 
                     c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
 }
 
-// np pieces of 16 per row; rows without gaps arrive as one long row
+// np pieces of 16 per row; rows without gaps arrive as one long row.  Rows count without
+// sign: up to 2^31 - 1 plus the grid's at most 65,535 stays below 2^32 (64-bit rows: 213
+// us where these take 210, 131,072 x 2,048 and back).
 template <bool NV, typename T, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const T* src, long long stride, int rows, long long np, const float* gp,
@@ -168,7 +170,7 @@ quantize_kernel(const T* src, long long stride, int rows, long long np, const fl
   tc::pdl_wait();
   const float g = NV && gp ? *gp : 1.f;
   const long long i0 = (long long)blockIdx.x * (kThreads * U) + threadIdx.x;
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+  for (unsigned row = blockIdx.y; row < (unsigned)rows; row += gridDim.y) {
     const T* p = src + row * stride;
     Raw<T> x[U];
 #pragma unroll
@@ -200,7 +202,7 @@ dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int rows, long lo
   tc::pdl_wait();
   const float g = NV && gp ? *gp : 1.f;
   const long long i0 = (long long)blockIdx.x * (kThreads * U) + threadIdx.x;
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+  for (unsigned row = blockIdx.y; row < (unsigned)rows; row += gridDim.y) {
     T* p = dst + row * stride;
     uint2 c[U];
     uint32_t sb[U];
@@ -240,7 +242,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 amax_kernel(const T* src, long long stride, int rows, long long cols, unsigned* out) {
   unsigned m = 0;
-  for (int row = blockIdx.y; row < rows; row += gridDim.y)
+  for (unsigned row = blockIdx.y; row < (unsigned)rows; row += gridDim.y)
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < cols;
          i += (long long)gridDim.x * kThreads) {
       if constexpr (VEC) {

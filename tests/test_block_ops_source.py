@@ -26,3 +26,9 @@ def test_early_launched_kernels_load_coherently(name):
     """A kernel that is resident while the one before it still writes may not read
     through the non-coherent path, nor let the compiler choose it."""
     assert not re.findall(r"__ldg\w*\(|ld\.global(?:\.\w+)*\.nc|__restrict__", code(name))
+
+
+@pytest.mark.parametrize("name", EARLY)
+def test_loops_over_rows_do_not_pass_the_type(name):
+    """rows + gridDim passes 2^31 where rows nears it."""
+    assert not re.findall(r"for \(int \w+ = blockIdx[^;]*;[^;]*;[^;)]*\+= gridDim", code(name))

@@ -128,3 +128,37 @@ def test_router_made_by_the_call_before(m):  # noqa: F811
         return outs
 
     chain(step, 40, src)
+
+
+# ------------------------------------------------------------------ rows near 2^31
+
+MOST = 2 ** 31 - 1
+
+
+def test_global_scale_of_the_most_rows(m):  # noqa: F811
+    x = torch.ones(MOST, 2, dtype=torch.bfloat16, device="cuda")
+    g = torch.empty(1, device="cuda")
+    for at in (MOST - 1, MOST - 1025, 5):
+        x[at, 0], x[at, 1] = 24.0, 99.0  # 99: between the rows
+        m.moe_fp4_global_scale(x, m.MOE_T_BF16, MOST, 1, g, src_stride=2)
+        assert g.item() == np.float32(24) / np.float32(2688)
+        x[at] = 1.0
+
+
+def test_conversions_of_the_most_rows(m):  # noqa: F811
+    """Strided rows of one block each, of which the last and some others are looked at."""
+    x = torch.empty(MOST * 17, dtype=torch.bfloat16, device="cuda").view(MOST, 17)
+    x.zero_()
+    codes = torch.empty(MOST, 8, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(MOST, 1, dtype=torch.uint8, device="cuda")
+    some = torch.tensor([0, 65534, 65535, 2 ** 30, MOST - 65536, MOST - 65535, MOST - 2, MOST - 1], device="cuda")
+    r = np.random.default_rng(1)
+    v = dev(r.normal(0, 1, (8, 16)).astype(np.float32)).bfloat16()
+    x[some, :16] = v
+    m.moe_fp4_quantize(m.MOE_W_NVFP4, x, m.MOE_T_BF16, MOST, 16, None, codes, scales, src_stride=17)
+    want_c, want_s = ref.quantize(v.float().cpu().numpy(), True)
+    assert np.array_equal(codes[some].cpu().numpy(), want_c) and np.array_equal(scales[some].cpu().numpy(), want_s)
+    x[some] = 7.0
+    m.moe_fp4_dequantize(m.MOE_W_NVFP4, codes, scales, None, MOST, 16, x, m.MOE_T_BF16, dst_stride=17)
+    back = x[some].double().cpu().numpy()
+    assert np.array_equal(back[:, :16], ref.decode(want_c, want_s, True).astype(np.float32)) and (back[:, 16] == 7).all()
