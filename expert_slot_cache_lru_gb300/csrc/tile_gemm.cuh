@@ -157,12 +157,13 @@ __device__ __forceinline__ void ScaleRows<NT>::load(const Args& a, int p_row, in
 #pragma unroll
   for (int u = 0; u < PR + QR; ++u) {
     const bool is_p = u < PR;
-    const int rows = is_p ? a.p_rows : a.q_rows, row = (is_p ? p_row + 64 * u : q_row + 64 * (u - PR)) + r0;
+    const int rows = is_p ? a.p_rows : a.q_rows;
+    const unsigned row = (unsigned)(is_p ? p_row : q_row) + (is_p ? 64 * u : 64 * (u - PR)) + r0;
     const uint8_t* bank = is_p ? a.ps : a.qs;
     const long long bytes = (long long)rows * a.sb, byte = (long long)row * a.sb + at;
     w0[u] = w1[u] = make_uint4(0, 0, 0, 0);
     sh[u] = (int)(byte & 15);
-    if (row < rows && n > 0 && (is_p || r0 + 64 * (u - PR) < NT)) {
+    if (row < (unsigned)rows && n > 0 && (is_p || r0 + 64 * (u - PR) < NT)) {
       if (((byte >> 4) + 2) * 16 <= bytes) {  // else at the bank's end
         w0[u] = reinterpret_cast<const uint4*>(bank)[byte >> 4];
         w1[u] = reinterpret_cast<const uint4*>(bank)[(byte >> 4) + 1];
@@ -739,7 +740,7 @@ long long cycles(long long p_rows, long long q_rows, int k, int sms) {
   constexpr int kStageCycles = KIND == kBf16 ? (NT <= 64 ? 450 : NT <= 128 ? 494 : 520)
                                              : (NT <= 64 ? 480 : NT <= 128 ? 600 : 630);
   const long long tiles = (p_rows + 128 * CG - 1) / (128 * CG) * ((q_rows + NT - 1) / NT);
-  const int slab = KIND == kBf16 ? 64 : 256, nk = (k + slab - 1) / slab;
+  const int slab = KIND == kBf16 ? 64 : 256, nk = (int)((k + (long long)slab - 1) / slab);
   const int split = split_for(tiles, (nk + T::kPer - 1) / T::kPer, CG, sms);
   const long long per = sms / (CG * split), waves = (tiles + per - 1) / per;
   return waves * ((nk + split - 1) / split * kStageCycles) + (split > 1 ? 2500 + 128 * NT * 4 / 18 : 0);
@@ -757,10 +758,11 @@ cudaError_t launch(const Problem& l, int sms, cudaStream_t s) {
   a.qs = l.qs;
   a.p_rows = l.p_rows;
   a.q_rows = l.q_rows;
-  a.tiles_p = (l.p_rows + 128 * CG - 1) / (128 * CG);
-  a.tiles_q = (l.q_rows + NT - 1) / NT;
+  // rows and K may be just below 2^31: rounded up in 64 bits
+  a.tiles_p = (int)((l.p_rows + 128ll * CG - 1) / (128 * CG));
+  a.tiles_q = (int)((l.q_rows + (long long)NT - 1) / NT);
   const int slab = KIND == kBf16 ? 64 : 256;
-  a.nk = (l.k + slab - 1) / slab;
+  a.nk = (int)((l.k + (long long)slab - 1) / slab);
   a.sb = KIND == kBf16 ? 0 : l.k / (KIND == kNv ? 16 : 32);
   a.tma_scales = a.sb % 16 == 0;
   a.g0 = l.g0;

@@ -162,3 +162,37 @@ def test_conversions_of_the_most_rows(m):  # noqa: F811
     m.moe_fp4_dequantize(m.MOE_W_NVFP4, codes, scales, None, MOST, 16, x, m.MOE_T_BF16, dst_stride=17)
     back = x[some].double().cpu().numpy()
     assert np.array_equal(back[:, :16], ref.decode(want_c, want_s, True).astype(np.float32)) and (back[:, 16] == 7).all()
+
+
+@pytest.mark.parametrize("nv", [True, False])
+def test_linear_of_the_most_weights(m, nv):  # noqa: F811
+    one, blk = (0x38, 16) if nv else (127, 32)
+    xc = torch.full((1, 16), 0x22, dtype=torch.uint8, device="cuda")  # all ones
+    xs = torch.full((1, 32 // blk), one, dtype=torch.uint8, device="cuda")
+    wc = torch.zeros(MOST, 16, dtype=torch.uint8, device="cuda")
+    ws = torch.full((MOST, 32 // blk), one, dtype=torch.uint8, device="cuda")
+    some = torch.tensor([0, 127, 2 ** 30, MOST - 129, MOST - 128, MOST - 1], device="cuda")
+    v = np.random.default_rng(2).integers(0, 256, (6, 16)).astype(np.uint8)
+    wc[some] = dev(v)
+    out = torch.full((1, MOST), float("nan"), dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int64, device="cuda")
+    m.moe_fp4_linear(fmt_of(m, nv), xc, xs, None, wc, ws, None, 1, MOST, 32, out, m.MOE_T_BF16, d_status=st)
+    assert st.item() == 0
+    want = ref.decode(v, np.full((6, 32 // blk), one, np.uint8), nv).sum(1)  # multiples of a half below 192
+    assert np.array_equal(out[0, some].double().cpu().numpy(), dev(want).bfloat16().double().cpu().numpy())
+    out[0, some] = 0.0
+    assert not out.any()
+
+
+def test_route_of_the_most_rows(m):  # noqa: F811
+    x = torch.zeros(MOST, 8, dtype=torch.bfloat16, device="cuda")
+    router = torch.ones(1, 8, dtype=torch.bfloat16, device="cuda")
+    some = torch.tensor([0, 2 ** 30, MOST - 130, MOST - 1], device="cuda")
+    v = dev(np.random.default_rng(3).normal(0, 1, (4, 8)).astype(np.float32)).bfloat16()
+    x[some] = v
+    z, w = (torch.full((MOST, 1), float("nan"), device="cuda") for _ in range(2))
+    ids = torch.full((MOST, 1), -7, dtype=torch.int32, device="cuda")
+    m.moe_route(x, router, None, MOST, 8, 1, 1, z, ids, w)
+    assert ((z[some].double() - v.double().sum(1, keepdim=True)).abs() <= 41 * 2 * U * v.double().abs().sum(1, keepdim=True)).all()
+    z[some] = 0.0
+    assert not z.any() and not ids.any() and bool((w == 1).all())
