@@ -35,6 +35,11 @@ __device__ __forceinline__ uint32_t choice_key(float c) {
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+// The key of a group's two largest values; a sum below the type's lowest value is that
+// value, since the group has unmasked experts.
+__device__ __forceinline__ uint32_t sum_key(float v1, float v2) {
+  return choice_key(fmaxf(v1 + v2, -3.40282347e38f));
+}
 
 // Score numerators: softmax's exp(z - max) or the sigmoid itself.  The fast
 // exponential's relative error, about |argument| 2^-24, is that of a score that is itself
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(128) select_warp_kernel(RouteArgs a, int shift
         v1 = raw_score(v1, softmax, mx) * inv;
         v2 = k2 ? raw_score(v2, softmax, mx) * inv : 0.f;
       }
-      mine = choice_key(v1 + v2);
+      mine = sum_key(v1, v2);
     }
     int rank = 0;  // groups ahead of this one
     for (int g = 0; g < a.groups; ++g) {
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kBigThreads) select_cta_kernel(RouteArgs a) {
       }
       uint32_t sc = k1;
       if (a.group_top == 2 && k1)
-        sc = choice_key(a.bias ? key_value(k1) + (k2 ? key_value(k2) : 0.f) : s1 + s2);
+        sc = a.bias ? sum_key(key_value(k1), k2 ? key_value(k2) : 0.f) : sum_key(s1, s2);
       if (lane == 0) sm.gk[g] = sc;
     }
     __syncthreads();

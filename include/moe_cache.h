@@ -561,9 +561,9 @@ MOE_API int moe_block_norm(const void* d_h, long long h_stride, const void* d_y,
  *   masked: it scores 0 and is never chosen; logits of +inf share a softmax equally;
  *   groups: experts g*E/G .. (g+1)*E/G - 1 form group g; a group's score is its
  *   largest choice (group_top 1) or the sum of its two largest (group_top 2; of s where
- *   d_bias is NULL; a missing second counts 0); the topk_groups groups of largest
- *   score stay eligible, a tie going to the lower group, groups without an
- *   unmasked expert never;
+ *   d_bias is NULL; a missing second counts 0; not below the lowest finite fp32
+ *   value); the topk_groups groups of largest score stay eligible, a tie going to
+ *   the lower group, groups without an unmasked expert never;
  *   the k experts of largest choice, largest first, a tie going to the lower
  *   id; weights w = s (never the bias), divided by their sum if renorm, times
  *   scale (a sum of 0 gives weights 0).  Where fewer than k experts are

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests import block_ref as ref
-from tests.test_gpu_block_ops import U, dev, fmt_of, m  # noqa: F401  (m: the library)
+from tests.test_gpu_block_ops import U, c_args, dev, fmt_of, m  # noqa: F401  (m: the library)
 
 pytestmark = pytest.mark.gpu
 
@@ -196,3 +196,48 @@ def test_route_of_the_most_rows(m):  # noqa: F811
     assert ((z[some].double() - v.double().sum(1, keepdim=True)).abs() <= 41 * 2 * U * v.double().abs().sum(1, keepdim=True)).all()
     z[some] = 0.0
     assert not z.any() and not ids.any() and bool((w == 1).all())
+
+
+# ------------------------------------------------------------------ router: extreme choices
+
+@pytest.mark.parametrize("E", [8, 64, 256, 1024, 1536])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_whose_sum_passes_fp32(m, E, score):  # noqa: F811
+    """group_top 2 with biases of the type's lowest value, a common finite mask: two of
+    them add up to less than fp32 holds, and the group still has unmasked experts."""
+    low, G, k = -np.finfo(np.float32).max, 4, 6
+    gs = E // G
+    kw = dict(score=score, groups=G, topk_groups=3, group_top=2, renorm=True)
+    r = np.random.default_rng(E)
+    z = np.round(r.normal(0, 2, (5, E)) * 64) / 64
+    for case in range(4):
+        bias = np.zeros(E, np.float32)
+        if case == 0:
+            bias[:] = low                    # every group
+        elif case == 1:
+            bias[gs:] = low                  # all but the first
+        elif case == 2:
+            bias[:gs] = low
+            bias[gs:2 * gs] = -np.inf        # truly masked: behind the lowest ones
+            bias[2 * gs:3 * gs] = low
+        else:
+            bias[:] = low
+            bias[gs:gs + 2] = -low           # sums beyond the other end
+            bias[3 * gs:] = np.nan
+        ids = torch.full((5, k), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((5, k), -7.0, device="cuda")
+        m.moe_route_logits(dev(z, torch.float32), m.MOE_T_F32, dev(bias), 5, E, k, ids, w, **c_args(m, kw))
+        # in fp32 the choices under the lowest value are equal: s + low = low
+        want = np.full((5, k), -1)
+        alive = [g for g in range(G) if not (np.isnan(bias[g * gs]) or bias[g * gs] == -np.inf)]
+        best = {g: np.clip(2.0 * np.float64(bias[g * gs]), low, -low) for g in alive}
+        kept = sorted(sorted(alive, key=lambda g: (-best[g], g))[:3])
+        for b in range(5):
+            s, c = ref.choice(z[b:b + 1], score, np.zeros(E))
+            choice = np.where(bias == low, low, np.where(bias == -low, -low, c[0] + bias))
+            cand = [e for g in kept for e in range(g * gs, (g + 1) * gs)]
+            pick = sorted(cand, key=lambda e: (-choice[e], e))[:k]
+            want[b, :len(pick)] = pick
+            assert ids[b].tolist() == want[b].tolist(), (case, b)
+            p = s[0][pick] / s[0][pick].sum()
+            assert (np.abs(w[b].double().cpu().numpy()[:len(pick)] - p) <= 64 * U * p + 1e-37).all()
