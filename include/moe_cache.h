@@ -566,8 +566,9 @@ MOE_API int moe_block_norm(const void* d_h, long long h_stride, const void* d_y,
  *   the lower group, groups without an unmasked expert never;
  *   the k experts of largest choice, largest first, a tie going to the lower
  *   id; weights w = s (never the bias), divided by their sum if renorm, times
- *   scale (a sum of 0 gives weights 0).  Where fewer than k experts are
- *   eligible the rest of the row is id -1, weight 0.
+ *   scale (a sum of 0 gives weights 0; a softmax's shares are taken from the picks'
+ *   logits, so that scores below fp32's range have them too).  Where fewer than k
+ *   experts are eligible the rest of the row is id -1, weight 0.
  * d_ids int32 and d_w float32 [n_rows][k] feed moe_decode_layer or moe_admit.
  * d_logits float32 [n_rows][E], required, receives z.  d_x bf16 (x_stride);
  * d_router bf16 [E][hidden]; d_bias float32 [E] or NULL.

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests import block_ref as ref
-from tests.test_gpu_block_ops import U, c_args, dev, fmt_of, m  # noqa: F401  (m: the library)
+from tests.test_gpu_block_ops import U, c_args, check_choice, dev, fmt_of, m  # noqa: F401  (m: the library)
 
 pytestmark = pytest.mark.gpu
 
@@ -241,3 +241,50 @@ def test_route_groups_whose_sum_passes_fp32(m, E, score):  # noqa: F811
             assert ids[b].tolist() == want[b].tolist(), (case, b)
             p = s[0][pick] / s[0][pick].sum()
             assert (np.abs(w[b].double().cpu().numpy()[:len(pick)] - p) <= 64 * U * p + 1e-37).all()
+
+
+def far_apart(E, lo, hi):
+    """Logits of a row from lo to hi, different ones, in multiples of 1/64 (differences are exact in fp32)."""
+    return np.round(np.linspace(hi, lo, E) * 64) / 64
+
+
+@pytest.mark.parametrize("E", [60, 64, 256, 1024, 1536])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("form", ["plain", "bias", "groups"])
+def test_route_weights_of_logits_far_apart(m, E, score, renorm, form):  # noqa: F811
+    """Scores many powers of ten below the largest are as exact as the largest: the picks' weights
+    against the formula, each within a few fp32 roundings of itself."""
+    k, r = 16, np.random.default_rng(E)
+    z = np.stack([far_apart(E, -80, 0), far_apart(E, -85, 20), r.permutation(far_apart(E, -60, 3)),
+                  far_apart(E, -86, -50)])
+    kw = dict(score=score, renorm=renorm, scale=1.0)
+    bias = None
+    if form == "bias":  # 2 more for the experts of smallest score, in different steps
+        bias = np.zeros(E, np.float32)
+        bias[-20:] = 2 + np.arange(20) * np.float32(0.25)
+    if form == "groups":
+        kw.update(groups=2, topk_groups=1, group_top=2)
+    ids = torch.empty(4, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(4, k, device="cuda")
+    m.moe_route_logits(dev(z, torch.float32), m.MOE_T_F32, None if bias is None else dev(bias), 4, E, k, ids, w,
+                       **c_args(m, kw))
+    check_choice(ids.cpu().numpy(), w.double().cpu().numpy(), z, k,
+                 None if bias is None else bias.astype(np.float64), kw)
+
+
+@pytest.mark.parametrize("E", [16, 256, 1536])
+@pytest.mark.parametrize("has_bias", [False, True])
+def test_route_sigmoids_near_the_smallest_normal_number(m, E, has_bias):  # noqa: F811
+    """All logits at -85 to -88.5: scores down to 4e-39, whose shares are still plain numbers."""
+    k, z = 4, far_apart(E, -88.5, -85)[None]
+    kw = dict(score="sigmoid", renorm=True, scale=2.5)
+    bias = np.zeros(E, np.float32) if has_bias else None
+    if has_bias:
+        bias[-4:] = [4, 3, 2, 1]  # the smallest scores
+    ids = torch.empty(1, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(1, k, device="cuda")
+    m.moe_route_logits(dev(z, torch.float32), m.MOE_T_F32, None if bias is None else dev(bias), 1, E, k, ids, w,
+                       **c_args(m, kw))
+    check_choice(ids.cpu().numpy(), w.double().cpu().numpy(), z, k,
+                 None if bias is None else bias.astype(np.float64), kw)
