@@ -17,8 +17,6 @@
 // 56.9; 8,192 x 2,048 bf16 with a gate per row 28.9 / 32.6; but with an fp32 residual, whose
 // rows put half as many bytes again in flight, 40.8 / 31.2 (6.5 TB/s) for 8,192 x 2,048
 // and 84.3 / 68.8 for 4,096 x 8,192.
-// A sigmoid gate's exponential is the fast one: a relative error of (|gate| + 4) 2^-24 of
-// a term that is added to h.
 #include "block_ops.cuh"
 #include "tc.cuh"
 
@@ -94,11 +92,29 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return v;
 }
 
-template <int GATE>
+// z sigmoid(g) of a bf16 gate.  With n = -g, e^n = 2^(n log2 e); divisor and dividend are a
+// quarter of 1 + e^n and of z, below 2^126 for every e^n that fp32 holds, so that the
+// reciprocal is a normal number.  n log2 e rounds, an error of up to |g| 2^-24 of the
+// result: far below a bf16 residual's own rounding.  EXACT, for an fp32 residual, takes
+// e^n = 2^(n hi) e^(n c): hi is the first 16 bits of log2 e, so that n hi is exact, and
+// c = 1 - hi ln 2, where 1 + n c leaves 1.5 u at n = 88; every step is within an ulp or two.
+// (expf instead: 63.0 us for 8,192 x 4,096 bf16 with a gate per row, 44.7 for 8,192 x 2,048
+// fp32, where these take 52.3 and 39.6; EXACT for bf16 too: 55.8.)
+template <bool EXACT>
+__device__ __forceinline__ float times_sigmoid(float z, float g) {
+  constexpr float kLog2e = 1.44269504f, kHi = 47274.f / 32768.f, kC = 4.88849515e-6f;
+  float n = -g, e, r;
+  if (EXACT) asm("max.NaN.f32 %0, %1, %2;" : "=f"(n) : "f"(n), "f"(-128.f));  // -inf would meet e = 0
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(n, EXACT ? kHi : kLog2e, -2.f)));
+  if (EXACT) e = fmaf(e, n * kC, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 0.25f));
+  return 0.25f * z * r;
+}
+
+template <int GATE, bool EXACT>
 __device__ __forceinline__ float gated(float z, float g) {
   if (GATE == MOE_GATE_LINEAR) return z * g;
-  // the divisor is at least 1; where the quotient underflows 0 is its value
-  if (GATE == MOE_GATE_SIGMOID) return __fdividef(z, 1.f + __expf(-g));
+  if (GATE == MOE_GATE_SIGMOID) return times_sigmoid<EXACT>(z, g);
   return z;
 }
 
@@ -175,8 +191,7 @@ __global__ void __launch_bounds__(512, N == 1 ? 2 : 1) ring_kernel(NormArgs a) {
       for (int j = 0; j < 4; ++j)
         f[i][j] = a.gate_kind == MOE_GATE_LINEAR
                       ? __fmul2_rn(f[i][j], w[j])
-                      : make_float2(gated<MOE_GATE_SIGMOID>(f[i][j].x, w[j].x),
-                                    gated<MOE_GATE_SIGMOID>(f[i][j].y, w[j].y));
+                      : make_float2(times_sigmoid<true>(f[i][j].x, w[j].x), times_sigmoid<true>(f[i][j].y, w[j].y));
     }
     if (a.pre_w) qw[i] = reinterpret_cast<const uint4*>(a.pre_w)[at];
   }
@@ -211,7 +226,7 @@ __global__ void __launch_bounds__(512, N == 1 ? 2 : 1) ring_kernel(NormArgs a) {
         for (int j = 0; j < 4; ++j) {
           z[i][j] = __fmul2_rn(z[i][j], inv);
           if (GATE != MOE_GATE_NONE)
-            z[i][j] = make_float2(gated<GATE>(z[i][j].x, w[j].x), gated<GATE>(z[i][j].y, w[j].y));
+            z[i][j] = make_float2(gated<GATE, false>(z[i][j].x, w[j].x), gated<GATE, false>(z[i][j].y, w[j].y));
           h[i][j] = __ffma2_rn(z[i][j], f[i][j], h[i][j]);
         }
       }
@@ -282,7 +297,8 @@ row_kernel(NormArgs a) {
         }
         if (GATE != MOE_GATE_NONE) load<VEC>(a.gate + b * a.gate_stride + at(i), w);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[i].v[j] = fmaf(a.alpha, gated<GATE>(z[i].v[j], w.v[j]), h[i].v[j]);
+        for (int j = 0; j < VEC; ++j)
+          h[i].v[j] = fmaf(a.alpha, gated<GATE, sizeof(R) == 4>(z[i].v[j], w.v[j]), h[i].v[j]);
       }
   }
   if (a.h_out) {
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(1024, 2) flat_kernel(NormArgs a) {
       else weights(a.gate, w);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h.v[j] = fmaf(a.alpha, gated<GATE>(z.v[j], w.v[j]), h.v[j]);
+    for (int j = 0; j < 8; ++j) h.v[j] = fmaf(a.alpha, gated<GATE, sizeof(R) == 4>(z.v[j], w.v[j]), h.v[j]);
   }
   if (a.h_out) write(static_cast<R*>(a.h_out), h);
   if (!a.pre_w) return;

@@ -543,8 +543,9 @@ typedef enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 } moe_dtype;
  * block output (h' = h; post_w and gate must be NULL / NONE then).  d_h_out
  * NULL: h' is not written.  d_pre_w and d_x_out are both given or both NULL.
  * x' is taken from h' before h' is rounded to res_dtype.  gate: [hidden] used for every row
- * (gate_stride 0) or one per row (gate_stride >= hidden).  d_h_out may equal
- * d_h, and d_x_out may equal d_y, with equal strides; no other overlap. */
+ * (gate_stride 0) or one per row (gate_stride >= hidden); a sigmoid is good to 16 2^-24 of
+ * itself, beside a bf16 residual to (|gate| + 16) 2^-24, down to 2^-128 (0 below).
+ * d_h_out may equal d_h, and d_x_out may equal d_y, with equal strides; no other overlap. */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_LINEAR = 1, MOE_GATE_SIGMOID = 2 } moe_gate_kind;
 MOE_API int moe_block_norm(const void* d_h, long long h_stride, const void* d_y, long long y_stride,
                            const void* d_post_w, const void* d_gate, long long gate_stride,

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests import block_ref as ref
-from tests.test_gpu_block_ops import U, c_args, check_choice, dev, fmt_of, m  # noqa: F401  (m: the library)
+from tests.test_gpu_block_ops import U, c_args, check_choice, dev, fmt_of, half_ulp, m  # noqa: F401  (m: the library)
 
 pytestmark = pytest.mark.gpu
 
@@ -288,3 +288,61 @@ def test_route_sigmoids_near_the_smallest_normal_number(m, E, has_bias):  # noqa
                        **c_args(m, kw))
     check_choice(ids.cpu().numpy(), w.double().cpu().numpy(), z, k,
                  None if bias is None else bias.astype(np.float64), kw)
+
+
+# ------------------------------------------------------------------ block norm: extreme gates
+
+@pytest.mark.parametrize("res", ["bf16", "f32"])
+@pytest.mark.parametrize("rows_gate", [False, True])
+@pytest.mark.parametrize("B,H", [(2, 64), (700, 2048), (5, 1002), (3, 8200), (400, 4104)])
+def test_norm_sigmoid_gates_far_from_zero(m, res, rows_gate, B, H):  # noqa: F811
+    """Gates from -88.5 to 40 on a block output of up to 2e38: terms that count come out as
+    exact as the others, down to sigmoids of 4e-39."""
+    r = np.random.default_rng([B, H])
+    rt = torch.bfloat16 if res == "bf16" else torch.float32
+    g = dev(r.uniform(-88.5, 40, (B, H) if rows_gate else (1, H)).astype(np.float32)).bfloat16()
+    g[:, 0], g[:, 1] = -88.0, 0.0
+    # a term of size 1 or so: 1 / sigmoid(gate) times a normal number
+    y = (torch.exp(-g.double()).add(1).expand(B, H) * dev(r.normal(0, 0.5, (B, H)))).clamp(-2e38, 2e38).bfloat16()
+    h = dev(r.normal(0, 0.01, (B, H)).astype(np.float32)).to(rt)
+    ho, qw = torch.empty_like(h), torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    xo = torch.empty(B, H, dtype=torch.bfloat16, device="cuda")
+    m.moe_block_norm(h, y, None, g, qw, ho, xo, B, H, res_dtype=m.MOE_T_BF16 if res == "bf16" else m.MOE_T_F32,
+                     gate_kind=m.MOE_GATE_SIGMOID, gate_stride=H if rows_gate else 0)
+    f64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    want, x, size = ref.block_norm(f64(h), f64(y), None, f64(g), "sigmoid", 1.0, f64(qw), eps=float(np.float32(1e-6)))
+    c = ((H / 256 + 13) / 2 + 8) * U  # as test_gpu_block_ops.norm_case
+    assert (np.abs(f64(ho) - want) <= half_ulp(rt) * np.abs(want) * 1.01 + c * size).all()
+    inv = np.abs(x) / np.maximum(np.abs(want), 1e-300)
+    assert (np.abs(f64(xo) - x) <= 2.0 ** -8 * np.abs(x) * 1.01 + 2 * c * size * inv + 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("res", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H", [(2, 64), (700, 2048), (5, 1002)])
+def test_norm_infinite_output_under_a_gate(m, res, B, H):  # noqa: F811
+    """An infinity times a sigmoid that is a number stays an infinity."""
+    rt = torch.bfloat16 if res == "bf16" else torch.float32
+    h = torch.zeros(B, H, dtype=rt, device="cuda")
+    y = torch.full((B, H), float("inf"), dtype=torch.bfloat16, device="cuda")
+    g = torch.full((B, H), -88.0, dtype=torch.bfloat16, device="cuda")
+    m.moe_block_norm(h, y, None, g, None, h, None, B, H, res_dtype=m.MOE_T_BF16 if res == "bf16" else m.MOE_T_F32,
+                     gate_kind=m.MOE_GATE_SIGMOID, gate_stride=H)
+    assert bool((h == float("inf")).all())
+
+
+@pytest.mark.parametrize("res", ["bf16", "f32"])
+@pytest.mark.parametrize("rows_gate", [False, True])
+@pytest.mark.parametrize("B,H", [(2, 64), (700, 2048), (5, 1002), (3, 9)])
+def test_norm_gates_without_a_finite_value(m, res, rows_gate, B, H):  # noqa: F811
+    """Gates of +inf, -inf and NaN: all of y, nothing of it, and NaN in that element alone."""
+    rt = torch.bfloat16 if res == "bf16" else torch.float32
+    h = torch.ones(B, H, dtype=rt, device="cuda")
+    y = torch.full((B, H), 2.0, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(B if rows_gate else 1, H, dtype=torch.bfloat16, device="cuda")
+    g[:, 0], g[:, 3], g[:, 8] = float("inf"), -float("inf"), float("nan")
+    m.moe_block_norm(h, y, None, g, None, h, None, B, H, res_dtype=m.MOE_T_BF16 if res == "bf16" else m.MOE_T_F32,
+                     gate_kind=m.MOE_GATE_SIGMOID, gate_stride=H if rows_gate else 0)
+    assert bool(((h[:, 0] - 3.0).abs() <= 8 * U * 3).all()) and bool((h[:, 3] == 1.0).all())
+    assert bool(h[:, 8].isnan().all()) and int(h.isnan().sum()) == B
+    keep = torch.tensor([i for i in range(H) if i not in (0, 3, 8)], device="cuda")
+    assert bool(((h[:, keep] - 2.0).abs() <= 8 * U * 2).all())
