@@ -274,11 +274,11 @@ struct Grid {
   long long width;
   bool wide;
 };
-Grid grid_for(int rows, long long width, bool whole, int per_thread) {
+Grid grid_for(int rows, long long width, bool whole, int per_thread, int sms) {
   Grid g;
   g.rows = whole ? 1 : rows;
   g.width = whole ? rows * width : width;
-  g.wide = (long long)rows * width >= 2LL * 152 * kThreads * per_thread &&
+  g.wide = (long long)rows * width >= 2LL * sms * kThreads * per_thread &&
            g.width >= (long long)kThreads * per_thread;
   const long long per = (long long)kThreads * (g.wide ? per_thread : 1);
   g.grid = dim3((unsigned)((g.width + per - 1) / per), (unsigned)(g.rows < 65535 ? g.rows : 65535));
@@ -288,8 +288,11 @@ Grid grid_for(int rows, long long width, bool whole, int per_thread) {
 template <bool NV, typename T>
 cudaError_t quantize(const T* src, long long stride, int rows, int cols, const float* g,
                      uint8_t* codes, uint8_t* scales, cudaStream_t s) {
+  tc::DeviceInfo d;
+  const cudaError_t e = tc::device_info(&d);
+  if (e != cudaSuccess) return e;
   const bool vec = aligned32(src, stride * (long long)sizeof(T));
-  const Grid q = grid_for(rows, cols / 16, stride == cols, vec ? kUnits : 1);
+  const Grid q = grid_for(rows, cols / 16, stride == cols, vec ? kUnits : 1, d.sms);
   auto go = [&](auto kern) {
     return tc::launch_early(kern, q.grid, dim3(kThreads), 0, s, src, stride, q.rows, q.width, g, codes, scales);
   };
@@ -299,8 +302,11 @@ cudaError_t quantize(const T* src, long long stride, int rows, int cols, const f
 template <bool NV, typename T>
 cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, const float* g, int rows,
                        int cols, T* dst, long long stride, cudaStream_t s) {
+  tc::DeviceInfo d;
+  const cudaError_t e = tc::device_info(&d);
+  if (e != cudaSuccess) return e;
   const bool vec = aligned32(dst, stride * (long long)sizeof(T));
-  const Grid q = grid_for(rows, cols / 16, stride == cols, vec ? kUnits : 1);
+  const Grid q = grid_for(rows, cols / 16, stride == cols, vec ? kUnits : 1, d.sms);
   auto go = [&](auto kern) {
     return tc::launch_early(kern, q.grid, dim3(kThreads), 0, s, codes, scales, q.rows, q.width, g, dst, stride);
   };
@@ -338,14 +344,16 @@ cudaError_t launch_fp4_dequantize(bool nv, const uint8_t* codes, const uint8_t* 
 
 cudaError_t launch_fp4_global_scale(const void* src, int dtype, long long stride, int rows,
                                     int cols, float* g, cudaStream_t s) {
-  const cudaError_t e = cudaMemsetAsync(g, 0, sizeof(float), s);
+  tc::DeviceInfo d;
+  cudaError_t e = tc::device_info(&d);
+  if (e == cudaSuccess) e = cudaMemsetAsync(g, 0, sizeof(float), s);
   if (e != cudaSuccess) return e;
   unsigned* u = reinterpret_cast<unsigned*>(g);
   auto go = [&](auto* p) {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
     const bool vec = cols % 16 == 0 && aligned32(src, stride * (long long)sizeof(T));
-    Grid q = grid_for(rows, vec ? cols / 16 : cols, stride == cols, 1);
-    const unsigned most = q.rows > 8 ? 152 : 152 * 8;  // CTAs loop over what is left
+    Grid q = grid_for(rows, vec ? cols / 16 : cols, stride == cols, 1, d.sms);
+    const unsigned most = q.rows > 8 ? d.sms : d.sms * 8;  // CTAs loop over what is left
     if (q.grid.x > most) q.grid.x = most;
     if (q.grid.y > 1024) q.grid.y = 1024;
     if (vec) amax_kernel<T, true><<<q.grid, kThreads, 0, s>>>(p, stride, q.rows, q.width, u);

@@ -32,3 +32,9 @@ def test_early_launched_kernels_load_coherently(name):
 def test_loops_over_rows_do_not_pass_the_type(name):
     """rows + gridDim passes 2^31 where rows nears it."""
     assert not re.findall(r"for \(int \w+ = blockIdx[^;]*;[^;]*;[^;)]*\+= gridDim", code(name))
+
+
+@pytest.mark.parametrize("name", EARLY + ["fp4_linear.cu", "tc_host.cu"])
+def test_sizes_come_from_the_device(name):
+    """The number of SMs is asked for, not written down."""
+    assert not re.findall(r"\b152\b", code(name))
