@@ -158,12 +158,13 @@ __device__ __forceinline__ void ScaleRows<NT>::load(const Args& a, int p_row, in
   for (int u = 0; u < PR + QR; ++u) {
     const bool is_p = u < PR;
     const int rows = is_p ? a.p_rows : a.q_rows;
-    const unsigned row = (unsigned)(is_p ? p_row : q_row) + (is_p ? 64 * u : 64 * (u - PR)) + r0;
+    // past 2^31 - 1 a row is negative, and not below `rows` without sign
+    const int row = (int)((unsigned)(is_p ? p_row : q_row) + (unsigned)(is_p ? 64 * u : 64 * (u - PR)) + r0);
     const uint8_t* bank = is_p ? a.ps : a.qs;
     const long long bytes = (long long)rows * a.sb, byte = (long long)row * a.sb + at;
     w0[u] = w1[u] = make_uint4(0, 0, 0, 0);
     sh[u] = (int)(byte & 15);
-    if (row < (unsigned)rows && n > 0 && (is_p || r0 + 64 * (u - PR) < NT)) {
+    if ((unsigned)row < (unsigned)rows && n > 0 && (is_p || r0 + 64 * (u - PR) < NT)) {
       if (((byte >> 4) + 2) * 16 <= bytes) {  // else at the bank's end
         w0[u] = reinterpret_cast<const uint4*>(bank)[byte >> 4];
         w1[u] = reinterpret_cast<const uint4*>(bank)[(byte >> 4) + 1];
