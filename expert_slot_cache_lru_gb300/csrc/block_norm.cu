@@ -13,10 +13,12 @@
 // row_kernel: one CTA per row, N pieces of VEC elements per thread, T pieces apart (VEC
 // = 8 for aligned rows, 1 for layouts nothing else takes).
 // flat_kernel: rows without gaps that are not whole 16-byte pieces, in aligned pieces.
-// Measured, ring / row: 8,192 x 4,096 bf16 with a gate per channel 43.9 us (6.1 TB/s) /
-// 56.9; 8,192 x 2,048 bf16 with a gate per row 28.9 / 32.6; but with an fp32 residual, whose
-// rows put half as many bytes again in flight, 40.8 / 31.2 (6.5 TB/s) for 8,192 x 2,048
-// and 84.3 / 68.8 for 4,096 x 8,192.
+// Measured, ring / row: 8,192 x 4,096 bf16 with a gate per channel 44.6 us (6.0 TB/s) /
+// 56.9; 8,192 x 2,048 bf16 with a gate per row 28.1 / 32.6; but with an fp32 residual, whose
+// rows put half as many bytes again in flight, 40.8 / 30.8 (6.5 TB/s) for 8,192 x 2,048
+// and 84.3 / 72.0 for 4,096 x 8,192 without a post-norm.  With one row_kernel takes 33.1 and
+// 99.0: at 1,024 threads an SM holds one CTA, which has nothing in flight across a row's
+// two sums.
 #include "block_ops.cuh"
 #include "tc.cuh"
 
@@ -344,7 +346,7 @@ __device__ __forceinline__ uint4 join(uint4 a, uint4 b) {
 // arrays in aligned pieces of 8, of which a row's first and last may be shared with
 // its neighbours; every array is `off` = row * hidden % 8 elements off the weights,
 // which are read as two pieces and shifted.  One piece per thread, 32 registers: a few
-// spills cost less than half the threads (8,192 x 4,095 bf16 with a gate 87 us, 107 with
+// spills cost less than half the threads (8,192 x 4,095 bf16 with a gate 89 us, 107 with
 // 44 registers, 126 element by element in row_kernel).
 template <typename R, int GATE>
 __global__ void __launch_bounds__(1024, 2) flat_kernel(NormArgs a) {

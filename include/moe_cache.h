@@ -555,11 +555,14 @@ MOE_API int moe_block_norm(const void* d_h, long long h_stride, const void* d_y,
                            void* stream);
 
 /* The router.  Logits z[b][e] = sum_h router[e][h] * x[b][h] (bf16 operands,
- * exact products, fp32 sums), then per row:
+ * exact products, fp32 sums; of more than 8 rows on the tensor cores, whose additions
+ * truncate: 1.0e-6 from the 64-bit sums at hidden 4,096, where rounded ones are 0.6e-6),
+ * then per row:
  *   score s = softmax(z) or sigmoid(z);  choice c = s + bias, or z itself where
  *   d_bias is NULL (the scores' order without their rounding);
  *   an expert whose logit is NaN or -inf, or whose choice is NaN or -inf, is
- *   masked: it scores 0 and is never chosen; logits of +inf share a softmax equally;
+ *   masked: it scores 0 and is never chosen (a softmax's sum leaves out masked logits
+ *   only, not experts that their bias masks); logits of +inf share a softmax equally;
  *   groups: experts g*E/G .. (g+1)*E/G - 1 form group g; a group's score is its
  *   largest choice (group_top 1) or the sum of its two largest (group_top 2; of s where
  *   d_bias is NULL; a missing second counts 0; not below the lowest finite fp32
@@ -575,7 +578,7 @@ MOE_API int moe_block_norm(const void* d_h, long long h_stride, const void* d_y,
  * d_router bf16 [E][hidden]; d_bias float32 [E] or NULL.
  * 1 <= k <= min(32, E), E <= 16384, G <= 64 and a divisor of E (with group_top 2, E/G >= 2).
  * d_status: device word that receives MOE_STATUS_TIMEOUT if a bounded wait
- * gives up (NULL = not reported). */
+ * gives up, which leaves outputs of the call unwritten (NULL = not reported). */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 MOE_API int moe_route(const void* d_x, long long x_stride, const void* d_router,
                       const float* d_bias, int n_rows, int hidden, int n_experts, int k, int score,
@@ -618,7 +621,7 @@ MOE_API int moe_fp4_global_scale(const void* d_src, int dtype, long long src_str
 
 /* The product of 4-bit matrices: out[b][i] = g_x * g_w * sum_k x[b][k] w[i][k],
  * x [n_rows][k] and w [n][k] in the banks moe_fp4_quantize writes (a blob's banks may be passed
- * where they lie), exact products, fp32 sums; out bf16 or fp32, out_stride.
+ * where they lie), exact products, fp32 sums whose additions truncate; out bf16 or fp32, out_stride.
  * wfmt MOE_W_NVFP4 or MOE_W_MXFP4 for both; d_xg, d_wg device global scales
  * (NULL = 1, must be NULL for MXFP4); scales without sign; k a multiple of 32; all four banks
  * 16-byte aligned.  d_status as moe_route. */
