@@ -27,6 +27,13 @@ extern "C" __attribute__((visibility("default"))) int product(
   a.rows = rows, a.n = n, a.k = k, a.nv = nv != 0, a.f32 = true, a.status = status;
   return (int)moe::launch_fp4_linear(a, static_cast<cudaStream_t>(stream));
 }
+extern "C" __attribute__((visibility("default"))) int logits(const void* x, const void* router, int rows, int hidden,
+                                                             int experts, float* z, unsigned long long* status,
+                                                             void* stream) {
+  return (int)moe::launch_route_logits(static_cast<const __nv_bfloat16*>(x), hidden,
+                                       static_cast<const __nv_bfloat16*>(router), rows, hidden, experts, z, status,
+                                       static_cast<cudaStream_t>(stream));
+}
 """
 
 
@@ -37,12 +44,13 @@ def impatient(request, tmp_path_factory):
     with open(shim, "w") as f:
         f.write(SHIM)
     subprocess.run([os.environ.get("NVCC", "nvcc"), "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17",
-                    "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-shared",
+                    "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-shared", "--threads", "0",
                     f"-DMOE_TC_WAIT_CYCLES={request.param}", "-I", CSRC, shim, os.path.join(CSRC, "fp4_linear.cu"),
-                    os.path.join(CSRC, "tc_host.cu"), "-o", lib], check=True)
+                    os.path.join(CSRC, "route.cu"), os.path.join(CSRC, "tc_host.cu"), "-o", lib], check=True)
     lib = C.CDLL(lib)
     lib.cycles = request.param
     lib.product.argtypes = [C.c_int] + [C.c_void_p] * 4 + [C.c_int] * 3 + [C.c_void_p] * 3
+    lib.logits.argtypes = [C.c_void_p] * 2 + [C.c_int] * 3 + [C.c_void_p] * 3
     return lib
 
 
@@ -92,3 +100,40 @@ def test_a_wait_that_runs_out(m, impatient, nv, B, N, K):  # noqa: F811
     w = ref.decode(a[1][:64].cpu().numpy(), s[1][:64].cpu().numpy(), nv)
     err = np.abs(want[-1:, :64].double().cpu().numpy() - x @ w.T)
     assert (err <= (K / 32 + 40) * 2 * U * (np.abs(x) @ np.abs(w).T)).all()
+
+
+# the router's bf16 tiles: one CTA, split in two and four, pairs, pairs split
+@pytest.mark.parametrize("B,H,E", [(20500, 256, 64), (40000, 128, 100), (16, 2048, 512), (64, 4096, 384), (600, 2048, 1024),
+                                   (8192, 4096, 256), (20000, 512, 700)])
+def test_a_wait_of_the_router_that_runs_out(m, impatient, B, H, E):  # noqa: F811
+    r = np.random.default_rng([B, H, E])
+    x = dev(r.normal(0, 1, (B, H)).astype(np.float32)).bfloat16()
+    router = dev(r.normal(0, H ** -0.5, (E, H)).astype(np.float32)).bfloat16()
+    ids, w = torch.empty(B, 1, dtype=torch.int32, device="cuda"), torch.empty(B, 1, device="cuda")
+    st = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def full():
+        z = torch.full((B, E), float("nan"), device="cuda")
+        st.zero_()
+        m.moe_route(x, router, None, B, H, E, 1, z, ids, w, d_status=st)
+        assert st.item() == 0
+        return z
+
+    want = full()
+    gave_up = 0
+    for _ in range(4):
+        z = torch.full((B, E), float("nan"), device="cuda")
+        st.zero_()
+        assert impatient.logits(x.data_ptr(), router.data_ptr(), B, H, E, z.data_ptr(), st.data_ptr(),
+                                torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        untouched = z.isnan()
+        assert torch.equal(z[~untouched], want[~untouched])
+        assert st.item() == m.MOE_STATUS_TIMEOUT if untouched.any() else st.item() in (0, m.MOE_STATUS_TIMEOUT)
+        gave_up += int(st.item() != 0)
+    if impatient.cycles == 0:
+        assert gave_up
+    print(f"router {B} x {H} x {E}: {gave_up} of 4 gave up, {untouched.double().mean().item():.3f} untouched in the last")
+    assert torch.equal(full(), want)
+    size = x.double().abs() @ router.double().abs().T
+    assert ((want.double() - x.double() @ router.double().T).abs() <= (H / 16 + 40) * 2 * U * size).all()
