@@ -56,6 +56,11 @@ MOE_GATE_LINEAR = 1
 MOE_GATE_SIGMOID = 2
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
+MOE_ACT_NONE = 0
+MOE_ACT_SILU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_GELU_TANH = 3
+MOE_ACT_RELU = 4
 
 
 class moe_cache_desc(C.Structure):
@@ -126,6 +131,12 @@ _SIGS = {
     "moe_fp4_dequantize": [_i, _vp, _vp, _vp, _i, _i, _vp, _i, _ll, _vp],
     "moe_fp4_global_scale": [_vp, _i, _ll, _i, _i, _vp, _vp],
     "moe_fp4_linear": [_i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _ll, _vp, _vp],
+    "moe_linear": [_vp, _ll, _vp, _ll, _vp, _i, _i, _vp, _ll, _fl, _i, _i, _i, _vp, _i, _ll, _vp,
+                   _vp],
+    "moe_group_routes": [_vp, _i, _i, _vp, _vp, _vp, _vp],
+    "moe_grouped_linear": [_vp, _ll, _i, _vp, _i, _vp, _i, _vp, _ll, _ll, _vp, _i, _i, _i, _i, _i,
+                           _vp, _i, _ll, _vp, _vp],
+    "moe_combine": [_vp, _i, _ll, _i, _vp, _vp, _vp, _ll, _i, _i, _i, _vp, _i, _ll, _vp],
     "moe_strerror": [_i],
     "moe_last_cuda_error": [],
     "moe_abi_version": [],
@@ -430,6 +441,45 @@ def moe_fp4_linear(wfmt: int, d_x_codes, d_x_scales, d_xg, d_w_codes, d_w_scales
     _check("moe_fp4_linear", _lib.moe_fp4_linear(
         wfmt, _ptr(d_x_codes), _ptr(d_x_scales), _ptr(d_xg), _ptr(d_w_codes), _ptr(d_w_scales),
         _ptr(d_wg), n_rows, n, k, _ptr(d_out), dtype, out_stride, _ptr(d_status), _stream(stream)))
+
+
+def moe_linear(d_x, d_w, d_bias, d_res, d_out, n_rows: int, n: int, k: int, *,
+               act: int = MOE_ACT_NONE, gated: bool = False, alpha: float = 1.0,
+               dtype: int = MOE_T_BF16, x_stride: int = 0, w_stride: int = 0, res_stride: int = 0,
+               out_stride: int = 0, d_status=None, stream=None) -> None:
+    """The bf16 product with bias, activation, gate and residual (see moe_cache.h)."""
+    _check("moe_linear", _lib.moe_linear(
+        _ptr(d_x), x_stride, _ptr(d_w), w_stride, _ptr(d_bias), act, gated, _ptr(d_res), res_stride,
+        alpha, n_rows, n, k, _ptr(d_out), dtype, out_stride, _ptr(d_status), _stream(stream)))
+
+
+def moe_group_routes(d_ids, n_routes: int, n_experts: int, d_offsets, d_order=None, d_pos=None, *,
+                     stream=None) -> None:
+    """A step's routes in order of their expert (see moe_cache.h)."""
+    _check("moe_group_routes", _lib.moe_group_routes(
+        _ptr(d_ids), n_routes, n_experts, _ptr(d_offsets), _ptr(d_order), _ptr(d_pos),
+        _stream(stream)))
+
+
+def moe_grouped_linear(d_x, x_rows: int, d_order, per_row: int, d_offsets, n_groups: int, d_w, d_bias,
+                       d_out, n_rows: int, n: int, k: int, *, act: int = MOE_ACT_NONE,
+                       gated: bool = False, dtype: int = MOE_T_BF16, x_stride: int = 0,
+                       w_group_stride: int = 0, w_stride: int = 0, out_stride: int = 0,
+                       d_status=None, stream=None) -> None:
+    """One product per group of rows (see moe_cache.h)."""
+    _check("moe_grouped_linear", _lib.moe_grouped_linear(
+        _ptr(d_x), x_stride, x_rows, _ptr(d_order), per_row, _ptr(d_offsets), n_groups, _ptr(d_w),
+        w_group_stride, w_stride, _ptr(d_bias), act, gated, n_rows, n, k, _ptr(d_out), dtype,
+        out_stride, _ptr(d_status), _stream(stream)))
+
+
+def moe_combine(d_y, y_rows: int, d_pos, d_w, d_add, d_out, n_rows: int, k: int, hidden: int, *,
+                y_dtype: int = MOE_T_BF16, dtype: int = MOE_T_BF16, y_stride: int = 0,
+                add_stride: int = 0, out_stride: int = 0, stream=None) -> None:
+    """The routes' outputs, weighted, back into their rows (see moe_cache.h)."""
+    _check("moe_combine", _lib.moe_combine(
+        _ptr(d_y), y_dtype, y_stride, y_rows, _ptr(d_pos), _ptr(d_w), _ptr(d_add), add_stride, n_rows,
+        k, hidden, _ptr(d_out), dtype, out_stride, _stream(stream)))
 
 
 def blob_bytes(wfmt: int, hidden: int, inter: int) -> int:

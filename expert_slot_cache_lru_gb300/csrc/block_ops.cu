@@ -37,6 +37,28 @@ int check_banks(int wfmt, int rows, int cols, const float* g) {
   return wfmt == MOE_W_BF16 || wfmt == MOE_W_Q4_0 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
 }
 
+// What the dense and the grouped product have in common; strides are filled in.
+int check_linear(moe::Linear& l, int gated, int dtype) {
+  if (l.rows < 0 || l.n < 1 || l.k < 1 || l.act < MOE_ACT_NONE || l.act > MOE_ACT_RELU ||
+      (gated != 0 && gated != 1) || !is_dtype(dtype))
+    return MOE_ERR_INVALID_ARG;
+  l.gated = gated != 0;
+  l.f32 = dtype == MOE_T_F32;
+  const long long wide = l.gated ? 2ll * l.n : l.n;
+  if (!take_stride(l.x_stride, l.k) || !take_stride(l.w_stride, l.k) ||
+      !take_stride(l.out_stride, l.n) || !take_stride(l.res_stride, l.n))
+    return MOE_ERR_INVALID_ARG;
+  if (l.group_stride == 0) l.group_stride = wide * l.w_stride;
+  if (l.group_stride < (wide - 1) * l.w_stride + l.k) return MOE_ERR_INVALID_ARG;
+  if (l.rows == 0) return MOE_OK;
+  const size_t e = size_of(dtype);
+  if (!l.x || !l.w || !l.out || !aligned(l.x, 2) || !aligned(l.w, 2) || !aligned(l.bias, 2) ||
+      !aligned(l.res, e) || !aligned(l.out, e) || !aligned(l.status, 8) ||
+      (l.res == l.out && l.res_stride != l.out_stride) || l.out == l.x || l.out == l.w)
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -198,6 +220,111 @@ int moe_fp4_linear(int wfmt, const uint8_t* d_x_codes, const uint8_t* d_x_scales
   a.f32 = dtype == MOE_T_F32;
   a.status = d_status;
   return done(moe::launch_fp4_linear(a, as_stream(stream)), "moe_fp4_linear");
+}
+
+int moe_linear(const void* d_x, long long x_stride, const void* d_w, long long w_stride,
+               const void* d_bias, int act, int gated, const void* d_res, long long res_stride,
+               float alpha, int n_rows, int n, int k, void* d_out, int dtype, long long out_stride,
+               unsigned long long* d_status, void* stream) {
+  using B = __nv_bfloat16;
+  moe::Linear l{};
+  l.x = static_cast<const B*>(d_x);
+  l.w = static_cast<const B*>(d_w);
+  l.bias = static_cast<const B*>(d_bias);
+  l.res = d_res;
+  l.out = d_out;
+  l.x_stride = x_stride;
+  l.w_stride = w_stride;
+  l.res_stride = res_stride;
+  l.out_stride = out_stride;
+  l.x_rows = l.rows = n_rows;
+  l.per_row = l.groups = 1;
+  l.n = n;
+  l.k = k;
+  l.act = act;
+  l.alpha = alpha;
+  l.status = d_status;
+  const int rc = check_linear(l, gated, dtype);
+  if (rc != MOE_OK || n_rows == 0) return rc;
+  return done(moe::launch_linear(l, as_stream(stream)), "moe_linear");
+}
+
+int moe_group_routes(const int32_t* d_ids, int n_routes, int n_experts, int32_t* d_offsets,
+                     int32_t* d_order, int32_t* d_pos, void* stream) {
+  if (n_routes < 0 || n_experts < 1) return MOE_ERR_INVALID_ARG;
+  if (n_experts > 16384) return MOE_ERR_UNSUPPORTED;
+  if (!d_offsets || (n_routes > 0 && !d_ids) || !aligned(d_ids, 4) || !aligned(d_offsets, 4) ||
+      !aligned(d_order, 4) || !aligned(d_pos, 4) || d_offsets == d_ids || d_offsets == d_order ||
+      d_offsets == d_pos || (d_order && (d_order == d_ids || d_order == d_pos)))
+    return MOE_ERR_INVALID_ARG;
+  return done(moe::launch_group_routes(d_ids, n_routes, n_experts, d_offsets, d_order, d_pos,
+                                       as_stream(stream)),
+              "moe_group_routes");
+}
+
+int moe_grouped_linear(const void* d_x, long long x_stride, int x_rows, const int32_t* d_order,
+                       int per_row, const int32_t* d_offsets, int n_groups, const void* d_w,
+                       long long w_group_stride, long long w_stride, const void* d_bias, int act,
+                       int gated, int n_rows, int n, int k, void* d_out, int dtype,
+                       long long out_stride, unsigned long long* d_status, void* stream) {
+  using B = __nv_bfloat16;
+  if (n_groups < 1 || per_row < 1 || x_rows < 0 || (!d_order && x_rows < n_rows))
+    return MOE_ERR_INVALID_ARG;
+  if (n_groups > 16384) return MOE_ERR_UNSUPPORTED;
+  moe::Linear l{};
+  l.x = static_cast<const B*>(d_x);
+  l.w = static_cast<const B*>(d_w);
+  l.bias = static_cast<const B*>(d_bias);
+  l.out = d_out;
+  l.x_stride = x_stride;
+  l.w_stride = w_stride;
+  l.group_stride = w_group_stride;
+  l.out_stride = out_stride;
+  l.order = d_order;
+  l.offsets = d_offsets;
+  l.x_rows = x_rows;
+  l.per_row = per_row;
+  l.groups = n_groups;
+  l.rows = n_rows;
+  l.n = n;
+  l.k = k;
+  l.act = act;
+  l.alpha = 1.f;
+  l.status = d_status;
+  const int rc = check_linear(l, gated, dtype);
+  if (rc != MOE_OK || n_rows == 0) return rc;
+  if (!d_offsets || !aligned(d_offsets, 4) || !aligned(d_order, 4)) return MOE_ERR_INVALID_ARG;
+  if (x_rows == 0) return MOE_OK;  // no place has a row
+  return done(moe::launch_linear(l, as_stream(stream)), "moe_grouped_linear");
+}
+
+int moe_combine(const void* d_y, int y_dtype, long long y_stride, int y_rows, const int32_t* d_pos,
+                const float* d_w, const void* d_add, long long add_stride, int n_rows, int k,
+                int hidden, void* d_out, int dtype, long long out_stride, void* stream) {
+  if (n_rows < 0 || y_rows < 0 || k < 1 || hidden < 1 || !is_dtype(y_dtype) || !is_dtype(dtype) ||
+      (y_dtype == MOE_T_F32 && dtype != MOE_T_F32) || !take_stride(y_stride, hidden) ||
+      !take_stride(add_stride, hidden) || !take_stride(out_stride, hidden))
+    return MOE_ERR_INVALID_ARG;
+  if (n_rows == 0) return MOE_OK;
+  const size_t e = size_of(dtype);
+  if ((!d_y && y_rows > 0) || !d_pos || !d_w || !d_out || !aligned(d_y, size_of(y_dtype)) ||
+      !aligned(d_pos, 4) || !aligned(d_w, 4) || !aligned(d_add, e) || !aligned(d_out, e) ||
+      d_out == d_y || (d_out == d_add && out_stride != add_stride))
+    return MOE_ERR_INVALID_ARG;
+  moe::CombineArgs a{};
+  a.y = d_y;
+  a.add = d_add;
+  a.out = d_out;
+  a.pos = d_pos;
+  a.w = d_w;
+  a.y_stride = y_stride;
+  a.add_stride = add_stride;
+  a.out_stride = out_stride;
+  a.y_rows = y_rows;
+  a.rows = n_rows;
+  a.k = k;
+  a.hidden = hidden;
+  return done(moe::launch_combine(a, y_dtype, dtype, as_stream(stream)), "moe_combine");
 }
 
 }  // extern "C"

@@ -60,4 +60,32 @@ struct Fp4Linear {
 };
 cudaError_t launch_fp4_linear(const Fp4Linear& a, cudaStream_t s);
 
+// A bf16 product, dense (offsets NULL: one group of all rows) or one per group.
+struct Linear {
+  const __nv_bfloat16 *x, *w, *bias;  // bias: [groups][n], or [groups][2 n]
+  const void* res;
+  void* out;
+  long long x_stride, w_stride, group_stride, res_stride, out_stride;
+  const int32_t *order, *offsets;
+  int x_rows, per_row, groups;
+  int rows, n, k, act;
+  bool gated, f32;
+  float alpha;
+  unsigned long long* status;
+};
+cudaError_t launch_linear(const Linear& a, cudaStream_t s);
+
+cudaError_t launch_group_routes(const int32_t* ids, int routes, int experts, int32_t* offsets,
+                                int32_t* order, int32_t* pos, cudaStream_t s);
+
+struct CombineArgs {
+  const void *y, *add;
+  void* out;
+  const int32_t* pos;
+  const float* w;
+  long long y_stride, add_stride, out_stride;
+  int y_rows, rows, k, hidden;
+};
+cudaError_t launch_combine(const CombineArgs& a, int y_dtype, int dtype, cudaStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,165 @@
+// linear.cuh -- what the bf16 products share: activations, the end of a result, and
+// the walk over the tiles of ragged groups.
+#pragma once
+
+#include "block_ops.cuh"
+
+namespace moe {
+namespace lin {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// e^-|z| over a divisor of 1 .. 2, where __fdividef has 2 ulp; NaN for a NaN
+__device__ __forceinline__ float sigmoid(float z) {
+  const float e = expf(-fabsf(z));
+  return __fdividef(z < 0.f ? e : 1.f, 1.f + e);
+}
+template <int ACT>
+__device__ __forceinline__ float act1(float z) {
+  if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid(z);
+  if constexpr (ACT == MOE_ACT_GELU) return z * normcdff(z);
+  // (1 + tanh u) / 2 is the sigmoid of 2 u, which does not cancel
+  if constexpr (ACT == MOE_ACT_GELU_TANH) return z * sigmoid(1.5957691216f * fmaf(0.044715f * z, z * z, z));
+  if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
+  return z;
+}
+template <int A>
+struct Act {
+  __device__ __forceinline__ float operator()(float z) const { return act1<A>(z); }
+};
+// f with the activation as its argument: one branch around a loop over many values
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == MOE_ACT_SILU) f(Act<MOE_ACT_SILU>{});
+  else if (act == MOE_ACT_GELU) f(Act<MOE_ACT_GELU>{});
+  else if (act == MOE_ACT_GELU_TANH) f(Act<MOE_ACT_GELU_TANH>{});
+  else if (act == MOE_ACT_RELU) f(Act<MOE_ACT_RELU>{});
+  else f(Act<MOE_ACT_NONE>{});
+}
+
+__device__ __forceinline__ float load_res(const Linear& l, long long at) {
+  return l.f32 ? static_cast<const float*>(l.res)[at]
+               : __bfloat162float(static_cast<const __nv_bfloat16*>(l.res)[at]);
+}
+__device__ __forceinline__ void store_out(const Linear& l, long long at, float v) {
+  if (l.f32) static_cast<float*>(l.out)[at] = v;
+  else static_cast<__nv_bfloat16*>(l.out)[at] = __float2bfloat16_rn(v);
+}
+// res + alpha * y at (row, n)
+__device__ __forceinline__ void finish(const Linear& l, long long row, long long n, float y) {
+  const float v = l.res ? fmaf(l.alpha, y, load_res(l, row * l.res_stride + n)) : l.alpha * y;
+  store_out(l, row * l.out_stride + n, v);
+}
+
+// The row of x behind place p, or -1 where there is none.
+__device__ __forceinline__ int source_row(const Linear& l, int p) {
+  if (!l.order) return p;
+  const int r = l.order[p];
+  const int b = r < 0 ? -1 : r / l.per_row;
+  return b < l.x_rows ? b : -1;
+}
+
+// Tiles of ragged groups in order, for a warp that asks for rising tile numbers.  A
+// group of R rows has ceil(R / 2^shift) tiles of equal size (up to a multiple of gran) by `tn`
+// tiles of n; the tiles of n run fastest, in strips of 8, so that tiles that run at the
+// same time share operands in L2.  128 groups are looked at together: each lane counts the
+// tiles of four, and a scan over the lanes finds the one a tile is in.  The next 128 groups' offsets
+// are loaded ahead.
+struct Tile {
+  int group, row, rows, n;  // rows: of this tile; n: which tile of n
+  int width;                // rows of the group's tiles
+};
+struct Walk {
+  const int32_t* offsets;
+  int groups, total_rows, shift, gran, tn;  // tiles of up to 1 << shift rows
+  int g0;         // first group of this chunk
+  int base, end;  // tile numbers of this chunk
+  int lo[4], hi[4], ahead[5], incl;
+
+  __device__ __forceinline__ void load(int g) {  // into `ahead`, lane's four groups of a chunk
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int at = g + 4 * (int)(threadIdx.x & 31) + i;
+      ahead[i] = offsets ? offsets[min(at, groups)] : (at == 0 ? 0 : total_rows);
+    }
+  }
+  __device__ __forceinline__ int parts(int rows) const {  // rows up to 2^31 - 1
+    return (int)(((unsigned)rows + (1u << shift) - 1) >> shift);
+  }
+  __device__ __forceinline__ int tiles(int i) const { return parts(hi[i] - lo[i]) * tn; }
+  __device__ __forceinline__ void take() {  // the chunk from `ahead`
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = min(max(ahead[i], 0), total_rows);
+      hi[i] = max(lo[i], min(ahead[i + 1], total_rows));
+      sum += tiles(i);
+    }
+    incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, incl, o);
+      if ((int)(threadIdx.x & 31) >= o) incl += v;
+    }
+    end = base + __shfl_sync(kAll, incl, 31);
+  }
+  __device__ __forceinline__ void start(const Linear& l, int shift_, int gran_, int tn_) {
+    offsets = l.offsets;
+    groups = l.groups;
+    total_rows = l.rows;
+    shift = shift_;
+    gran = gran_;
+    tn = tn_;
+    g0 = base = 0;
+    load(0);
+    take();
+    load(128);
+  }
+  // false where tile t is past the last
+  __device__ __forceinline__ bool seek(int t, Tile& out) {
+    while (t >= end) {
+      g0 += 128;
+      if (g0 >= groups) return false;
+      base = end;
+      take();
+      load(g0 + 128);
+    }
+    int r = t - base;
+    const int lane = __ffs(__ballot_sync(kAll, incl > r)) - 1;
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine += tiles(i);
+    r -= __shfl_sync(kAll, incl - mine, lane);
+    int l0 = 0, h0 = 0, g = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = __shfl_sync(kAll, lo[i], lane), b = __shfl_sync(kAll, hi[i], lane);
+      const int n = parts(b - a) * tn;
+      if (!found && r < n) {
+        found = true;
+        l0 = a;
+        h0 = b;
+        g = g0 + 4 * lane + i;
+      }
+      if (!found) r -= n;
+    }
+    const int R = h0 - l0, T = parts(R);
+    out.group = g;
+    out.width = ((R - 1) / T + gran) / gran * gran;  // ceil(R / T), up to a multiple of gran
+    const int per = 8 * T, strip = r / per, in = r - strip * per, w = min(8, tn - strip * 8);
+    out.n = strip * 8 + in % w;
+    out.row = l0 + in / w * out.width;
+    out.rows = min(out.width, h0 - out.row);
+    return true;
+  }
+};
+
+// Most tiles there can be, for a grid.
+inline long long most_tiles(const Linear& l, int shift, long long tn) {
+  const long long part = l.rows < l.groups ? l.rows : l.groups;
+  return (((long long)l.rows >> shift) + part) * tn;
+}
+
+}  // namespace lin
+}  // namespace moe

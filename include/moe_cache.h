@@ -630,6 +630,68 @@ MOE_API int moe_fp4_linear(int wfmt, const uint8_t* d_x_codes, const uint8_t* d_
                            const float* d_wg, int n_rows, int n, int k, void* d_out, int dtype,
                            long long out_stride, unsigned long long* d_status, void* stream);
 
+/* ---------------------------------------------------------------- bf16 products, groups of routes
+ * Beside the operators above, under the same conventions (no handle, no allocation, no state, strides,
+ * alignment, streams): the bf16 product with an epilogue, and what runs experts that lie on the device
+ * whole (a pool of bf16 blobs, a layer's weights) over a step of any size:
+ *   moe_group_routes     ids -> the routes in order of their expert;
+ *   moe_grouped_linear   one product per expert over its own rows (gate and up, then down);
+ *   moe_combine          the routes' outputs, weighted, back into their rows.
+ * Operands bf16, exact products, fp32 sums; sums of the tensor cores truncate their additions, as
+ * moe_fp4_linear's do.
+ * act(z):  NONE z;  SILU z / (1 + e^-z);  GELU z Phi(z), Phi the normal distribution function;
+ *   GELU_TANH (z / 2) (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)));  RELU max(z, 0).  In fp32, a NaN
+ *   stays NaN, and -inf is NaN but for NONE and RELU. */
+typedef enum {
+  MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_RELU = 4
+} moe_act;
+
+/* out[b][i] = res[b][i] + alpha * act(z[b][i]),  z = x w^T + bias:  x [n_rows][k], w [n][k],
+ * bias [n] (NULL = 0), bf16; res (NULL = 0) and out [n_rows][n] of dtype.  One rounding, to dtype.
+ * gated != 0: w [2 n][k] holds a gate matrix and then an up matrix (a bf16 blob's first two banks),
+ * bias [2 n]:  out = res + alpha * act(z_gate) * z_up.
+ * d_out may equal d_res, with equal strides; no other overlap.  Any n, k >= 1; x and w in rows of whole
+ * 16-byte pieces (strides and k multiples of 8, 16-byte aligned bases) and, if gated, n a multiple
+ * of 16 take the tensor cores.  d_status as moe_route. */
+MOE_API int moe_linear(const void* d_x, long long x_stride, const void* d_w, long long w_stride,
+                       const void* d_bias, int act, int gated, const void* d_res,
+                       long long res_stride, float alpha, int n_rows, int n, int k, void* d_out,
+                       int dtype, long long out_stride, unsigned long long* d_status, void* stream);
+
+/* The routes of a step in order of their expert.  d_ids int32 [n_routes] (a step's [rows][k] ids, or
+ * slot ids); an id outside [0, n_experts) is no route.
+ *   d_offsets [n_experts + 1]: group e is places offsets[e] .. offsets[e + 1] - 1;
+ *   d_order [n_routes] (NULL = not wanted): the route at each place, by (id, route) ascending; -1 from
+ *     offsets[n_experts] on;
+ *   d_pos [n_routes] (NULL = not wanted, may equal d_ids): the place of each route, -1 for none.
+ * One launch.  n_experts 1 .. 16384. n_routes 0 fills d_offsets with 0. */
+MOE_API int moe_group_routes(const int32_t* d_ids, int n_routes, int n_experts, int32_t* d_offsets,
+                             int32_t* d_order, int32_t* d_pos, void* stream);
+
+/* One product per group: for each place p of group g (d_offsets as moe_group_routes writes it)
+ *   out[p] = act(w_g x[r] + bias_g),  r = order[p] / per_row, or p where d_order is NULL;
+ * gated as moe_linear.  w_g = d_w + g * w_group_stride (elements; 0 = without gaps; a slot pool's bank:
+ * slot_stride / 2), bias [n_groups][n] or [n_groups][2 n].  x has x_rows rows (>= n_rows where
+ * d_order is NULL); out n_rows, the most places there may be.  Offsets are taken within
+ * 0 .. n_rows.  Rows of out that are no place of a group, or whose order is negative or names a row
+ * from x_rows on, stay as they were.  A group's weights may be unset where it has no rows.
+ * n_groups 1 .. 16384.  Tensor cores and d_status as moe_linear (w_group_stride a multiple of 8). */
+MOE_API int moe_grouped_linear(const void* d_x, long long x_stride, int x_rows,
+                               const int32_t* d_order, int per_row, const int32_t* d_offsets,
+                               int n_groups, const void* d_w, long long w_group_stride,
+                               long long w_stride, const void* d_bias, int act, int gated,
+                               int n_rows, int n, int k, void* d_out, int dtype,
+                               long long out_stride, unsigned long long* d_status, void* stream);
+
+/* out[b] = add[b] + sum_j w[b][j] * y[pos[b][j]],  j ascending from add (NULL = 0), fp32 sums;
+ * a pos outside [0, y_rows) adds nothing, whatever its weight.  y [y_rows][hidden] of y_dtype (fp32 only
+ * into an fp32 out), pos int32 and w float32 [n_rows][k], add and out [n_rows][hidden] of dtype.
+ * d_out may equal d_add, with equal strides; no other overlap. */
+MOE_API int moe_combine(const void* d_y, int y_dtype, long long y_stride, int y_rows,
+                        const int32_t* d_pos, const float* d_w, const void* d_add,
+                        long long add_stride, int n_rows, int k, int hidden, void* d_out, int dtype,
+                        long long out_stride, void* stream);
+
 /* Text of an error code; last CUDA error text seen by this thread. */
 MOE_API const char* moe_strerror(int err);
 MOE_API const char* moe_last_cuda_error(void);
