@@ -74,6 +74,8 @@ struct Linear {
   unsigned long long* status;
 };
 cudaError_t launch_linear(const Linear& a, cudaStream_t s);
+// ... on the tensor cores: rows of whole 16-byte pieces, n a multiple of 16 if gated.
+cudaError_t launch_linear_tc(const Linear& a, int sms, cudaStream_t s);
 
 cudaError_t launch_group_routes(const int32_t* ids, int routes, int experts, int32_t* offsets,
                                 int32_t* order, int32_t* pos, cudaStream_t s);

@@ -1,0 +1,560 @@
+// linear_tc.cu -- the bf16 products on the tensor cores: out = epilogue(x w^T), dense or
+// one product per group, for operands in rows of whole 16-byte pieces.
+//
+// The weights are the MMA's 128 rows (256 with a CTA pair, CG = 2), the tokens its
+// columns: a tile takes as many tokens as are there, up to NT and a multiple of 16, so that a
+// ragged group costs what its rows cost, and one tile shape serves groups of any size.
+// A stage of the pipeline is 128 bytes of every row (64 of K, four MMAs).  CTAs (or pairs)
+// are persistent and take tiles in turn; the groups' offsets are read on the device.  Warps:
+//   0..7  epilogue: tensor memory -> bias, activation, gate, residual -> out.  Warp w reads
+//         lanes 32 (w % 4) .. (its results' n), blocks w / 4, w / 4 + 2, .. of the tokens.  Two
+//         accumulators alternate, so the next tile's MMAs run beside it;
+//   8     TMA loads: weights as boxes, tokens as boxes of 32 rows or, by the order's
+//         indices, four rows an instruction (each lane its own four);
+//   9     MMAs (the first CTA's of a pair).
+// Gated products: a CTA's 128 rows are 64 gate rows and their 64 up rows in runs of 16
+// (boxes of 16 gate and 16 up rows), so that lane l and lane l + 16 of a warp hold the two
+// halves of a result: of two tokens the gate lanes finish one, the up lanes the other, after
+// one exchange.
+// Sums: the tensor cores add with truncation, an error that grows with the chain of additions;
+// where the tensor memory has room the sum is taken in up to four parts of K.
+// Where tiles are few, `split` CTAs (pairs) of a cluster share a tile: each sums its part of K,
+// then its share of the rows over the parts in ascending order.
+// Every wait is bounded; on a timeout the CTA reports it, drains its copies and MMAs, frees
+// its tensor memory and returns.  A tile is stored whole and right or not at all.
+#include "linear.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+using namespace lin;
+
+constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
+
+template <int NT, int CG>
+struct Shape {
+  static constexpr int kX = NT / CG;                     // token rows a CTA loads
+  static constexpr int kStage = 128 * 128 + kX * 128;
+  static constexpr int kFit = (226 * 1024 - 2048) / kStage;
+  static constexpr int kStages = kFit > 12 ? 12 : kFit;
+  static constexpr int kChains = 256 / NT < 4 ? 256 / NT : 4;
+  static constexpr int kCols = 2 * kChains * NT;         // of tensor memory
+  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int W = 16;                            // tokens the epilogue reads at a time
+  static constexpr int kPitch = NT + 4;                  // of a split's sums
+  static_assert(kCols <= 512 && (kCols & (kCols - 1)) == 0 && kStage % 1024 == 0, "tile shape");
+  static_assert(kStages * kStage >= 128 * kPitch * 4 * (CG == 1 ? 7 : 6) / 4, "room for a split's sums");
+};
+
+struct Args {
+  Linear l;
+  int tn;     // tiles of n
+  int nk;     // stages of K
+  int split;  // parts of K
+};
+
+template <int ST>
+struct Ctl {
+  uint64_t full[ST], empty[ST];
+  uint64_t acc_full[2], acc_empty[2], drain, sums;
+  uint32_t tmem;
+  int abort_flag, epi_ok[2];  // epi_ok: the epilogue's wait, by tile parity
+};
+
+#define MOE_LIN_LOAD(cg, dim, coords)                                                             \
+  asm volatile("cp.async.bulk.tensor." dim cg ".mbarrier::complete_tx::bytes [%0], [%1, {" coords \
+               "}], [%2];"
+// rows n .. n + 127 of a group's weights
+template <int CG>
+__device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, int x, int n, int g, uint32_t bar) {
+  if constexpr (CG == 1)
+    MOE_LIN_LOAD(".shared::cluster.global", "3d", "%3, %4, %5")
+    ::"r"(sa(dst)), "l"(map), "r"(bar), "r"(x), "r"(n), "r"(g) : "memory");
+  else
+    MOE_LIN_LOAD(".cta_group::2.shared::cluster.global", "3d", "%3, %4, %5")
+    ::"r"(sa(dst)), "l"(map), "r"(bar), "r"(x), "r"(n), "r"(g) : "memory");
+}
+// 16 gate rows and their 16 up rows; c: n / 16
+template <int CG>
+__device__ __forceinline__ void load_gated(void* dst, const CUtensorMap* map, int x, int c, int g, uint32_t bar) {
+  if constexpr (CG == 1)
+    MOE_LIN_LOAD(".shared::cluster.global", "5d", "%3, %4, %5, %6, %7")
+    ::"r"(sa(dst)), "l"(map), "r"(bar), "r"(x), "r"(0), "r"(c), "r"(0), "r"(g) : "memory");
+  else
+    MOE_LIN_LOAD(".cta_group::2.shared::cluster.global", "5d", "%3, %4, %5, %6, %7")
+    ::"r"(sa(dst)), "l"(map), "r"(bar), "r"(x), "r"(0), "r"(c), "r"(0), "r"(g) : "memory");
+}
+// four rows of x anywhere
+template <int CG>
+__device__ __forceinline__ void load_four(uint32_t dst, const CUtensorMap* map, int x, const int (&r)[4],
+                                          uint32_t bar) {
+  if constexpr (CG == 1)
+    MOE_LIN_LOAD(".shared::cluster.global.tile::gather4", "2d", "%3, %4, %5, %6, %7")
+    ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+  else
+    MOE_LIN_LOAD(".cta_group::2.shared::cluster.global.tile::gather4", "2d", "%3, %4, %5, %6, %7")
+    ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+#undef MOE_LIN_LOAD
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t w, uint64_t x, uint32_t id, uint32_t acc) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(w), "l"(x), "r"(id), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(w), "l"(x), "r"(id), "r"(acc)
+        : "memory");
+}
+// bf16 operands, both K-major, fp32 sums, m x n
+__device__ __forceinline__ uint32_t idesc(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// W tokens of the warp's lanes, the sums of n_chains parts of K added up in order
+template <int NT, int W>
+__device__ __forceinline__ void read_sums(uint32_t at, int n_chains, uint32_t (&v)[W]) {
+  uint32_t u[W];
+  tmem_ld(at, v);
+  if (n_chains > 1) tmem_ld(at + NT, u);
+  tmem_wait_ld();
+  for (int k = 1; k < n_chains; ++k) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+    if (k + 1 < n_chains) {
+      tmem_ld(at + (k + 1) * NT, u);
+      tmem_wait_ld();
+    }
+  }
+}
+
+// Where a lane's results go: column n, the rows' base
+template <typename T>
+__device__ __forceinline__ float get(const T* p) {
+  if constexpr (sizeof(T) == 4) return *p;
+  else return __bfloat162float(*p);
+}
+template <typename T>
+__device__ __forceinline__ void put(T* p, float v) {
+  if constexpr (sizeof(T) == 4) *p = v;
+  else *p = __float2bfloat16_rn(v);
+}
+
+// One block of W tokens: rows row .. of those in `mask`, results of this lane's n (nmax: n < l.n).
+template <typename T, bool GATED, int W, typename A>
+__device__ __forceinline__ void finish_block(const Linear& l, A act, const uint32_t (&v)[W], long long row,
+                                             uint32_t mask, long long n, bool in, float bias) {
+  const int lane = threadIdx.x & 31;
+  T* out = static_cast<T*>(l.out) + row * l.out_stride + n;
+  const T* res = l.res ? static_cast<const T*>(l.res) + row * l.res_stride + n : nullptr;
+  if constexpr (!GATED) {
+    float r[W];
+    if (res) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) r[i] = in && (mask >> i & 1) ? get(res + i * l.res_stride) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float y = act(__uint_as_float(v[i]) + bias);
+      const float o = res ? fmaf(l.alpha, y, r[i]) : l.alpha * y;
+      if (in && (mask >> i & 1)) put(out + i * l.out_stride, o);
+    }
+  } else {
+    const int up = lane >> 4;  // gate lanes take the even tokens, up lanes the odd ones
+    float r[W / 2];
+    if (res) {
+#pragma unroll
+      for (int i = 0; i < W; i += 2)
+        r[i / 2] = in && (mask >> (i + up) & 1) ? get(res + (i + up) * l.res_stride) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float a = __uint_as_float(v[i]) + bias, b = __uint_as_float(v[i + 1]) + bias;
+      const float got = __shfl_xor_sync(kAll, up ? a : b, 16);
+      const float y = act(up ? got : a) * (up ? b : got);
+      const float o = res ? fmaf(l.alpha, y, r[i / 2]) : l.alpha * y;
+      if (in && (mask >> (i + up) & 1)) put(out + (i + up) * l.out_stride, o);
+    }
+  }
+}
+
+template <int NT, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+              const __grid_constant__ Args a) {
+  using S = Shape<NT, CG>;
+  constexpr int ST = S::kStages, W = S::W;
+  extern __shared__ uint8_t raw[];
+  uint8_t* stg = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Ctl<ST> c;
+  const Linear& l = a.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // cluster: `split` parts of K, each CG CTAs; a lone CTA's cluster is itself
+  const int crank = CG == 1 && a.split == 1 ? 0 : (int)cluster_rank();
+  const int pair = crank % CG, first = crank - pair, part = crank / CG;
+  const int team = CG * a.split;
+  const int k_lo = (int)((long long)a.nk * part / a.split), k_hi = (int)((long long)a.nk * (part + 1) / a.split);
+  const int n_k = k_hi - k_lo, n_chains = min(S::kChains, n_k);
+  const int tile0 = blockIdx.x / team, step = gridDim.x / team;
+  const uint16_t both = (uint16_t)(((1 << CG) - 1) << first);
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&c.full[i], 1);
+      mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.acc_full[i], 1);
+      mbar_init(&c.acc_empty[i], kEpiWarps * CG);
+    }
+    mbar_init(&c.drain, 1);
+    mbar_init(&c.sums, 1);
+    c.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc<CG>(&c.tmem, S::kCols);
+  fence_before();
+  __syncthreads();
+  if (CG > 1) cluster_sync();  // the peer's barriers exist before anything arrives there
+  else if (a.split > 1) cluster_arrive();  // waited for before anything goes to a peer
+  fence_after();
+  const uint32_t tmem = c.tmem;
+  pdl_wait();
+
+  // the part of a tile's tokens that a CTA loads, a multiple of 8
+  auto half = [](int rows) { return (rows + 15) / 16 * 16 / CG; };
+  Walk walk;
+  Tile t;
+  constexpr int kShift = NT == 32 ? 5 : NT == 128 ? 7 : 8;
+  static_assert(NT == 1 << kShift, "tokens of a tile");
+  if (warp != kTmaWarp && warp != kMmaWarp && a.split > 1) {
+    // a split's sums are exchanged below
+  } else {
+    walk.start(l, kShift, 16, a.tn);
+  }
+
+  if (warp == kTmaWarp) {
+    int it = 0, s = 0;
+    bool ok = true;
+    for (int i = tile0; ok && walk.seek(i, t); i += step) {
+      const int hx = half(t.rows), boxes = (hx + 31) / 32;
+      const int bytes = CG * (128 * 128 + (l.order ? hx * 128 : boxes * 4096));
+      const int x0 = t.row + pair * hx;
+      int src[4] = {0, 0, 0, 0};
+      if (l.order) {  // places without a row load row 0, and are not stored
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (pair * hx + 4 * lane + j < t.rows) src[j] = max(source_row(l, x0 + 4 * lane + j), 0);
+      }
+      for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
+        if (it >= ST && !warp_wait(&c.empty[s], (it / ST - 1) & 1, &c.abort_flag, a.l.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* p = stg + (size_t)s * S::kStage;
+        const int x = ks * 64;
+        const uint32_t bar = CG == 1 ? sa(&c.full[s]) : peer_addr(sa(&c.full[s]), first);
+        if (elect_one()) {
+          // a pair's copies all count on the first CTA's barrier
+          if (pair == 0) mbar_expect(&c.full[s], bytes);
+          const int nt = t.n * CG + pair;
+          if (l.gated) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_gated<CG>(p + j * 4096, &wmap, x, nt * 4 + j, t.group, bar);
+          } else {
+            load_rows<CG>(p, &wmap, x, nt * 128, t.group, bar);
+          }
+          if (!l.order)
+            for (int j = 0; j < boxes; ++j)
+              tma_load<CG>(p + 128 * 128 + j * 4096, &xmap, x, x0 + 32 * j, bar);
+        }
+        __syncwarp();
+        if (l.order) {
+          if (4 * lane < hx) load_four<CG>(sa(p) + 128 * 128 + lane * 512, &xmap, x, src, bar);
+          __syncwarp();
+        }
+        s = s + 1 == ST ? 0 : s + 1;
+      }
+    }
+    // the copies in flight land before the CTA ends, whichever warp may have given up
+    if (pair == 0)
+      for (int i = it > ST ? it - ST : 0; i < it; ++i)
+        if (!drain_bar(&c.full[i % ST], (i / ST) & 1)) break;
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (pair == 0) {
+      int u = 0, s = 0;
+      uint32_t full_par = 0;
+      bool ok = true;
+      const uint64_t w_base = desc_tile(sa(stg)), x_base = desc_tile(sa(stg) + 128 * 128);
+      for (int i = tile0; ok && walk.seek(i, t); i += step, ++u) {
+        const int b = u & 1;
+        if (u >= 2 && !warp_wait(&c.acc_empty[b], (u / 2 - 1) & 1, &c.abort_flag, a.l.status)) break;
+        const uint32_t id = idesc(128 * CG, half(t.rows) * CG);
+        uint32_t d = tmem + b * S::kChains * NT;
+        int chain = 0, first_of = 0;  // the part of K being summed, its first stage
+        for (int k = 0; k < n_k; ++k) {
+          if (S::kChains > 1 && k == n_k * (chain + 1) / n_chains) {
+            ++chain;
+            first_of = k;
+            d += NT;
+          }
+          if (!warp_wait(&c.full[s], full_par, &c.abort_flag, a.l.status)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          if (elect_one()) {
+            const uint64_t w0 = w_base + (uint64_t)(s * (S::kStage / 16)), x0 = x_base + (uint64_t)(s * (S::kStage / 16));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // 32 bytes of every row each
+              mma<CG>(d, w0 + 2 * j, x0 + 2 * j, id, j > 0 || k > first_of);
+            mma_commit<CG>(&c.empty[s], both);
+          }
+          __syncwarp();
+          if (++s == ST) s = 0, full_par ^= 1;
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit<CG>(&c.acc_full[b], both);
+        __syncwarp();
+      }
+      if (elect_one()) mma_commit<CG>(&c.drain, both);
+      __syncwarp();
+    }
+    drain_bar(&c.drain, 0);  // every MMA has finished before the tensor memory is freed
+    __syncwarp();
+  } else if (a.split > 1) {
+    if (threadIdx.x == 0) c.epi_ok[0] = wait_bar(&c.acc_full[0], 0, &c.abort_flag, a.l.status);
+    __syncwarp();
+  } else {
+    int u = 0;
+    const int quarter = warp & 3;
+    for (int i = tile0; walk.seek(i, t); i += step, ++u) {
+      const int b = u & 1;
+      const long long n = l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter + (lane & 15)
+                                  : ((long long)t.n * CG + pair) * 128 + 32 * quarter + lane;
+      const bool in = n < l.n;
+      float bias = 0.f;
+      if (l.bias && in)
+        bias = __bfloat162float(l.gated ? l.bias[((long long)t.group * 2 + (lane >> 4)) * l.n + n]
+                                        : l.bias[(long long)t.group * l.n + n]);
+      if (threadIdx.x == 0)
+        c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], (u / 2) & 1, &c.abort_flag, a.l.status);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (!c.epi_ok[u & 1]) break;
+      fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + b * S::kChains * NT;
+#pragma unroll 1
+      for (int n0 = (warp >> 2) * W; n0 < t.rows; n0 += 2 * W) {
+        const int row = t.row + n0;
+        bool here = lane < W && n0 + lane < t.rows;
+        if (here && l.order) here = source_row(l, row + lane) >= 0;
+        const uint32_t mask = __ballot_sync(kAll, here);
+        uint32_t v[W];
+        read_sums<NT>(acc + n0, n_chains, v);
+        with_act(l.act, [&](auto act) {
+          using B = __nv_bfloat16;
+          if (l.gated) {
+            if (l.f32) finish_block<float, true>(l, act, v, row, mask, n, in, bias);
+            else finish_block<B, true>(l, act, v, row, mask, n, in, bias);
+          } else {
+            if (l.f32) finish_block<float, false>(l, act, v, row, mask, n, in, bias);
+            else finish_block<B, false>(l, act, v, row, mask, n, in, bias);
+          }
+        });
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1) mbar_arrive(&c.acc_empty[b]);
+        else mbar_arrive_at(peer_addr(sa(&c.acc_empty[b]), first));
+      }
+    }
+    __syncwarp();
+  }
+  bool failed = false;
+  if (CG > 1 || a.split > 1) {
+    // a CTA that has given up tells its cluster, which gives a split tile up as one; every
+    // thread that raised the flag passes here, and nothing raises it from here on
+    if (CG == 1) cluster_wait();
+    if (*reinterpret_cast<volatile int*>(&c.abort_flag))
+      for (int k = 0; k < team; ++k) store_at(peer_addr(sa(&c.abort_flag), k), 1);
+    __syncwarp();
+    cluster_sync();
+    failed = *reinterpret_cast<volatile int*>(&c.abort_flag);
+    // a pair's copies count on its first CTA's barriers, which may have been left by then:
+    // a copy takes microseconds, so both CTAs stay half a millisecond
+    if (CG > 1 && failed) {
+      for (const long long t0 = clock64(); clock64() - t0 < 1000 * 1000;) {
+      }
+      cluster_sync();
+    }
+  }
+  if (a.split > 1 && !failed) {
+    // One tile per cluster (of a dense product), its operands done with everywhere.  Every part
+    // lays its sums out in rows and copies each peer the rows that the peer adds up.
+    constexpr int kPitch = S::kPitch;
+    const int rows_per = 128 / a.split, bytes = rows_per * kPitch * 4;
+    float* own = reinterpret_cast<float*>(stg);  // [128][kPitch], then [split - 1][rows_per][kPitch]
+    float* in = own + 128 * kPitch;
+    if (warp < kEpiWarps) {
+      fence_after();
+      const int pr = 32 * (warp & 3) + lane;
+      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll 1
+      for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
+        uint32_t v[W];
+        read_sums<NT>(acc + n0, n_chains, v);
+#pragma unroll
+        for (int i = 0; i < W; i += 4)
+          *reinterpret_cast<uint4*>(own + pr * kPitch + n0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+      fence_before();
+      fence_async_smem();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (warp == 0 && elect_one()) {
+        mbar_expect(&c.sums, (a.split - 1) * bytes);
+        for (int k = 0; k < a.split; ++k) {  // peer k keeps what it gets from part p at p, without itself
+          if (k == part) continue;
+          const int rank = k * CG + pair, at = part < k ? part : part - 1;
+          copy_to_peer(peer_addr(sa(in + at * rows_per * kPitch), rank), own + k * rows_per * kPitch, bytes,
+                       peer_addr(sa(&c.sums), rank));
+        }
+      }
+    }
+    // the peers' copies are under way to this CTA: no flag ends this wait
+    const bool here = drain_bar(&c.sums, 0);
+    if (!here && a.l.status) atomicOr(a.l.status, (unsigned long long)MOE_STATUS_TIMEOUT);
+    __syncthreads();
+    cluster_arrive();  // what the peers copied here has left their shared memory
+    walk.start(l, kShift, 16, a.tn);
+    if (here && walk.seek(tile0, t)) {
+      auto sum = [&](int row, int col) {  // a row of this part's, over the parts
+        float v = 0.f;
+        for (int k = 0; k < a.split; ++k)
+          v += k == part ? own[(part * rows_per + row) * kPitch + col]
+                         : in[((k < part ? k : k - 1) * rows_per + row) * kPitch + col];
+        return v;
+      };
+      const long long tn = (long long)t.n * CG + pair;
+      with_act(l.act, [&](auto act) {
+        // neighbouring threads take neighbouring rows: results of one token
+        if (l.gated) {
+          const int per = rows_per / 2;
+          for (int i = threadIdx.x; i < t.rows * per; i += kThreads) {
+            const int r = i % per, col = i / per;
+            const long long n = tn * 64 + part * per + r;
+            if (n >= l.n) continue;
+            float g = sum(r / 16 * 32 + r % 16, col), up = sum(r / 16 * 32 + 16 + r % 16, col);
+            if (l.bias) g += __bfloat162float(l.bias[n]), up += __bfloat162float(l.bias[l.n + n]);
+            finish(l, t.row + col, n, act(g) * up);
+          }
+        } else {
+          for (int i = threadIdx.x; i < t.rows * rows_per; i += kThreads) {
+            const int r = i % rows_per, col = i / rows_per;
+            const long long n = tn * 128 + part * rows_per + r;
+            if (n >= l.n) continue;
+            float v = sum(r, col);
+            if (l.bias) v += __bfloat162float(l.bias[n]);
+            finish(l, t.row + col, n, act(v));
+          }
+        }
+      });
+    }
+    __syncwarp();
+    cluster_wait();  // this CTA's copies have left its shared memory
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    fence_after();
+    tmem_free<CG>(tmem, S::kCols);
+  }
+}
+
+// Parts of K that give every SM a CTA where tiles are few.
+int split_for(long long tiles, int nk, int cg, int sms) {
+  int s = 1;
+  while (2 * s <= kMaxCluster / cg && 2 * s <= nk && tiles * cg * 2 * s <= sms) s *= 2;
+  return s;
+}
+
+long long tiles_n(const Linear& l, int cg) {
+  const int per = (l.gated ? 64 : 128) * cg;
+  return (l.n + (long long)per - 1) / per;
+}
+
+template <int NT, int CG>
+cudaError_t launch(const Linear& l, int sms, cudaStream_t s) {
+  using S = Shape<NT, CG>;
+  auto kern = linear_kernel<NT, CG>;
+  static Once once;
+  cudaError_t e = raise_smem(once, kern, S::kSmem);
+  if (e != cudaSuccess) return e;
+  Args a{};
+  a.l = l;
+  const long long tn = tiles_n(l, CG);
+  constexpr int kShift = NT == 32 ? 5 : NT == 128 ? 7 : 8;
+  const long long most = l.offsets ? most_tiles(l, kShift, tn) : (l.rows + (long long)NT - 1) / NT * tn;
+  if (most > 0x3fffffff) return cudaErrorInvalidValue;
+  a.tn = (int)tn;
+  a.nk = (int)((l.k + 63ll) / 64);
+  a.split = l.offsets ? 1 : split_for(most, a.nk, CG, sms);
+  const int team = CG * a.split;
+  CUtensorMap wm, xm;
+  e = make_weight_map(&wm, l.w, l.gated, l.k, l.n, l.w_stride * 2, l.groups, l.group_stride * 2);
+  if (e == cudaSuccess) e = make_map(&xm, l.x, 2, l.k, l.x_rows, l.x_stride * 2, l.order ? 1 : 32);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  const long long teams = most < sms / team ? most : sms / team;
+  cfg.gridDim = dim3((unsigned)(teams * team));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)team, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, wm, xm, a);
+}
+
+// Estimated cycles of a dense product with this tile: a stage's MMAs take 2 cycles per token, its
+// copies a cycle per 64 bytes.
+template <int NT, int CG>
+long long cycles(const Linear& l, int sms) {
+  const long long tm = (l.rows + (long long)NT - 1) / NT, tiles = tm * tiles_n(l, CG);
+  const int nk = (int)((l.k + 63ll) / 64), split = split_for(tiles, nk, CG, sms);
+  const int width = (int)(((l.rows + tm - 1) / tm + 15) / 16 * 16);
+  const int copies = (128 * 128 + width / CG * 128) / 64, stage = 2 * width > copies ? 2 * width : copies;
+  const long long per = sms / (CG * split), waves = (tiles + per - 1) / per;
+  return waves * ((nk + split - 1) / split * (long long)stage) + (split > 1 ? 2500 + 128 * NT * 4 / 18 : 0);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_tc(const Linear& l, int sms, cudaStream_t s) {
+  if (l.offsets) {
+    // rows a group has on average decide; ragged sizes fill either tile as they come
+    if (l.rows / l.groups < 24) return launch<32, 1>(l, sms, s);
+    return launch<256, 2>(l, sms, s);
+  }
+  if (l.rows <= 32) return launch<32, 1>(l, sms, s);
+  const long long c32 = cycles<32, 1>(l, sms), c128 = cycles<128, 1>(l, sms), c256 = cycles<256, 2>(l, sms);
+  if (c256 <= c128 && c256 <= c32) return launch<256, 2>(l, sms, s);
+  return c128 <= c32 ? launch<128, 1>(l, sms, s) : launch<32, 1>(l, sms, s);
+}
+
+}  // namespace moe

@@ -307,6 +307,12 @@ cudaError_t make_map(CUtensorMap* map, const void* base, int elem, long long wid
 cudaError_t make_scale_map(CUtensorMap* map, const void* base, long long row_bytes, long long rows,
                            int box_rows);
 
+// Maps of `groups` matrices of bf16 rows, group_bytes apart, 128-byte swizzle: boxes of 64
+// elements x 128 rows {k, n, groups}; gated, of 64 elements x 16 gate rows and their
+// 16 up rows {k, 16, n / 16, 2, groups} (n a multiple of 16).
+cudaError_t make_weight_map(CUtensorMap* map, const void* base, bool gated, long long k, long long n,
+                            long long row_bytes, long long groups, long long group_bytes);
+
 // A map of an output matrix of bf16 or fp32 in tiles of 32 x 32, 64- or 128-byte
 // swizzle (rows a multiple of 16 bytes apart; base 16-byte aligned).
 cudaError_t make_out_map(CUtensorMap* map, void* base, bool f32, long long width, long long rows,

@@ -56,6 +56,21 @@ cudaError_t make_scale_map(CUtensorMap* map, const void* base, long long row_byt
                 CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+cudaError_t make_weight_map(CUtensorMap* map, const void* base, bool gated, long long k, long long n,
+                            long long row_bytes, long long groups, long long group_bytes) {
+  const Encode f = encoder();
+  if (!f) return cudaErrorNotSupported;
+  const cuuint64_t K = k, N = n, G = groups, rb = row_bytes, gb = group_bytes;
+  const cuuint64_t dims3[3] = {K, N, G}, strides3[2] = {rb, gb};
+  const cuuint64_t dims5[5] = {K, 16, N / 16, 2, G}, strides5[4] = {rb, 16 * rb, N * rb, gb};
+  const cuuint32_t box3[3] = {64, 128, 1}, box5[5] = {64, 16, 1, 2, 1}, step[5] = {1, 1, 1, 1, 1};
+  const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, gated ? 5 : 3, const_cast<void*>(base),
+                       gated ? dims5 : dims3, gated ? strides5 : strides3, gated ? box5 : box3, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_out_map(CUtensorMap* map, void* base, bool f32, long long width, long long rows,
                          long long row_bytes) {
   return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, width,
