@@ -97,7 +97,9 @@ cudaError_t launch_linear(const Linear& l, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool whole = l.k % 8 == 0 && l.x_stride % 8 == 0 && l.w_stride % 8 == 0 && l.group_stride % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
-  if (whole && (!l.gated || l.n % 16 == 0)) return launch_linear_tc(l, d.sms, s);
+  // gathered rows are addressed in 32 bits of 16-byte pieces
+  const bool near = !l.order || (double)l.x_rows * l.x_stride / 8 < 4294967296.0;
+  if (whole && near && (!l.gated || l.n % 16 == 0)) return launch_linear_tc(l, d.sms, s);
   return l.gated ? launch_tiles<true>(l, d.sms, s) : launch_tiles<false>(l, d.sms, s);
 }
 

@@ -9,9 +9,9 @@
 //   0..7  epilogue: tensor memory -> bias, activation, gate, residual -> out.  Warp w reads
 //         lanes 32 (w % 4) .. (its results' n), blocks w / 4, w / 4 + 2, .. of the tokens.  Two
 //         accumulators alternate, so the next tile's MMAs run beside it;
-//   8     TMA loads: weights as boxes, tokens as boxes of 32 rows or, by the order's
-//         indices, four rows an instruction (each lane its own four);
-//   9     MMAs (the first CTA's of a pair).
+//   8     TMA loads: weights as boxes, tokens as boxes of 32 rows;
+//   9     MMAs (the first CTA's of a pair);
+//   10,11 tokens by the order's indices, where there is one.
 // Gated products: a CTA's 128 rows are 64 gate rows and their 64 up rows in runs of 16
 // (boxes of 16 gate and 16 up rows), so that lane l and lane l + 16 of a warp hold the two
 // halves of a result: of two tokens the gate lanes finish one, the up lanes the other, after
@@ -31,22 +31,22 @@ namespace {
 using namespace tc;
 using namespace lin;
 
-constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kGatherWarp = 10, kThreads = 384;
 constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
 
 template <int NT, int CG>
 struct Shape {
   static constexpr int kX = NT / CG;                     // token rows a CTA loads
   static constexpr int kStage = 128 * 128 + kX * 128;
-  static constexpr int kFit = (226 * 1024 - 2048) / kStage;
+  static constexpr int kTurn = kEpiWarps * 2048;         // the epilogue's
+  static constexpr int kFit = (226 * 1024 - 2048 - kTurn) / kStage;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr int kChains = 256 / NT < 4 ? 256 / NT : 4;
   static constexpr int kCols = 2 * kChains * NT;         // of tensor memory
-  static constexpr int kSmem = kStages * kStage + 1024;
-  static constexpr int W = 16;                            // tokens the epilogue reads at a time
+  static constexpr int kSmem = kStages * kStage + kTurn + 1024;
   static constexpr int kPitch = NT + 4;                  // of a split's sums
   static_assert(kCols <= 512 && (kCols & (kCols - 1)) == 0 && kStage % 1024 == 0, "tile shape");
-  static_assert(kStages * kStage >= 128 * kPitch * 4 * (CG == 1 ? 7 : 6) / 4, "room for a split's sums");
+  static_assert(kStages * kStage + kTurn >= 128 * kPitch * 4 * (CG == 1 ? 7 : 6) / 4, "room for a split's sums");
 };
 
 struct Args {
@@ -54,11 +54,12 @@ struct Args {
   int tn;     // tiles of n
   int nk;     // stages of K
   int split;  // parts of K
+  int wide;   // four neighbouring results of out and res are one aligned access
 };
 
 template <int ST>
 struct Ctl {
-  uint64_t full[ST], empty[ST];
+  uint64_t full[ST], empty[ST], landed[ST];  // landed: gathered rows of x
   uint64_t acc_full[2], acc_empty[2], drain, sums;
   uint32_t tmem;
   int abort_flag, epi_ok[2];  // epi_ok: the epilogue's wait, by tile parity
@@ -87,19 +88,16 @@ __device__ __forceinline__ void load_gated(void* dst, const CUtensorMap* map, in
     MOE_LIN_LOAD(".cta_group::2.shared::cluster.global", "5d", "%3, %4, %5, %6, %7")
     ::"r"(sa(dst)), "l"(map), "r"(bar), "r"(x), "r"(0), "r"(c), "r"(0), "r"(g) : "memory");
 }
-// four rows of x anywhere
-template <int CG>
-__device__ __forceinline__ void load_four(uint32_t dst, const CUtensorMap* map, int x, const int (&r)[4],
-                                          uint32_t bar) {
-  if constexpr (CG == 1)
-    MOE_LIN_LOAD(".shared::cluster.global.tile::gather4", "2d", "%3, %4, %5, %6, %7")
-    ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-  else
-    MOE_LIN_LOAD(".cta_group::2.shared::cluster.global.tile::gather4", "2d", "%3, %4, %5, %6, %7")
-    ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-}
 #undef MOE_LIN_LOAD
 
+// 16 bytes (or zeros) to shared memory; an arrival once all such copies of this thread have landed
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t w, uint64_t x, uint32_t id, uint32_t acc) {
   if constexpr (CG == 1)
@@ -137,62 +135,110 @@ __device__ __forceinline__ void read_sums(uint32_t at, int n_chains, uint32_t (&
   }
 }
 
-// Where a lane's results go: column n, the rows' base
-template <typename T>
-__device__ __forceinline__ float get(const T* p) {
-  if constexpr (sizeof(T) == 4) return *p;
-  else return __bfloat162float(*p);
-}
-template <typename T>
-__device__ __forceinline__ void put(T* p, float v) {
-  if constexpr (sizeof(T) == 4) *p = v;
-  else *p = __float2bfloat16_rn(v);
-}
-
-// One block of W tokens: rows row .. of those in `mask`, results of this lane's n (nmax: n < l.n).
-template <typename T, bool GATED, int W, typename A>
-__device__ __forceinline__ void finish_block(const Linear& l, A act, const uint32_t (&v)[W], long long row,
-                                             uint32_t mask, long long n, bool in, float bias) {
-  const int lane = threadIdx.x & 31;
-  T* out = static_cast<T*>(l.out) + row * l.out_stride + n;
-  const T* res = l.res ? static_cast<const T*>(l.res) + row * l.res_stride + n : nullptr;
-  if constexpr (!GATED) {
-    float r[W];
-    if (res) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) r[i] = in && (mask >> i & 1) ? get(res + i * l.res_stride) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float y = act(__uint_as_float(v[i]) + bias);
-      const float o = res ? fmaf(l.alpha, y, r[i]) : l.alpha * y;
-      if (in && (mask >> i & 1)) put(out + i * l.out_stride, o);
+// Four neighbouring results of a row: from and to memory, whole where `wide` (aligned,
+// none past n), else those below n.  A residual stays in the bits it was loaded in until it
+// is used, so that a load ahead is not waited for.
+__device__ __forceinline__ void get4(const Linear& l, bool wide, long long at, int left, uint32_t (&v)[4]) {
+  if (wide) {
+    if (l.f32) {
+      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const float*>(l.res) + at);
+      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(l.res) + at);
+      v[0] = q.x, v[1] = q.y;
     }
   } else {
-    const int up = lane >> 4;  // gate lanes take the even tokens, up lanes the odd ones
-    float r[W / 2];
-    if (res) {
 #pragma unroll
-      for (int i = 0; i < W; i += 2)
-        r[i / 2] = in && (mask >> (i + up) & 1) ? get(res + (i + up) * l.res_stride) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < W; i += 2) {
-      const float a = __uint_as_float(v[i]) + bias, b = __uint_as_float(v[i + 1]) + bias;
-      const float got = __shfl_xor_sync(kAll, up ? a : b, 16);
-      const float y = act(up ? got : a) * (up ? b : got);
-      const float o = res ? fmaf(l.alpha, y, r[i / 2]) : l.alpha * y;
-      if (in && (mask >> (i + up) & 1)) put(out + (i + up) * l.out_stride, o);
-    }
+    for (int j = 0; j < 4; ++j) v[j] = j < left ? __float_as_uint(load_res(l, at + j)) : 0u;
   }
 }
+__device__ __forceinline__ float res_of(const uint32_t (&v)[4], bool packed, int j) {
+  if (!packed) return __uint_as_float(v[j]);
+  return __uint_as_float(j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void put4(const Linear& l, bool wide, long long at, int left, const float (&v)[4]) {
+  if (wide) {
+    if (l.f32) *reinterpret_cast<float4*>(static_cast<float*>(l.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(l.out) + at) =
+          make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < left) store_out(l, at + j, v[j]);
+  }
+}
+
+// The epilogue of a warp: blocks of 16 tokens, its 32 lanes' sums turned in shared memory so that
+// a lane finishes four neighbouring results of a token (1 store of 8 or 16 bytes, and as
+// large a load of the residual, for four scattered ones).  Rows of 32 floats; odd tokens
+// have their halves exchanged, which keeps the reads of 16 gate or up sums off each other's banks.
+struct Epilogue {
+  const Linear& l;
+  float* buf;       // [16][32]
+  int lane, token;  // first token of the lane's: token, token + step, ..
+  int col, left;    // first of the lane's four results in the warp's row of sums; results that are below n
+  long long n;      // and in out
+  bool wide;
+  float bias[4], ubias[4];
+
+  // n0: first result of the warp's lanes
+  __device__ __forceinline__ void start(long long n0, int group, bool aligned) {
+    const int q = l.gated ? lane & 3 : lane & 7;
+    token = l.gated ? lane >> 2 : lane >> 3;
+    col = 4 * q;
+    n = n0 + col;
+    left = (int)max(0ll, min(4ll, l.n - n));
+    wide = aligned && left == 4;
+    const __nv_bfloat16* b = l.bias ? l.bias + (long long)group * l.n * (l.gated ? 2 : 1) + n : nullptr;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bias[j] = b && j < left ? __bfloat162float(b[j]) : 0.f;
+      ubias[j] = b && l.gated && j < left ? __bfloat162float(b[l.n + j]) : 0.f;
+    }
+  }
+  // the residual of the lane's results of a block
+  __device__ __forceinline__ void fetch(long long row, uint32_t mask, uint32_t (&r)[4][4]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = l.gated ? token + 8 * k : token + 4 * k;
+      if (k < (l.gated ? 2 : 4) && (mask >> t & 1) && left > 0) get4(l, wide, (row + t) * l.res_stride + n, left, r[k]);
+    }
+  }
+  __device__ __forceinline__ void turn(const uint32_t (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) buf[i * 32 + (lane ^ (i & 1 ? 16 : 0))] = __uint_as_float(v[i]);
+  }
+  template <bool GATED, typename A>
+  __device__ __forceinline__ void finish(A act, long long row, uint32_t mask, const uint32_t (&r)[4][4]) const {
+#pragma unroll
+    for (int k = 0; k < (GATED ? 2 : 4); ++k) {
+      const int t = GATED ? token + 8 * k : token + 4 * k;
+      const float* z = buf + t * 32;
+      const int turned = t & 1 ? 16 : 0;
+      const float4 g = *reinterpret_cast<const float4*>(z + (col ^ turned));
+      float y[4] = {act(g.x + bias[0]), act(g.y + bias[1]), act(g.z + bias[2]), act(g.w + bias[3])};
+      if (GATED) {
+        const float4 u = *reinterpret_cast<const float4*>(z + ((16 + col) ^ turned));
+        y[0] *= u.x + ubias[0], y[1] *= u.y + ubias[1], y[2] *= u.z + ubias[2], y[3] *= u.w + ubias[3];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = l.res ? fmaf(l.alpha, y[j], res_of(r[k], wide && !l.f32, j)) : l.alpha * y[j];
+      if ((mask >> t & 1) && left > 0) put4(l, wide, (row + t) * l.out_stride + n, left, y);
+    }
+  }
+};
 
 template <int NT, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
               const __grid_constant__ Args a) {
   using S = Shape<NT, CG>;
-  constexpr int ST = S::kStages, W = S::W;
+  constexpr int ST = S::kStages, W = 16;
   extern __shared__ uint8_t raw[];
   uint8_t* stg = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ Ctl<ST> c;
@@ -210,8 +256,9 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&c.full[i], 1);
+      mbar_init(&c.full[i], l.order ? CG : 1);  // with the second CTA's gathered rows handed on
       mbar_init(&c.empty[i], 1);
+      mbar_init(&c.landed[i], 64);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.acc_full[i], 1);
@@ -237,7 +284,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   Tile t;
   constexpr int kShift = NT == 32 ? 5 : NT == 128 ? 7 : 8;
   static_assert(NT == 1 << kShift, "tokens of a tile");
-  if (warp != kTmaWarp && warp != kMmaWarp && a.split > 1) {
+  if (warp < kEpiWarps && a.split > 1) {
     // a split's sums are exchanged below
   } else {
     walk.start(l, kShift, 16, a.tn);
@@ -247,15 +294,9 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     int it = 0, s = 0;
     bool ok = true;
     for (int i = tile0; ok && walk.seek(i, t); i += step) {
-      const int hx = half(t.rows), boxes = (hx + 31) / 32;
-      const int bytes = CG * (128 * 128 + (l.order ? hx * 128 : boxes * 4096));
+      const int hx = half(t.rows), boxes = l.order ? 0 : (hx + 31) / 32;
+      const int bytes = CG * (128 * 128 + boxes * 4096);
       const int x0 = t.row + pair * hx;
-      int src[4] = {0, 0, 0, 0};
-      if (l.order) {  // places without a row load row 0, and are not stored
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (pair * hx + 4 * lane + j < t.rows) src[j] = max(source_row(l, x0 + 4 * lane + j), 0);
-      }
       for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
         if (it >= ST && !warp_wait(&c.empty[s], (it / ST - 1) & 1, &c.abort_flag, a.l.status)) {
           ok = false;
@@ -274,15 +315,10 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           } else {
             load_rows<CG>(p, &wmap, x, nt * 128, t.group, bar);
           }
-          if (!l.order)
-            for (int j = 0; j < boxes; ++j)
-              tma_load<CG>(p + 128 * 128 + j * 4096, &xmap, x, x0 + 32 * j, bar);
+          for (int j = 0; j < boxes; ++j)
+            tma_load<CG>(p + 128 * 128 + j * 4096, &xmap, x, x0 + 32 * j, bar);
         }
         __syncwarp();
-        if (l.order) {
-          if (4 * lane < hx) load_four<CG>(sa(p) + 128 * 128 + lane * 512, &xmap, x, src, bar);
-          __syncwarp();
-        }
         s = s + 1 == ST ? 0 : s + 1;
       }
     }
@@ -309,9 +345,14 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
             first_of = k;
             d += NT;
           }
-          if (!warp_wait(&c.full[s], full_par, &c.abort_flag, a.l.status)) {
+          if ((l.order && !warp_wait(&c.landed[s], full_par, &c.abort_flag, a.l.status)) ||
+              !warp_wait(&c.full[s], full_par, &c.abort_flag, a.l.status)) {
             ok = false;
             break;
+          }
+          if (l.order) {
+            fence_async_smem();
+            __syncwarp();
           }
           fence_after();
           if (elect_one()) {
@@ -330,8 +371,66 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       }
       if (elect_one()) mma_commit<CG>(&c.drain, both);
       __syncwarp();
+    } else if (l.order) {
+      // The second CTA's gathered rows, fenced and handed on to the first.  The arrival is the default one:
+      // with .release.cluster it took 2,000 cycles beside copies in flight, four times a stage
+      // (65,536 x 1,024 x 2,048 in 256 groups: 564 us, so 284); the rows are in this CTA's shared memory, in order
+      // for its MMAs by the fence.
+      int s = 0;
+      uint32_t par = 0;
+      bool ok = true;
+      for (int i = tile0; ok && walk.seek(i, t); i += step)
+        for (int k = 0; ok && k < n_k; ++k) {
+          ok = warp_wait(&c.landed[s], par, &c.abort_flag, a.l.status);
+          fence_async_smem();
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive_at(peer_addr(sa(&c.full[s]), first));
+          if (++s == ST) s = 0, par ^= 1;
+        }
+      __syncwarp();
     }
     drain_bar(&c.drain, 0);  // every MMA has finished before the tensor memory is freed
+    __syncwarp();
+  } else if (warp >= kGatherWarp) {
+    // Rows of x by the order's indices: 16 bytes a lane, four rows a warp and instruction, in the
+    // copies' swizzle.  A thread's copies arrive at `landed` by themselves; the warp that waits
+    // there fences them for the MMAs.  (TMA's four-row gathers took about 70 cycles each, 2,200 a
+    // stage of 128 rows; a fence by the copying threads waits for all their copies in flight.)
+    if (l.order) {
+      constexpr int kPer = S::kX / 8;  // rows of a lane
+      const int gw = warp - kGatherWarp, chunk = lane & 7, r0 = 4 * gw + (lane >> 3);
+      int it = 0, s = 0;
+      bool ok = true;
+      for (int i = tile0; ok && walk.seek(i, t); i += step) {
+        const int hx = half(t.rows);
+        uint32_t row[kPer];  // in 16-byte pieces
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          // past the tile its last row again (one row for all tiles would be one L2 slice's); places
+          // without a row load row 0, and are not stored
+          const int r = min(pair * hx + r0 + 8 * j, t.rows - 1);
+          row[j] = (uint32_t)(max(source_row(l, t.row + r), 0) * (l.x_stride / 8));
+        }
+        const uint4* from = reinterpret_cast<const uint4*>(l.x) + k_lo * 8 + chunk;
+        for (int ks = k_lo; ks < k_hi; ++ks, ++it, from += 8) {
+          if (it >= ST && !warp_wait(&c.empty[s], (it / ST - 1) & 1, &c.abort_flag, a.l.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sa(stg + (size_t)s * S::kStage) + 128 * 128 + r0 * 128 + ((chunk ^ r0) << 4);
+          const int bytes = ks * 64ll + chunk * 8 < l.k ? 16 : 0;  // zeros past K, without a read
+#pragma unroll
+          for (int j = 0; j < kPer; j += 2)
+            if (8 * j < hx) {
+#pragma unroll
+              for (int z = 0; z < 2; ++z) copy16(dst + (j + z) * 1024, from + row[j + z], bytes);
+            }
+          copies_arrive(&c.landed[s]);
+          s = s + 1 == ST ? 0 : s + 1;
+        }
+      }
+      copies_wait();
+    }
     __syncwarp();
   } else if (a.split > 1) {
     if (threadIdx.x == 0) c.epi_ok[0] = wait_bar(&c.acc_full[0], 0, &c.abort_flag, a.l.status);
@@ -339,15 +438,21 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   } else {
     int u = 0;
     const int quarter = warp & 3;
+    Epilogue e{l, reinterpret_cast<float*>(stg + (size_t)ST * S::kStage) + warp * 512, lane};
     for (int i = tile0; walk.seek(i, t); i += step, ++u) {
       const int b = u & 1;
-      const long long n = l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter + (lane & 15)
-                                  : ((long long)t.n * CG + pair) * 128 + 32 * quarter + lane;
-      const bool in = n < l.n;
-      float bias = 0.f;
-      if (l.bias && in)
-        bias = __bfloat162float(l.gated ? l.bias[((long long)t.group * 2 + (lane >> 4)) * l.n + n]
-                                        : l.bias[(long long)t.group * l.n + n]);
+      e.start(l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter
+                      : ((long long)t.n * CG + pair) * 128 + 32 * quarter,
+              t.group, a.wide);
+      auto rows_of = [&](int n0) {  // which of 16 tokens have a row
+        bool here = lane < 16 && n0 + lane < t.rows;
+        if (here && l.order) here = source_row(l, t.row + n0 + lane) >= 0;
+        return __ballot_sync(kAll, here);
+      };
+      int n0 = (warp >> 2) * 16;
+      uint32_t mask = rows_of(n0), next = 0;
+      uint32_t r[4][4], r_next[4][4];
+      if (l.res) e.fetch(t.row + (long long)n0, mask, r);
       if (threadIdx.x == 0)
         c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], (u / 2) & 1, &c.abort_flag, a.l.status);
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -355,23 +460,24 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + b * S::kChains * NT;
 #pragma unroll 1
-      for (int n0 = (warp >> 2) * W; n0 < t.rows; n0 += 2 * W) {
-        const int row = t.row + n0;
-        bool here = lane < W && n0 + lane < t.rows;
-        if (here && l.order) here = source_row(l, row + lane) >= 0;
-        const uint32_t mask = __ballot_sync(kAll, here);
-        uint32_t v[W];
+      for (; n0 < t.rows; n0 += 32) {
+        const long long row = t.row + (long long)n0;
+        next = rows_of(n0 + 32);
+        if (l.res) e.fetch(row + 32, next, r_next);
+        uint32_t v[16];
         read_sums<NT>(acc + n0, n_chains, v);
+        __syncwarp();
+        e.turn(v);
+        __syncwarp();
         with_act(l.act, [&](auto act) {
-          using B = __nv_bfloat16;
-          if (l.gated) {
-            if (l.f32) finish_block<float, true>(l, act, v, row, mask, n, in, bias);
-            else finish_block<B, true>(l, act, v, row, mask, n, in, bias);
-          } else {
-            if (l.f32) finish_block<float, false>(l, act, v, row, mask, n, in, bias);
-            else finish_block<B, false>(l, act, v, row, mask, n, in, bias);
-          }
+          if (l.gated) e.finish<true>(act, row, mask, r);
+          else e.finish<false>(act, row, mask, r);
         });
+        mask = next;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[k][j] = r_next[k][j];
       }
       fence_before();
       __syncwarp();
@@ -511,6 +617,10 @@ cudaError_t launch(const Linear& l, int sms, cudaStream_t s) {
   a.nk = (int)((l.k + 63ll) / 64);
   a.split = l.offsets ? 1 : split_for(most, a.nk, CG, sms);
   const int team = CG * a.split;
+  auto whole = [&](const void* p, long long stride) {  // 4 results
+    return (reinterpret_cast<uintptr_t>(p) & (l.f32 ? 15 : 7)) == 0 && stride % 4 == 0;
+  };
+  a.wide = whole(l.out, l.out_stride) && whole(l.res, l.res ? l.res_stride : 0);
   CUtensorMap wm, xm;
   e = make_weight_map(&wm, l.w, l.gated, l.k, l.n, l.w_stride * 2, l.groups, l.group_stride * 2);
   if (e == cudaSuccess) e = make_map(&xm, l.x, 2, l.k, l.x_rows, l.x_stride * 2, l.order ? 1 : 32);
