@@ -9,7 +9,7 @@
 //   0..7  epilogue: tensor memory -> bias, activation, gate, residual -> out.  Warp w reads
 //         lanes 32 (w % 4) .. (its results' n), blocks w / 4, w / 4 + 2, .. of the tokens.  Two
 //         accumulators alternate, so the next tile's MMAs run beside it;
-//   8     TMA loads: weights as boxes, tokens as boxes of 32 rows;
+//   8     TMA loads: weights as boxes, tokens as boxes of 32 rows or of all;
 //   9     MMAs (the first CTA's of a pair);
 //   10,11 tokens by the order's indices, where there is one.
 // Gated products: a CTA's 128 rows are 64 gate rows and their 64 up rows in runs of 16
@@ -135,100 +135,138 @@ __device__ __forceinline__ void read_sums(uint32_t at, int n_chains, uint32_t (&
   }
 }
 
-// Four neighbouring results of a row: from and to memory, whole where `wide` (aligned,
-// none past n), else those below n.  A residual stays in the bits it was loaded in until it
-// is used, so that a load ahead is not waited for.
-__device__ __forceinline__ void get4(const Linear& l, bool wide, long long at, int left, uint32_t (&v)[4]) {
-  if (wide) {
-    if (l.f32) {
-      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const float*>(l.res) + at);
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(l.res) + at);
-      v[0] = q.x, v[1] = q.y;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = j < left ? __float_as_uint(load_res(l, at + j)) : 0u;
-  }
-}
-__device__ __forceinline__ float res_of(const uint32_t (&v)[4], bool packed, int j) {
-  if (!packed) return __uint_as_float(v[j]);
-  return __uint_as_float(j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16);
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void put4(const Linear& l, bool wide, long long at, int left, const float (&v)[4]) {
-  if (wide) {
-    if (l.f32) *reinterpret_cast<float4*>(static_cast<float*>(l.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(l.out) + at) =
-          make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < left) store_out(l, at + j, v[j]);
-  }
+__device__ __forceinline__ void sts(uint32_t saddr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
 }
 
 // The epilogue of a warp: blocks of 16 tokens, its 32 lanes' sums turned in shared memory so that
 // a lane finishes four neighbouring results of a token (1 store of 8 or 16 bytes, and as
 // large a load of the residual, for four scattered ones).  Rows of 32 floats; odd tokens
 // have their halves exchanged, which keeps the reads of 16 gate or up sums off each other's banks.
+// A lane's tokens of a block are `step` apart, an even number, so its places are fixed.
 struct Epilogue {
   const Linear& l;
-  float* buf;       // [16][32]
-  int lane, token;  // first token of the lane's: token, token + step, ..
-  int col, left;    // first of the lane's four results in the warp's row of sums; results that are below n
-  long long n;      // and in out
-  bool wide;
+  const bool gated, f32;
+  const int lane, token, step;  // first of the lane's tokens in a block
+  const uint32_t put0, put1;    // shared memory: this lane's sums of even and odd tokens
+  const uint32_t get_a, get_u;  // the four sums of its first token, and their up sums
+  const long long out_step, res_step, es;  // bytes between the lane's rows, of an element
+  int left;                     // the lane's results that are below n
+  bool wide;                    // all four, in one aligned access
+  char* out;                    // the lane's first result of the tile
+  const char* res;
   float bias[4], ubias[4];
 
-  // n0: first result of the warp's lanes
-  __device__ __forceinline__ void start(long long n0, int group, bool aligned) {
-    const int q = l.gated ? lane & 3 : lane & 7;
-    token = l.gated ? lane >> 2 : lane >> 3;
-    col = 4 * q;
-    n = n0 + col;
+  __device__ __forceinline__ Epilogue(const Linear& l_, uint32_t buf, int lane_)
+      : l(l_), gated(l_.gated), f32(l_.f32), lane(lane_), token(l_.gated ? lane_ >> 2 : lane_ >> 3),
+        step(l_.gated ? 8 : 4), put0(buf + 4 * lane_), put1(buf + 128 + 4 * (lane_ ^ 16)),
+        get_a(buf + token * 128 + 16 * ((l_.gated ? lane_ & 3 : lane_ & 7) ^ (token & 1 ? 4 : 0))),
+        get_u(get_a ^ 64), out_step(step * l_.out_stride * (l_.f32 ? 4 : 2)),
+        res_step(step * l_.res_stride * (l_.f32 ? 4 : 2)), es(l_.f32 ? 4 : 2) {}
+
+  // n0: first result of the warp's lanes; row: the tile's first
+  __device__ __forceinline__ void start(long long n0, long long row, int group, bool aligned) {
+    const long long n = n0 + 4 * (gated ? lane & 3 : lane & 7);
     left = (int)max(0ll, min(4ll, l.n - n));
     wide = aligned && left == 4;
-    const __nv_bfloat16* b = l.bias ? l.bias + (long long)group * l.n * (l.gated ? 2 : 1) + n : nullptr;
+    out = static_cast<char*>(l.out) + ((row + token) * l.out_stride + n) * es;
+    res = static_cast<const char*>(l.res) + (l.res ? ((row + token) * l.res_stride + n) * es : 0);
+    const __nv_bfloat16* b = l.bias ? l.bias + (long long)group * l.n * (gated ? 2 : 1) + n : nullptr;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       bias[j] = b && j < left ? __bfloat162float(b[j]) : 0.f;
-      ubias[j] = b && l.gated && j < left ? __bfloat162float(b[l.n + j]) : 0.f;
+      ubias[j] = b && gated && j < left ? __bfloat162float(b[l.n + j]) : 0.f;
     }
   }
-  // the residual of the lane's results of a block
-  __device__ __forceinline__ void fetch(long long row, uint32_t mask, uint32_t (&r)[4][4]) const {
+  // The residual of the lane's results of the block at token n0; it stays in the bits it was
+  // loaded in until it is used, so that a load ahead is not waited for.
+  __device__ __forceinline__ void fetch(int n0, uint32_t mask, uint32_t (&r)[4][4]) const {
+    const char* p = res + n0 * l.res_stride * es;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int t = l.gated ? token + 8 * k : token + 4 * k;
-      if (k < (l.gated ? 2 : 4) && (mask >> t & 1) && left > 0) get4(l, wide, (row + t) * l.res_stride + n, left, r[k]);
+      if ((k < 2 || !gated) && (mask >> (token + k * step) & 1) && left > 0) {
+        const char* q = p + k * res_step;
+        if (wide && f32) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q);
+          r[k][0] = u.x, r[k][1] = u.y, r[k][2] = u.z, r[k][3] = u.w;
+        } else if (wide) {
+          const uint2 u = *reinterpret_cast<const uint2*>(q);
+          r[k][0] = u.x, r[k][1] = u.y;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < left)
+              r[k][j] = f32 ? reinterpret_cast<const uint32_t*>(q)[j]
+                            : (uint32_t)reinterpret_cast<const uint16_t*>(q)[j] << 16;
+        }
+      }
     }
   }
   __device__ __forceinline__ void turn(const uint32_t (&v)[16]) const {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) buf[i * 32 + (lane ^ (i & 1 ? 16 : 0))] = __uint_as_float(v[i]);
+    for (int i = 0; i < 16; i += 2) {
+      sts(put0 + i * 128, v[i]);
+      sts(put1 + i * 128, v[i + 1]);
+    }
   }
   template <bool GATED, typename A>
-  __device__ __forceinline__ void finish(A act, long long row, uint32_t mask, const uint32_t (&r)[4][4]) const {
+  __device__ __forceinline__ void finish(A act, int n0, uint32_t mask, const uint32_t (&r)[4][4]) const {
+    constexpr int M = GATED ? 2 : 4;
+    char* p = out + n0 * l.out_stride * es;
+    float y[M][4];
 #pragma unroll
-    for (int k = 0; k < (GATED ? 2 : 4); ++k) {
-      const int t = GATED ? token + 8 * k : token + 4 * k;
-      const float* z = buf + t * 32;
-      const int turned = t & 1 ? 16 : 0;
-      const float4 g = *reinterpret_cast<const float4*>(z + (col ^ turned));
-      float y[4] = {act(g.x + bias[0]), act(g.y + bias[1]), act(g.z + bias[2]), act(g.w + bias[3])};
-      if (GATED) {
-        const float4 u = *reinterpret_cast<const float4*>(z + ((16 + col) ^ turned));
-        y[0] *= u.x + ubias[0], y[1] *= u.y + ubias[1], y[2] *= u.z + ubias[2], y[3] *= u.w + ubias[3];
+    for (int k = 0; k < M; ++k) {
+      const float4 g = lds4(get_a + k * (GATED ? 1024 : 512));
+      y[k][0] = g.x, y[k][1] = g.y, y[k][2] = g.z, y[k][3] = g.w;
+    }
+#pragma unroll
+    for (int k = 0; k < M; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[k][j] = act(y[k][j] + bias[j]);
+    if constexpr (GATED) {
+#pragma unroll
+      for (int k = 0; k < M; ++k) {
+        const float4 u = lds4(get_u + k * 1024);
+        y[k][0] *= u.x + ubias[0], y[k][1] *= u.y + ubias[1], y[k][2] *= u.z + ubias[2], y[k][3] *= u.w + ubias[3];
       }
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = l.res ? fmaf(l.alpha, y[j], res_of(r[k], wide && !l.f32, j)) : l.alpha * y[j];
-      if ((mask >> t & 1) && left > 0) put4(l, wide, (row + t) * l.out_stride + n, left, y);
+    for (int k = 0; k < M; ++k) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[k][j] *= l.alpha;
+      if (l.res) {
+        if (f32 || !wide) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[k][j] += __uint_as_float(r[k][j]);
+        } else {
+          y[k][0] += __uint_as_float(r[k][0] << 16), y[k][1] += __uint_as_float(r[k][0] & 0xffff0000u);
+          y[k][2] += __uint_as_float(r[k][1] << 16), y[k][3] += __uint_as_float(r[k][1] & 0xffff0000u);
+        }
+      }
+    }
+    if (wide) {
+#pragma unroll
+      for (int k = 0; k < M; ++k) {
+        char* q = p + k * out_step;
+        if (mask >> (token + k * step) & 1) {
+          if (f32) *reinterpret_cast<float4*>(q) = make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
+          else *reinterpret_cast<uint2*>(q) = make_uint2(pack2(y[k][0], y[k][1]), pack2(y[k][2], y[k][3]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < M; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < left && (mask >> (token + k * step) & 1)) {
+            char* q = p + k * out_step + j * es;
+            if (f32) *reinterpret_cast<float*>(q) = y[k][j];
+            else *reinterpret_cast<__nv_bfloat16*>(q) = __float2bfloat16_rn(y[k][j]);
+          }
     }
   }
 };
@@ -236,7 +274,7 @@ struct Epilogue {
 template <int NT, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-              const __grid_constant__ Args a) {
+              const __grid_constant__ CUtensorMap xmap_all, const __grid_constant__ Args a) {
   using S = Shape<NT, CG>;
   constexpr int ST = S::kStages, W = 16;
   extern __shared__ uint8_t raw[];
@@ -294,7 +332,10 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     int it = 0, s = 0;
     bool ok = true;
     for (int i = tile0; ok && walk.seek(i, t); i += step) {
-      const int hx = half(t.rows), boxes = l.order ? 0 : (hx + 31) / 32;
+      // boxes of 32 rows, or all the CTA has room for at once: an instruction takes the warp about 100 cycles
+      const int hx = half(t.rows);
+      const bool all = !l.order && hx > S::kX / 2;
+      const int boxes = l.order ? 0 : all ? S::kX / 32 : (hx + 31) / 32;
       const int bytes = CG * (128 * 128 + boxes * 4096);
       const int x0 = t.row + pair * hx;
       for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
@@ -315,8 +356,11 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           } else {
             load_rows<CG>(p, &wmap, x, nt * 128, t.group, bar);
           }
-          for (int j = 0; j < boxes; ++j)
-            tma_load<CG>(p + 128 * 128 + j * 4096, &xmap, x, x0 + 32 * j, bar);
+          if (all) {
+            tma_load<CG>(p + 128 * 128, &xmap_all, x, x0, bar);
+          } else {
+            for (int j = 0; j < boxes; ++j) tma_load<CG>(p + 128 * 128 + j * 4096, &xmap, x, x0 + 32 * j, bar);
+          }
         }
         __syncwarp();
         s = s + 1 == ST ? 0 : s + 1;
@@ -438,21 +482,21 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   } else {
     int u = 0;
     const int quarter = warp & 3;
-    Epilogue e{l, reinterpret_cast<float*>(stg + (size_t)ST * S::kStage) + warp * 512, lane};
+    Epilogue e(l, sa(stg) + ST * S::kStage + warp * 2048, lane);
     for (int i = tile0; walk.seek(i, t); i += step, ++u) {
       const int b = u & 1;
       e.start(l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter
                       : ((long long)t.n * CG + pair) * 128 + 32 * quarter,
-              t.group, a.wide);
+              t.row, t.group, a.wide);
       auto rows_of = [&](int n0) {  // which of 16 tokens have a row
-        bool here = lane < 16 && n0 + lane < t.rows;
-        if (here && l.order) here = source_row(l, t.row + n0 + lane) >= 0;
-        return __ballot_sync(kAll, here);
+        const uint32_t in = n0 + 16 <= t.rows ? 0xffffu : n0 < t.rows ? (1u << (t.rows - n0)) - 1 : 0u;
+        if (!l.order) return in;
+        return __ballot_sync(kAll, (in >> lane & 1) && source_row(l, t.row + n0 + lane) >= 0);
       };
       int n0 = (warp >> 2) * 16;
-      uint32_t mask = rows_of(n0), next = 0;
+      uint32_t mask = rows_of(n0);
       uint32_t r[4][4], r_next[4][4];
-      if (l.res) e.fetch(t.row + (long long)n0, mask, r);
+      if (l.res) e.fetch(n0, mask, r);
       if (threadIdx.x == 0)
         c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], (u / 2) & 1, &c.abort_flag, a.l.status);
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -461,17 +505,16 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + b * S::kChains * NT;
 #pragma unroll 1
       for (; n0 < t.rows; n0 += 32) {
-        const long long row = t.row + (long long)n0;
-        next = rows_of(n0 + 32);
-        if (l.res) e.fetch(row + 32, next, r_next);
+        const uint32_t next = rows_of(n0 + 32);
+        if (l.res) e.fetch(n0 + 32, next, r_next);
         uint32_t v[16];
         read_sums<NT>(acc + n0, n_chains, v);
         __syncwarp();
         e.turn(v);
         __syncwarp();
         with_act(l.act, [&](auto act) {
-          if (l.gated) e.finish<true>(act, row, mask, r);
-          else e.finish<false>(act, row, mask, r);
+          if (e.gated) e.finish<true>(act, n0, mask, r);
+          else e.finish<false>(act, n0, mask, r);
         });
         mask = next;
 #pragma unroll
@@ -621,9 +664,10 @@ cudaError_t launch(const Linear& l, int sms, cudaStream_t s) {
     return (reinterpret_cast<uintptr_t>(p) & (l.f32 ? 15 : 7)) == 0 && stride % 4 == 0;
   };
   a.wide = whole(l.out, l.out_stride) && whole(l.res, l.res ? l.res_stride : 0);
-  CUtensorMap wm, xm;
+  CUtensorMap wm, xm, xa;
   e = make_weight_map(&wm, l.w, l.gated, l.k, l.n, l.w_stride * 2, l.groups, l.group_stride * 2);
-  if (e == cudaSuccess) e = make_map(&xm, l.x, 2, l.k, l.x_rows, l.x_stride * 2, l.order ? 1 : 32);
+  if (e == cudaSuccess) e = make_map(&xm, l.x, 2, l.k, l.x_rows, l.x_stride * 2, 32);
+  if (e == cudaSuccess) e = make_map(&xa, l.x, 2, l.k, l.x_rows, l.x_stride * 2, S::kX);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const long long teams = most < sms / team ? most : sms / team;
@@ -638,7 +682,7 @@ cudaError_t launch(const Linear& l, int sms, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, wm, xm, a);
+  return cudaLaunchKernelEx(&cfg, kern, wm, xm, xa, a);
 }
 
 // Estimated cycles of a dense product with this tile: a stage's MMAs take 2 cycles per token, its
