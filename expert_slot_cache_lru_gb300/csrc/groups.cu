@@ -151,34 +151,27 @@ cudaError_t launch_group(const GroupArgs& a, int smem, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// V elements from 16-byte aligned memory (or one)
-template <int V>
-__device__ __forceinline__ void load_v(const float* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = *p;
-  } else {
+// V elements (8, or one) as they lie in memory, and their values
+template <typename T, int V>
+struct Raw {
+  uint4 q[V * sizeof(T) / 16 > 0 ? V * sizeof(T) / 16 : 1];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V == 1) {
+      q[0].x = sizeof(T) == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p) << 16;
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(p + i);
-      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+      for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
     }
   }
-}
-template <int V>
-__device__ __forceinline__ void load_v(const __nv_bfloat16* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = __bfloat162float(*p);
-  } else {
-    static_assert(V == 8, "16 bytes");
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const unsigned w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  __device__ __forceinline__ float at(int i) const {
+    const int per = 4 / sizeof(T) * 4;  // elements of 16 bytes
+    const uint4& u = q[V == 1 ? 0 : i / per];
+    const int word = V == 1 ? 0 : sizeof(T) == 4 ? i % 4 : i % 8 / 2;
+    const uint32_t w = word == 0 ? u.x : word == 1 ? u.y : word == 2 ? u.z : u.w;
+    if (V == 1 || sizeof(T) == 4) return __uint_as_float(w);
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
   }
-}
+};
 template <int V>
 __device__ __forceinline__ void store_v(float* p, const float (&v)[V]) {
   if constexpr (V == 1) {
@@ -216,11 +209,17 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int p
   const int32_t* pos = a.pos + b * a.k;
   const float* w = a.w + b * a.k;
   float acc[V] = {};
-  if (a.add) load_v<V>(static_cast<const O*>(a.add) + b * a.add_stride + c, acc);
-  constexpr int U = 8;  // routes in flight
+  if (a.add) {
+    Raw<O, V> r;
+    r.load(static_cast<const O*>(a.add) + b * a.add_stride + c);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = r.at(e);
+  }
+  constexpr int U = sizeof(Y) == 4 ? 4 : 8;  // routes in flight: loaded before any is used
   for (int j0 = 0; j0 < a.k; j0 += U) {
     int p[U];
-    float f[U], v[U][V];
+    float f[U];
+    Raw<Y, V> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       p[u] = j0 + u < a.k ? pos[j0 + u] : -1;
@@ -228,12 +227,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int p
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if ((unsigned)p[u] < (unsigned)a.y_rows) load_v<V>(y + p[u] * a.y_stride, v[u]);
+      if ((unsigned)p[u] < (unsigned)a.y_rows) v[u].load(y + p[u] * a.y_stride);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if ((unsigned)p[u] < (unsigned)a.y_rows)
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(f[u], v[u][e], acc[e]);
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(f[u], v[u].at(e), acc[e]);
   }
   store_v<V>(static_cast<O*>(a.out) + b * a.out_stride + c, acc);
 }

@@ -1,5 +1,9 @@
 // linear.cu -- the bf16 products (formulas in moe_cache.h): which kernel takes a
-// call, and the CUDA-core tiles for operands of any layout.
+// call, the dot products of a few rows, and the CUDA-core tiles for operands of any layout.
+//
+// A few rows are bound by the weights' bytes: a CTA takes a few rows of weights, its warps a slice of K each, 16 bytes
+// a lane and load, all loads of a slice in flight together and x in registers beside them.  Grouped, a place is a
+// row of its own: its group is looked up by the whole block at once.
 //
 // Tiles of 64 rows x 64 results (of both matrices if gated), 4 x 4 results per thread, operands through
 // shared memory as fp32: bound by its FMAs.
@@ -10,6 +14,15 @@ namespace moe {
 namespace {
 
 using namespace lin;
+
+constexpr int kDotThreads = 128, kDotRows = 4, kDotPlaces = 16;
+// Rows of weights of a CTA's part and 256-element pieces of K of a warp, for R rows of x: the best of
+// 4 and 8 and of 1, 2 and 4 at 4,096 x 4,096 (8.1, 7.9 and 10.1 us; with more in flight per thread
+// and fewer threads 9 to 13).
+template <int R>
+struct Dots {
+  static constexpr int NB = R == 4 ? 8 : 4, U = R == 1 ? 2 : 1;
+};
 
 template <bool GATED>
 __global__ void __launch_bounds__(256) tile_kernel(const Linear l, int tn) {
@@ -80,6 +93,139 @@ __global__ void __launch_bounds__(256) tile_kernel(const Linear l, int tn) {
   }
 }
 
+__device__ __forceinline__ void dot8(float& acc, const uint4& w, const uint4& x) {
+  const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    acc = fmaf(__uint_as_float(a[j] << 16), __uint_as_float(b[j] << 16), acc);
+    acc = fmaf(__uint_as_float(a[j] & 0xffff0000u), __uint_as_float(b[j] & 0xffff0000u), acc);
+  }
+}
+// Sums of N values over the lanes: lane l keeps that of value l * N / 32 (in its highest bits).  Half the values change
+// hands at each of the first steps: N - 1 + log2(32 / N) shuffles for N * 5.
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int m = N / 2; m >= 1; m >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float got = __shfl_xor_sync(kAll, up ? v[i] : v[i + m], o);
+      v[i] = (up ? v[i + m] : v[i]) + got;
+    }
+  }
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(kAll, v[0], o);
+  return v[0];
+}
+
+// R rows of x (the last again where there are fewer; grouped: the place blockIdx.y alone).  A CTA takes NB rows of
+// weights per part of n (of each matrix half as many if gated); `kw` of its warps share a part, each a
+// slice of K at a time, the slices of x in registers.
+template <int R, bool GATED>
+__global__ void __launch_bounds__(kDotThreads) dot_kernel(const Linear l, int kw) {
+  constexpr int kWarps = kDotThreads / 32, U = Dots<R>::U, NB = Dots<R>::NB, H = GATED ? NB / 2 : NB;  // H results a part
+  __shared__ int found;
+  __shared__ float sums[kWarps][NB * R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tc::pdl_trigger();
+  if (threadIdx.x == 0) found = -1;
+  tc::pdl_wait();
+  int group = 0;
+  long long row0 = 0;  // of out
+  const __nv_bfloat16* x = l.x;
+  if (l.offsets) {
+    const int p = blockIdx.y;
+    __syncthreads();
+    for (int g = threadIdx.x; g < l.groups; g += kDotThreads)
+      if (l.offsets[g] <= p && p < l.offsets[g + 1]) found = g;  // one at most where offsets ascend
+    __syncthreads();
+    group = found;
+    const int src = group < 0 ? -1 : source_row(l, p);
+    if (src < 0) return;
+    x += src * l.x_stride;
+    row0 = p;
+  }
+  const int part = warp / kw, slice = warp % kw, parts = kWarps / kw;
+  const long long n0 = ((long long)blockIdx.x * parts + part) * H;
+  // thread i of a part finishes result i % H of row i / H; what it needs is loaded now
+  const int mine = slice * 32 + lane;
+  const long long n = n0 + mine % H;
+  const int row = mine / H;
+  const bool ends = mine < H * R && n < l.n && (l.offsets || row < l.rows);
+  float bias = 0.f, ubias = 0.f, res = 0.f;
+  if (ends) {
+    if (l.bias) {
+      const __nv_bfloat16* b = l.bias + (long long)group * l.n * (GATED ? 2 : 1);
+      bias = __bfloat162float(b[n]);
+      if (GATED) ubias = __bfloat162float(b[l.n + n]);
+    }
+    if (l.res) res = load_res(l, (row0 + row) * l.res_stride + n);
+  }
+  const uint4 *w[NB], *xr[R];
+  const __nv_bfloat16* base = l.w + group * l.group_stride;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {  // rows past the matrix are its last
+    const long long at = n0 + j % H < l.n ? n0 + j % H : l.n - 1;
+    w[j] = reinterpret_cast<const uint4*>(base + (at + (j >= H ? l.n : 0)) * l.w_stride) + lane;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    xr[r] = reinterpret_cast<const uint4*>(x + (l.offsets || r < l.rows ? r : l.rows - 1) * l.x_stride) + lane;
+  float acc[NB * R] = {};
+  const int pieces = l.k / 8;
+  int i = slice * (32 * U);
+  for (; i + 32 * U <= pieces; i += kw * 32 * U) {
+    uint4 p[NB][U], v[R][U];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int u = 0; u < U; ++u) p[j][u] = w[j][i + 32 * u];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[r][u] = xr[r][i + 32 * u];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int u = 0; u < U; ++u) dot8(acc[j * R + r], p[j][u], v[r][u]);
+  }
+  for (int u = 0; u < U; ++u)  // the slice that is not whole
+    if (i + 32 * u + lane < pieces)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) dot8(acc[j * R + r], w[j][i + 32 * u], xr[r][i + 32 * u]);
+  const float sum = lane_sums(acc);
+  if (lane % (32 / (NB * R)) == 0) sums[warp][lane / (32 / (NB * R))] = sum;
+  __syncthreads();
+  if (!ends) return;
+  float y = bias, up = ubias;
+  for (int k = 0; k < kw; ++k) {
+    y += sums[part * kw + k][(mine % H) * R + row];
+    if (GATED) up += sums[part * kw + k][(H + mine % H) * R + row];
+  }
+  with_act(l.act, [&](auto act) {
+    y = act(y);
+    if (GATED) y *= up;
+    store_out(l, (row0 + row) * l.out_stride + n, l.res ? fmaf(l.alpha, y, res) : l.alpha * y);
+  });
+}
+
+template <int R>
+cudaError_t launch_dots(const Linear& l, cudaStream_t s) {
+  constexpr int kWarps = kDotThreads / 32;
+  int kw = 1;  // slices of K as there are whole ones
+  while (kw < kWarps && l.k >= 2 * kw * 256 * Dots<R>::U) kw *= 2;
+  const long long per = (long long)(kWarps / kw) * (l.gated ? Dots<R>::NB / 2 : Dots<R>::NB), blocks = (l.n + per - 1) / per;
+  const dim3 grid((unsigned)blocks, l.offsets ? l.rows : 1), block(kDotThreads);
+  if (l.gated) return tc::launch_early(dot_kernel<R, true>, grid, block, 0, s, l, kw);
+  return tc::launch_early(dot_kernel<R, false>, grid, block, 0, s, l, kw);
+}
+
 template <bool GATED>
 cudaError_t launch_tiles(const Linear& l, int sms, cudaStream_t s) {
   const int tn = (int)((l.n + 63ll) / 64);
@@ -99,6 +245,9 @@ cudaError_t launch_linear(const Linear& l, cudaStream_t s) {
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
   // gathered rows are addressed in 32 bits of 16-byte pieces
   const bool near = !l.order || (double)l.x_rows * l.x_stride / 8 < 4294967296.0;
+  if (whole && l.offsets && l.rows <= kDotPlaces) return launch_dots<1>(l, s);
+  if (whole && !l.offsets && l.rows <= kDotRows)
+    return l.rows == 1 ? launch_dots<1>(l, s) : l.rows == 2 ? launch_dots<2>(l, s) : launch_dots<4>(l, s);
   if (whole && near && (!l.gated || l.n % 16 == 0)) return launch_linear_tc(l, d.sms, s);
   return l.gated ? launch_tiles<true>(l, d.sms, s) : launch_tiles<false>(l, d.sms, s);
 }
