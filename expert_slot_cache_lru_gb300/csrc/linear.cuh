@@ -75,6 +75,7 @@ struct Walk {
   int g0;         // first group of this chunk
   int base, end;  // tile numbers of this chunk
   int lo[4], hi[4], ahead[5], incl;
+  int dense_tiles, dense_width;  // of tokens, where there are no groups
 
   __device__ __forceinline__ void load(int g) {  // into `ahead`, lane's four groups of a chunk
 #pragma unroll
@@ -103,20 +104,38 @@ struct Walk {
     }
     end = base + __shfl_sync(kAll, incl, 31);
   }
-  __device__ __forceinline__ void start(const Linear& l, int shift_, int gran_, int tn_) {
+  // tiles, width: of a dense product (0: as for a group)
+  __device__ __forceinline__ void start(const Linear& l, int shift_, int gran_, int tn_, int tiles = 0, int width = 0) {
     offsets = l.offsets;
+    dense_tiles = tiles;
+    dense_width = width;
     groups = l.groups;
     total_rows = l.rows;
     shift = shift_;
     gran = gran_;
     tn = tn_;
+    if (dense_tiles) return;
     g0 = base = 0;
     load(0);
     take();
     load(128);
   }
+  // tile r of T by tn tiles of `width` rows from lo to hi
+  __device__ __forceinline__ void place(int r, int T, int width, int lo_, int hi_, Tile& out) const {
+    const int per = 8 * T, strip = r / per, in = r - strip * per, w = min(8, tn - strip * 8);
+    out.width = width;
+    out.n = strip * 8 + in % w;
+    out.row = lo_ + in / w * width;
+    out.rows = min(width, hi_ - out.row);
+  }
   // false where tile t is past the last
   __device__ __forceinline__ bool seek(int t, Tile& out) {
+    if (dense_tiles) {
+      if (t >= dense_tiles * tn) return false;
+      out.group = 0;
+      place(t, dense_tiles, dense_width, 0, total_rows, out);
+      return true;
+    }
     while (t >= end) {
       g0 += 128;
       if (g0 >= groups) return false;
@@ -146,11 +165,7 @@ struct Walk {
     }
     const int R = h0 - l0, T = parts(R);
     out.group = g;
-    out.width = ((R - 1) / T + gran) / gran * gran;  // ceil(R / T), up to a multiple of gran
-    const int per = 8 * T, strip = r / per, in = r - strip * per, w = min(8, tn - strip * 8);
-    out.n = strip * 8 + in % w;
-    out.row = l0 + in / w * out.width;
-    out.rows = min(out.width, h0 - out.row);
+    place(r, T, ((R - 1) / T + gran) / gran * gran, l0, h0, out);  // ceil(R / T), up to a multiple of gran
     return true;
   }
 };

@@ -31,13 +31,15 @@ namespace {
 using namespace tc;
 using namespace lin;
 
-constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kGatherWarp = 10, kThreads = 384;
+constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kRowWarp = 10, kThreads = 384;
 constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
 
 template <int NT, int CG>
 struct Shape {
   static constexpr int kX = NT / CG;                     // token rows a CTA loads
-  static constexpr int kStage = 128 * 128 + kX * 128;
+  static constexpr int kSub = NT == 256 ? 1 : 2;   // 64-element slabs of K in a stage
+  static constexpr int kSlab = 128 * 128 + kX * 128;
+  static constexpr int kStage = kSub * kSlab;
   static constexpr int kTurn = kEpiWarps * 2048;         // the epilogue's
   static constexpr int kFit = (226 * 1024 - 2048 - kTurn) / kStage;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
@@ -52,6 +54,8 @@ struct Shape {
 struct Args {
   Linear l;
   int tn;     // tiles of n
+  int tiles, width;  // of tokens, in a dense product
+  int shift;  // a group's tiles have up to 1 << shift tokens
   int nk;     // stages of K
   int split;  // parts of K
   int wide;   // four neighbouring results of out and res are one aligned access
@@ -143,6 +147,12 @@ __device__ __forceinline__ void sts(uint32_t saddr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ float lds(uint32_t saddr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(saddr));
+  return v;
+}
+
 // The epilogue of a warp: blocks of 16 tokens, its 32 lanes' sums turned in shared memory so that
 // a lane finishes four neighbouring results of a token (1 store of 8 or 16 bytes, and as
 // large a load of the residual, for four scattered ones).  Rows of 32 floats; odd tokens
@@ -155,8 +165,9 @@ struct Epilogue {
   const uint32_t put0, put1;    // shared memory: this lane's sums of even and odd tokens
   const uint32_t get_a, get_u;  // the four sums of its first token, and their up sums
   const long long out_step, res_step, es;  // bytes between the lane's rows, of an element
-  int left;                     // the lane's results that are below n
-  bool wide;                    // all four, in one aligned access
+  // Where the lanes' results are all below n and aligned: four of a token each.  Else one of each token (of
+  // every second one if gated), neighbours in neighbouring lanes.
+  bool wide, in;                // in: a narrow lane's result is below n
   char* out;                    // the lane's first result of the tile
   const char* res;
   float bias[4], ubias[4];
@@ -170,40 +181,46 @@ struct Epilogue {
 
   // n0: first result of the warp's lanes; row: the tile's first
   __device__ __forceinline__ void start(long long n0, long long row, int group, bool aligned) {
-    const long long n = n0 + 4 * (gated ? lane & 3 : lane & 7);
-    left = (int)max(0ll, min(4ll, l.n - n));
-    wide = aligned && left == 4;
-    out = static_cast<char*>(l.out) + ((row + token) * l.out_stride + n) * es;
-    res = static_cast<const char*>(l.res) + (l.res ? ((row + token) * l.res_stride + n) * es : 0);
+    wide = aligned && n0 + (gated ? 16 : 32) <= l.n;
+    const long long n = n0 + (wide ? 4 * (gated ? lane & 3 : lane & 7) : gated ? lane & 15 : lane);
+    in = n < l.n;
+    row += wide ? token : gated ? lane >> 4 : 0;
+    out = static_cast<char*>(l.out) + (row * l.out_stride + n) * es;
+    res = static_cast<const char*>(l.res) + (l.res ? (row * l.res_stride + n) * es : 0);
     const __nv_bfloat16* b = l.bias ? l.bias + (long long)group * l.n * (gated ? 2 : 1) + n : nullptr;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      bias[j] = b && j < left ? __bfloat162float(b[j]) : 0.f;
-      ubias[j] = b && gated && j < left ? __bfloat162float(b[l.n + j]) : 0.f;
+      const bool here = b && in && (wide || j == 0);
+      bias[j] = here ? __bfloat162float(b[j]) : 0.f;
+      ubias[j] = here && gated ? __bfloat162float(b[l.n + j]) : 0.f;
     }
   }
   // The residual of the lane's results of the block at token n0; it stays in the bits it was
   // loaded in until it is used, so that a load ahead is not waited for.
   __device__ __forceinline__ void fetch(int n0, uint32_t mask, uint32_t (&r)[4][4]) const {
     const char* p = res + n0 * l.res_stride * es;
+    if (wide) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if ((k < 2 || !gated) && (mask >> (token + k * step) & 1) && left > 0) {
-        const char* q = p + k * res_step;
-        if (wide && f32) {
-          const uint4 u = *reinterpret_cast<const uint4*>(q);
-          r[k][0] = u.x, r[k][1] = u.y, r[k][2] = u.z, r[k][3] = u.w;
-        } else if (wide) {
-          const uint2 u = *reinterpret_cast<const uint2*>(q);
-          r[k][0] = u.x, r[k][1] = u.y;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < left)
-              r[k][j] = f32 ? reinterpret_cast<const uint32_t*>(q)[j]
-                            : (uint32_t)reinterpret_cast<const uint16_t*>(q)[j] << 16;
+      for (int k = 0; k < 4; ++k)
+        if ((k < 2 || !gated) && (mask >> (token + k * step) & 1)) {
+          const char* q = p + k * res_step;
+          if (f32) {
+            const uint4 u = *reinterpret_cast<const uint4*>(q);
+            r[k][0] = u.x, r[k][1] = u.y, r[k][2] = u.z, r[k][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(q);
+            r[k][0] = u.x, r[k][1] = u.y;
+          }
         }
-      }
+    } else {
+      const int first = gated ? lane >> 4 : 0, by = gated ? 2 : 1;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i * by < 16 && in && (mask >> (first + i * by) & 1)) {
+          const char* q = p + i * by * l.res_stride * es;
+          r[i / 4][i % 4] = f32 ? *reinterpret_cast<const uint32_t*>(q)
+                                : (uint32_t)*reinterpret_cast<const uint16_t*>(q) << 16;
+        }
     }
   }
   __device__ __forceinline__ void turn(const uint32_t (&v)[16]) const {
@@ -215,6 +232,7 @@ struct Epilogue {
   }
   template <bool GATED, typename A>
   __device__ __forceinline__ void finish(A act, int n0, uint32_t mask, const uint32_t (&r)[4][4]) const {
+    if (!wide) return finish_narrow<GATED>(act, n0, mask, r);
     constexpr int M = GATED ? 2 : 4;
     char* p = out + n0 * l.out_stride * es;
     float y[M][4];
@@ -239,7 +257,7 @@ struct Epilogue {
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[k][j] *= l.alpha;
       if (l.res) {
-        if (f32 || !wide) {
+        if (f32) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[k][j] += __uint_as_float(r[k][j]);
         } else {
@@ -247,26 +265,32 @@ struct Epilogue {
           y[k][2] += __uint_as_float(r[k][1] << 16), y[k][3] += __uint_as_float(r[k][1] & 0xffff0000u);
         }
       }
-    }
-    if (wide) {
-#pragma unroll
-      for (int k = 0; k < M; ++k) {
-        char* q = p + k * out_step;
-        if (mask >> (token + k * step) & 1) {
-          if (f32) *reinterpret_cast<float4*>(q) = make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
-          else *reinterpret_cast<uint2*>(q) = make_uint2(pack2(y[k][0], y[k][1]), pack2(y[k][2], y[k][3]));
-        }
+      char* q = p + k * out_step;
+      if (mask >> (token + k * step) & 1) {
+        if (f32) *reinterpret_cast<float4*>(q) = make_float4(y[k][0], y[k][1], y[k][2], y[k][3]);
+        else *reinterpret_cast<uint2*>(q) = make_uint2(pack2(y[k][0], y[k][1]), pack2(y[k][2], y[k][3]));
       }
-    } else {
+    }
+  }
+  template <bool GATED, typename A>
+  __device__ __forceinline__ void finish_narrow(A act, int n0, uint32_t mask, const uint32_t (&r)[4][4]) const {
+    constexpr int BY = GATED ? 2 : 1;
+    const int first = GATED ? lane >> 4 : 0;
+    char* p = out + n0 * l.out_stride * es;
 #pragma unroll
-      for (int k = 0; k < M; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < left && (mask >> (token + k * step) & 1)) {
-            char* q = p + k * out_step + j * es;
-            if (f32) *reinterpret_cast<float*>(q) = y[k][j];
-            else *reinterpret_cast<__nv_bfloat16*>(q) = __float2bfloat16_rn(y[k][j]);
-          }
+    for (int i = 0; i < 16 / BY; ++i) {
+      // sums of token first + BY * i; gated, the up lanes' tokens are odd and turned
+      const uint32_t at = GATED ? put0 - 4 * lane + (2 * i + first) * 128 + 4 * ((lane & 15) ^ (first ? 16 : 0))
+                                : (i & 1 ? put1 - 128 : put0) + i * 128;
+      float y = act(lds(at) + bias[0]);
+      if (GATED) y *= lds(at ^ 64) + ubias[0];
+      y *= l.alpha;
+      if (l.res) y += __uint_as_float(r[i / 4][i % 4]);
+      if (in && (mask >> (first + BY * i) & 1)) {
+        char* q = p + i * BY * l.out_stride * es;
+        if (f32) *reinterpret_cast<float*>(q) = y;
+        else *reinterpret_cast<__nv_bfloat16*>(q) = __float2bfloat16_rn(y);
+      }
     }
   }
 };
@@ -281,7 +305,8 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   uint8_t* stg = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ Ctl<ST> c;
   const Linear& l = a.l;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the warp's number from a shuffle: known to be the same for all lanes, with what follows from it
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // cluster: `split` parts of K, each CG CTAs; a lone CTA's cluster is itself
   const int crank = CG == 1 && a.split == 1 ? 0 : (int)cluster_rank();
   const int pair = crank % CG, first = crank - pair, part = crank / CG;
@@ -320,46 +345,48 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   auto half = [](int rows) { return (rows + 15) / 16 * 16 / CG; };
   Walk walk;
   Tile t;
-  constexpr int kShift = NT == 32 ? 5 : NT == 128 ? 7 : 8;
-  static_assert(NT == 1 << kShift, "tokens of a tile");
   if (warp < kEpiWarps && a.split > 1) {
     // a split's sums are exchanged below
   } else {
-    walk.start(l, kShift, 16, a.tn);
+    walk.start(l, a.shift, 16, a.tn, a.tiles, a.width);
   }
 
-  if (warp == kTmaWarp) {
+  if (warp == kTmaWarp || (warp == kRowWarp && !l.order)) {
+    // two warps, since an instruction takes one about 100 cycles: the weights' copies, the tokens'
     int it = 0, s = 0;
     bool ok = true;
     for (int i = tile0; ok && walk.seek(i, t); i += step) {
-      // boxes of 32 rows, or all the CTA has room for at once: an instruction takes the warp about 100 cycles
+      // boxes of 32 rows, or all the CTA has room for at once
       const int hx = half(t.rows);
-      const bool all = !l.order && hx > S::kX / 2;
+      const bool all = hx > S::kX / 2;
       const int boxes = l.order ? 0 : all ? S::kX / 32 : (hx + 31) / 32;
-      const int bytes = CG * (128 * 128 + boxes * 4096);
-      const int x0 = t.row + pair * hx;
+      const int bytes = CG * S::kSub * (128 * 128 + boxes * 4096);
+      const int x0 = t.row + pair * hx, nt = t.n * CG + pair;
       for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
         if (it >= ST && !warp_wait(&c.empty[s], (it / ST - 1) & 1, &c.abort_flag, a.l.status)) {
           ok = false;
           break;
         }
-        uint8_t* p = stg + (size_t)s * S::kStage;
-        const int x = ks * 64;
         const uint32_t bar = CG == 1 ? sa(&c.full[s]) : peer_addr(sa(&c.full[s]), first);
         if (elect_one()) {
           // a pair's copies all count on the first CTA's barrier
-          if (pair == 0) mbar_expect(&c.full[s], bytes);
-          const int nt = t.n * CG + pair;
-          if (l.gated) {
+          if (warp == kTmaWarp && pair == 0) mbar_expect(&c.full[s], bytes);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_gated<CG>(p + j * 4096, &wmap, x, nt * 4 + j, t.group, bar);
-          } else {
-            load_rows<CG>(p, &wmap, x, nt * 128, t.group, bar);
-          }
-          if (all) {
-            tma_load<CG>(p + 128 * 128, &xmap_all, x, x0, bar);
-          } else {
-            for (int j = 0; j < boxes; ++j) tma_load<CG>(p + 128 * 128 + j * 4096, &xmap, x, x0 + 32 * j, bar);
+          for (int q = 0; q < S::kSub; ++q) {
+            uint8_t* p = stg + (size_t)s * S::kStage + q * S::kSlab;
+            const int x = (ks * S::kSub + q) * 64;
+            if (warp == kTmaWarp) {
+              if (l.gated) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) load_gated<CG>(p + j * 4096, &wmap, x, nt * 4 + j, t.group, bar);
+              } else {
+                load_rows<CG>(p, &wmap, x, nt * 128, t.group, bar);
+              }
+            } else if (all) {
+              tma_load<CG>(p + 128 * 128, &xmap_all, x, x0, bar);
+            } else {
+              for (int j = 0; j < boxes; ++j) tma_load<CG>(p + 128 * 128 + j * 4096, &xmap, x, x0 + 32 * j, bar);
+            }
           }
         }
         __syncwarp();
@@ -402,8 +429,10 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           if (elect_one()) {
             const uint64_t w0 = w_base + (uint64_t)(s * (S::kStage / 16)), x0 = x_base + (uint64_t)(s * (S::kStage / 16));
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // 32 bytes of every row each
-              mma<CG>(d, w0 + 2 * j, x0 + 2 * j, id, j > 0 || k > first_of);
+            for (int j = 0; j < 4 * S::kSub; ++j) {  // 32 bytes of every row each
+              const int at = j / 4 * (S::kSlab / 16) + j % 4 * 2;
+              mma<CG>(d, w0 + at, x0 + at, id, j > 0 || k > first_of);
+            }
             mma_commit<CG>(&c.empty[s], both);
           }
           __syncwarp();
@@ -435,14 +464,14 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     }
     drain_bar(&c.drain, 0);  // every MMA has finished before the tensor memory is freed
     __syncwarp();
-  } else if (warp >= kGatherWarp) {
+  } else if (warp >= kRowWarp) {
     // Rows of x by the order's indices: 16 bytes a lane, four rows a warp and instruction, in the
     // copies' swizzle.  A thread's copies arrive at `landed` by themselves; the warp that waits
     // there fences them for the MMAs.  (TMA's four-row gathers took about 70 cycles each, 2,200 a
     // stage of 128 rows; a fence by the copying threads waits for all their copies in flight.)
     if (l.order) {
       constexpr int kPer = S::kX / 8;  // rows of a lane
-      const int gw = warp - kGatherWarp, chunk = lane & 7, r0 = 4 * gw + (lane >> 3);
+      const int gw = warp - kRowWarp, chunk = lane & 7, r0 = 4 * gw + (lane >> 3);
       int it = 0, s = 0;
       bool ok = true;
       for (int i = tile0; ok && walk.seek(i, t); i += step) {
@@ -455,20 +484,23 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           const int r = min(pair * hx + r0 + 8 * j, t.rows - 1);
           row[j] = (uint32_t)(max(source_row(l, t.row + r), 0) * (l.x_stride / 8));
         }
-        const uint4* from = reinterpret_cast<const uint4*>(l.x) + k_lo * 8 + chunk;
-        for (int ks = k_lo; ks < k_hi; ++ks, ++it, from += 8) {
+        const uint4* from = reinterpret_cast<const uint4*>(l.x) + (long long)k_lo * S::kSub * 8 + chunk;
+        for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
           if (it >= ST && !warp_wait(&c.empty[s], (it / ST - 1) & 1, &c.abort_flag, a.l.status)) {
             ok = false;
             break;
           }
-          const uint32_t dst = sa(stg + (size_t)s * S::kStage) + 128 * 128 + r0 * 128 + ((chunk ^ r0) << 4);
-          const int bytes = ks * 64ll + chunk * 8 < l.k ? 16 : 0;  // zeros past K, without a read
+          uint32_t dst = sa(stg + (size_t)s * S::kStage) + 128 * 128 + r0 * 128 + ((chunk ^ r0) << 4);
 #pragma unroll
-          for (int j = 0; j < kPer; j += 2)
-            if (8 * j < hx) {
+          for (int q = 0; q < S::kSub; ++q, dst += S::kSlab, from += 8) {
+            const int bytes = (ks * S::kSub + q) * 64ll + chunk * 8 < l.k ? 16 : 0;  // zeros past K, without a read
 #pragma unroll
-              for (int z = 0; z < 2; ++z) copy16(dst + (j + z) * 1024, from + row[j + z], bytes);
-            }
+            for (int j = 0; j < kPer; j += 2)
+              if (8 * j < hx) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) copy16(dst + (j + z) * 1024, from + row[j + z], bytes);
+              }
+          }
           copies_arrive(&c.landed[s]);
           s = s + 1 == ST ? 0 : s + 1;
         }
@@ -586,7 +618,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     if (!here && a.l.status) atomicOr(a.l.status, (unsigned long long)MOE_STATUS_TIMEOUT);
     __syncthreads();
     cluster_arrive();  // what the peers copied here has left their shared memory
-    walk.start(l, kShift, 16, a.tn);
+    walk.start(l, a.shift, 16, a.tn, a.tiles, a.width);
     if (here && walk.seek(tile0, t)) {
       auto sum = [&](int row, int col) {  // a row of this part's, over the parts
         float v = 0.f;
@@ -631,12 +663,11 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   }
 }
 
-// Parts of K that give every SM a CTA where tiles are few.
-int split_for(long long tiles, int nk, int cg, int sms) {
-  int s = 1;
-  while (2 * s <= kMaxCluster / cg && 2 * s <= nk && tiles * cg * 2 * s <= sms) s *= 2;
-  return s;
-}
+// How a product is cut: the kernel's tile, a dense product's tiles of tokens and their width, parts of K.
+struct Cut {
+  int nt, cg, tiles, width, split;
+  long long cost;
+};
 
 long long tiles_n(const Linear& l, int cg) {
   const int per = (l.gated ? 64 : 128) * cg;
@@ -644,7 +675,7 @@ long long tiles_n(const Linear& l, int cg) {
 }
 
 template <int NT, int CG>
-cudaError_t launch(const Linear& l, int sms, cudaStream_t s) {
+cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
   using S = Shape<NT, CG>;
   auto kern = linear_kernel<NT, CG>;
   static Once once;
@@ -653,12 +684,14 @@ cudaError_t launch(const Linear& l, int sms, cudaStream_t s) {
   Args a{};
   a.l = l;
   const long long tn = tiles_n(l, CG);
-  constexpr int kShift = NT == 32 ? 5 : NT == 128 ? 7 : 8;
-  const long long most = l.offsets ? most_tiles(l, kShift, tn) : (l.rows + (long long)NT - 1) / NT * tn;
+  a.shift = NT == 32 ? 5 : NT == 128 ? 7 : 8;
+  a.tiles = cut.tiles;
+  a.width = cut.width;
+  const long long most = l.offsets ? most_tiles(l, a.shift, tn) : cut.tiles * tn;
   if (most > 0x3fffffff) return cudaErrorInvalidValue;
   a.tn = (int)tn;
-  a.nk = (int)((l.k + 63ll) / 64);
-  a.split = l.offsets ? 1 : split_for(most, a.nk, CG, sms);
+  a.nk = (int)((l.k + 64ll * S::kSub - 1) / (64 * S::kSub));
+  a.split = cut.split;
   const int team = CG * a.split;
   auto whole = [&](const void* p, long long stride) {  // 4 results
     return (reinterpret_cast<uintptr_t>(p) & (l.f32 ? 15 : 7)) == 0 && stride % 4 == 0;
@@ -685,30 +718,55 @@ cudaError_t launch(const Linear& l, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, wm, xm, xa, a);
 }
 
-// Estimated cycles of a dense product with this tile: a stage's MMAs take 2 cycles per token, its
-// copies a cycle per 64 bytes.
+// Parts of K that give every SM a CTA where tiles are few.
+int split_for(long long tiles, int nk, int cg, int sms) {
+  int s = 1;
+  while (2 * s <= kMaxCluster / cg && 2 * s <= nk && tiles * cg * 2 * s <= sms) s *= 2;
+  return s;
+}
+
+// Estimated cycles of a dense product cut into `tiles` of tokens, kept if less than `best`'s.
 template <int NT, int CG>
-long long cycles(const Linear& l, int sms) {
-  const long long tm = (l.rows + (long long)NT - 1) / NT, tiles = tm * tiles_n(l, CG);
-  const int nk = (int)((l.k + 63ll) / 64), split = split_for(tiles, nk, CG, sms);
-  const int width = (int)(((l.rows + tm - 1) / tm + 15) / 16 * 16);
-  const int copies = (128 * 128 + width / CG * 128) / 64, stage = 2 * width > copies ? 2 * width : copies;
-  const long long per = sms / (CG * split), waves = (tiles + per - 1) / per;
-  return waves * ((nk + split - 1) / split * (long long)stage) + (split > 1 ? 2500 + 128 * NT * 4 / 18 : 0);
+void consider(const Linear& l, int sms, long long tiles, Cut& best) {
+  if (tiles < (l.rows + (long long)NT - 1) / NT || tiles > (l.rows + 15ll) / 16) return;
+  const int width = (int)((l.rows + tiles - 1) / tiles + 15) / 16 * 16;
+  tiles = (l.rows + (long long)width - 1) / width;
+  const long long all = tiles * tiles_n(l, CG);
+  const int nk = (int)((l.k + 63ll) / 64);
+  // a slab of 64 of K: its MMAs, its copies, the issuing warps' time
+  const int mmas = 2 * width, copies = (128 * 128 + width / CG * 128) / 68, issue = CG == 1 ? 250 : 400;
+  const int slab = mmas > copies ? (mmas > issue ? mmas : issue) : (copies > issue ? copies : issue);
+  for (int split = 1; split <= split_for(all, nk, CG, sms); split *= 2) {
+    const long long per = sms / (CG * split), waves = (all + per - 1) / per;
+    const long long cost = waves * ((nk + split - 1) / split) * slab + width * 40 + (split > 1 ? 3000 + 60 * NT : 0);
+    if (best.nt == 0 || cost < best.cost) best = {NT, CG, (int)tiles, width, split, cost};
+  }
+}
+template <int NT, int CG>
+void consider(const Linear& l, int sms, Cut& best) {
+  const long long least = (l.rows + (long long)NT - 1) / NT, tn = tiles_n(l, CG);
+  consider<NT, CG>(l, sms, least, best);
+  for (int waves = 1; waves <= 3; ++waves) {  // as many as fill the SMs so often
+    const long long t = waves * (long long)(sms / CG) / tn;
+    if (t > least) consider<NT, CG>(l, sms, t, best);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_linear_tc(const Linear& l, int sms, cudaStream_t s) {
+  Cut cut{0, 0, 0, 0, 1, 0};
   if (l.offsets) {
     // rows a group has on average decide; ragged sizes fill either tile as they come
-    if (l.rows / l.groups < 24) return launch<32, 1>(l, sms, s);
-    return launch<256, 2>(l, sms, s);
+    if (l.rows / l.groups < 24) return launch<32, 1>(l, cut, sms, s);
+    return launch<256, 2>(l, cut, sms, s);
   }
-  if (l.rows <= 32) return launch<32, 1>(l, sms, s);
-  const long long c32 = cycles<32, 1>(l, sms), c128 = cycles<128, 1>(l, sms), c256 = cycles<256, 2>(l, sms);
-  if (c256 <= c128 && c256 <= c32) return launch<256, 2>(l, sms, s);
-  return c128 <= c32 ? launch<128, 1>(l, sms, s) : launch<32, 1>(l, sms, s);
+  consider<32, 1>(l, sms, cut);
+  consider<128, 1>(l, sms, cut);
+  consider<256, 2>(l, sms, cut);
+  if (cut.nt == 32) return launch<32, 1>(l, cut, sms, s);
+  if (cut.nt == 128) return launch<128, 1>(l, cut, sms, s);
+  return launch<256, 2>(l, cut, sms, s);
 }
 
 }  // namespace moe
