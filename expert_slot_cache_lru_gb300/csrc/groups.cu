@@ -3,10 +3,11 @@
 //
 // The order is a stable counting sort in one launch of one cluster.  Every counting warp
 // takes a run of consecutive routes: it counts them by expert in its own counters in
-// shared memory (lanes with the same expert find one another, the first adds for all, so
-// no order of atomics matters); prefixes over the warps, the cluster's CTAs and the experts
-// turn the counts into each warp's first places; and a second pass over the routes hands
-// the places out.
+// shared memory (lanes with the same expert find one another by a ballot per bit of the id, the first
+// adds for all, so no order of atomics matters; __match_any_sync took three times as long where
+// the experts differ); prefixes over the warps, the cluster's CTAs (each CTA a slice of the
+// experts) and the experts turn the counts into each warp's first places; and a second pass
+// over the routes hands the places out.
 //
 // The combine is one pass bound by HBM: 16 bytes of a row per thread, the routes' loads
 // in flight together.
@@ -19,13 +20,18 @@ namespace {
 
 constexpr unsigned kAll = lin::kAll;
 constexpr int kMaxPer = 16;  // experts per thread of a block of 1,024
+constexpr int kCtas = 16;  // of the largest cluster
+// Routes up to which one CTA takes them, and up to which eight do (256 experts: 4,096 routes 9.9 us alone, 7.7 on
+// eight, 8.6 on sixteen; 65,536 15.6 on eight, 12.3 on sixteen, whose scattered stores bound them).
+constexpr int kAlone = 1024, kEight = 16384;
 
 struct GroupArgs {
   const int32_t* ids;
   int32_t *offsets, *order, *pos;
   int routes, experts;
   int warps, per_warp;  // counting warps of a CTA, routes of a warp (a multiple of 32)
-  int ctas;
+  int ctas, slice;      // experts of a CTA's slice
+  int bits;             // of an id
 };
 
 // inclusive sum over the lanes
@@ -45,7 +51,7 @@ __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
   extern __shared__ unsigned smem[];
   unsigned* first = smem;                              // [experts]: a CTA's routes, then its first place
   C* count = reinterpret_cast<C*>(smem + a.experts);   // [warps][experts]
-  __shared__ unsigned sums[32];
+  __shared__ unsigned sums[32], slice_total[kCtas];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
   const int rank = a.ctas == 1 ? 0 : (int)tc::cluster_rank();
   tc::pdl_trigger();
@@ -55,22 +61,46 @@ __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
   const long long lo = ((long long)rank * a.warps + warp) * a.per_warp;
   const int n_mine = warp < a.warps ? (int)max(0ll, min((long long)a.per_warp, a.routes - lo)) : 0;
   C* mine = count + (warp < a.warps ? warp : 0) * E;
+  const C* start = mine;
 
-  // the warp's routes, 32 at a time: f(route or -1, expert or -1, lanes with the same expert)
-  auto each = [&](auto f) {
-    int next = lane < n_mine ? a.ids[lo + lane] : -1;
-    for (int i = 0; i < n_mine; i += 32) {
-      const int id = next;
-      if (i + 32 + lane < n_mine) next = a.ids[lo + i + 32 + lane];
-      const int e = i + lane < n_mine && (unsigned)id < (unsigned)E ? id : -1;
-      const unsigned same = __match_any_sync(kAll, e);
-      f(i + lane < n_mine ? (int)(lo + i + lane) : -1, e, same);
-      __syncwarp();
+  // The place of each lane's route among those of its expert that the warp has seen, which are counted: lanes
+  // with the same expert find one another by a ballot per bit, the first adds for all.
+  auto count_in = [&](int e) {
+    const unsigned valid = __ballot_sync(kAll, e >= 0);
+    unsigned same = e >= 0 ? valid : 0u;
+    for (int b = 0; b < a.bits; b += 4) {
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const bool on = e >> (b + z) & 1;
+        const unsigned with = __ballot_sync(kAll, on);
+        same &= on ? with : ~with;
+      }
     }
+    const unsigned below = __popc(same & ((1u << lane) - 1));
+    unsigned rank = below;
+    if (e >= 0) rank += mine[e];
+    __syncwarp();
+    if (e >= 0 && below == 0) mine[e] += (C)__popc(same);
+    __syncwarp();
+    return rank;
   };
-  each([&](int, int e, unsigned same) {
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += (C)__popc(same);
-  });
+  // routes, their experts (-1: none) and, in the first pass over a warp's only block, their ranks
+  constexpr int U = 8;
+  int id[U];
+  unsigned rank_of[U];
+  const bool once = a.per_warp <= 32 * U;  // all of a warp's routes at once: the ranks stay in registers
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = i0 + 32 * u + lane < n_mine ? a.ids[lo + i0 + 32 * u + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = (unsigned)id[u] < (unsigned)E ? id[u] : -1;
+  };
+  for (int i0 = 0; i0 < n_mine; i0 += 32 * U) {
+    load(i0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + 32 * u < n_mine) rank_of[u] = count_in(id[u]);
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += THREADS) {  // counts to prefixes over the warps
     unsigned sum = 0;
@@ -83,49 +113,101 @@ __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
   }
   if (a.ctas > 1) tc::cluster_sync();
   else __syncthreads();
-  // a thread's consecutive experts: routes of all CTAs, and of those before this one
-  const int per = (E + THREADS - 1) / THREADS, e0 = threadIdx.x * per;
-  unsigned all[kMaxPer], before[kMaxPer], sum = 0;
+  // a thread's consecutive experts of the CTA's slice: routes of each CTA, and places within the slice
+  const int per = (a.slice + THREADS - 1) / THREADS, e0 = rank * a.slice + threadIdx.x * per;
+  const int e1 = min(min(e0 + per, (rank + 1) * a.slice), E);
+  unsigned before[kMaxPer], sum = 0;  // before: an expert's routes and all before it of the thread's
 #pragma unroll
   for (int j = 0; j < kMaxPer; ++j) {
-    all[j] = before[j] = 0;
-    if (j < per && e0 + j < E) {
-      for (int c = 0; c < a.ctas; ++c) {
-        const unsigned n = a.ctas == 1 ? first[e0 + j] : tc::load_at(tc::peer_addr(tc::sa(first + e0 + j), c));
-        all[j] += n;
-        before[j] += c < rank ? n : 0;
+    before[j] = sum;
+    if (j < per && e0 + j < e1) {
+      if (a.ctas == 1) {
+        sum += first[e0 + j];
+      } else {
+        unsigned n[kCtas];
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c)
+          n[c] = c < a.ctas ? tc::load_at(tc::peer_addr(tc::sa(first + e0 + j), c)) : 0;
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) sum += n[c];
       }
-      sum += all[j];
     }
   }
   const unsigned incl = warp_scan(sum);
   if (lane == 31) sums[warp] = incl;
-  if (a.ctas > 1) tc::cluster_sync();  // everyone has read the CTAs' counts
-  else __syncthreads();
-  const unsigned part = lane < THREADS / 32 ? sums[lane] : 0, upto = warp_scan(part);
-  unsigned place = __shfl_sync(kAll, upto - part, warp) + incl - sum;
-  const unsigned total = __shfl_sync(kAll, upto, 31);
+  __syncthreads();
+  const unsigned in_warp = lane < THREADS / 32 ? sums[lane] : 0, upto = warp_scan(in_warp);
+  const unsigned place = __shfl_sync(kAll, upto - in_warp, warp) + incl - sum;
+  const unsigned total = __shfl_sync(kAll, upto, 31);  // of the slice
 #pragma unroll
   for (int j = 0; j < kMaxPer; ++j)
-    if (j < per && e0 + j < E) {
-      first[e0 + j] = place + before[j];
-      if (rank == 0) a.offsets[e0 + j] = (int32_t)place;
-      place += all[j];
+    if (j < per && e0 + j < e1) {  // first place of the expert's routes in each CTA, within the slice
+      unsigned at = place + before[j];
+      if (a.ctas == 1) {
+        first[e0 + j] = at;
+      } else {
+        unsigned n[kCtas];
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c)
+          n[c] = c < a.ctas ? tc::load_at(tc::peer_addr(tc::sa(first + e0 + j), c)) : 0;
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) {
+          if (c >= a.ctas) break;
+          tc::store_at(tc::peer_addr(tc::sa(first + e0 + j), c), (int)at);
+          at += n[c];
+        }
+      }
     }
-  if (rank == 0 && threadIdx.x == 0) a.offsets[E] = (int32_t)total;
+  if (a.ctas > 1) {
+    if (threadIdx.x < a.ctas) tc::store_at(tc::peer_addr(tc::sa(slice_total + rank), threadIdx.x), (int)total);
+    tc::cluster_sync();
+  } else {
+    if (threadIdx.x == 0) slice_total[0] = total;
+    __syncthreads();
+  }
+  unsigned base[kCtas], all = 0;  // places before each slice
+#pragma unroll
+  for (int c = 0; c < kCtas; ++c) {
+    base[c] = all;
+    if (c < a.ctas) all += slice_total[c];
+  }
+  if (a.ctas > 1) {
+    for (int e = threadIdx.x; e < E; e += THREADS) {
+      const int c = e / a.slice;
+#pragma unroll
+      for (int k = 1; k < kCtas; ++k)
+        if (c == k) first[e] += base[k];
+    }
+  }
+  unsigned mine_base = 0;
+#pragma unroll
+  for (int k = 1; k < kCtas; ++k)
+    if (rank == k) mine_base = base[k];
+#pragma unroll
+  for (int j = 0; j < kMaxPer; ++j)
+    if (j < per && e0 + j < e1) a.offsets[e0 + j] = (int32_t)(mine_base + place + before[j]);
+  if (rank == 0 && threadIdx.x == 0) a.offsets[E] = (int32_t)all;
   __syncthreads();
-  each([&](int r, int e, unsigned same) {
-    int p = -1;
-    if (e >= 0) p = (int)(first[e] + mine[e] + __popc(same & ((1u << lane) - 1)));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += (C)__popc(same);
-    if (r >= 0) {
+  for (int i0 = 0; i0 < n_mine; i0 += 32 * U) {
+    if (!once) {
+      load(i0);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + 32 * u < n_mine) rank_of[u] = count_in(id[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 32 * u + lane;
+      if (i >= n_mine) continue;
+      const int e = id[u], r = (int)(lo + i);
+      // counters hold the warp's first places and, in the second pass over a long run, its routes so far
+      const int p = e < 0 ? -1 : (int)(first[e] + rank_of[u] + (once ? start[e] : 0));
       if (a.pos) a.pos[r] = p;
       if (a.order && p >= 0) a.order[p] = r;
     }
-  });
+  }
   if (a.order)
-    for (long long i = total + (long long)rank * THREADS + threadIdx.x; i < a.routes;
+    for (long long i = all + (long long)rank * THREADS + threadIdx.x; i < a.routes;
          i += (long long)a.ctas * THREADS)
       a.order[i] = -1;
 }
@@ -134,7 +216,9 @@ template <typename C, int THREADS>
 cudaError_t launch_group(const GroupArgs& a, int smem, cudaStream_t s) {
   auto kern = group_kernel<C, THREADS>;
   static tc::Once once;
-  const cudaError_t e = tc::raise_smem(once, kern, 226 * 1024);
+  cudaError_t e = tc::raise_smem(once, kern, 226 * 1024);
+  if (e != cudaSuccess) return e;
+  if (a.ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.ctas);
@@ -197,71 +281,121 @@ __device__ __forceinline__ void store_v(__nv_bfloat16* p, const float (&v)[V]) {
   }
 }
 
-// Y, O: types of y and of add and out; V elements per thread, `pieces` per row
-template <typename Y, typename O, int V>
-__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int pieces) {
+// Y, O: types of y and of add and out; V elements per thread.  A CTA takes `rows_per` rows at a time, or 256 of
+// `pieces` pieces of one row; a thread has IT such items at once and U routes of each, all loaded before
+// any is used, and loads the next ones' places and weights while it waits.
+template <typename Y, typename O, int V, int U, int IT>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int pieces, int rows_per, int chunks) {
   tc::pdl_trigger();
   tc::pdl_wait();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, b = i / pieces;
-  if (b >= a.rows) return;
-  const long long c = (i - b * pieces) * V;
-  const Y* y = static_cast<const Y*>(a.y) + c;
-  const int32_t* pos = a.pos + b * a.k;
-  const float* w = a.w + b * a.k;
-  float acc[V] = {};
-  if (a.add) {
-    Raw<O, V> r;
-    r.load(static_cast<const O*>(a.add) + b * a.add_stride + c);
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = r.at(e);
-  }
-  constexpr int U = sizeof(Y) == 4 ? 4 : 8;  // routes in flight: loaded before any is used
-  for (int j0 = 0; j0 < a.k; j0 += U) {
-    int p[U];
-    float f[U];
-    Raw<Y, V> v[U];
+  const int sub = rows_per > 1 ? threadIdx.x / pieces : 0, c0 = threadIdx.x - sub * pieces;
+  const unsigned items = (unsigned)((a.rows + rows_per - 1ll) / rows_per * chunks), step = gridDim.x * IT;
+  int p[IT][U], p_next[IT][U];
+  float f[IT][U], f_next[IT][U];
+  struct At {
+    long long b;
+    long long c;
+    bool in;
+  };
+  auto at = [&](unsigned i) {
+    const unsigned g = chunks > 1 ? i / chunks : i;
+    const int piece = chunks > 1 ? (int)(i - g * chunks) * 256 + c0 : c0;
+    const long long b = (long long)g * rows_per + sub;
+    return At{b, (long long)piece * V, i < items && sub < rows_per && piece < pieces && b < a.rows};
+  };
+  auto places = [&](const At& x, int j0, int (&to)[U], float (&weight)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      p[u] = j0 + u < a.k ? pos[j0 + u] : -1;
-      f[u] = j0 + u < a.k ? w[j0 + u] : 0.f;
+      const bool in = x.in && j0 + u < a.k;
+      to[u] = in ? a.pos[x.b * a.k + j0 + u] : -1;
+      weight[u] = in ? a.w[x.b * a.k + j0 + u] : 0.f;
+    }
+  };
+  unsigned i = blockIdx.x * IT;
+#pragma unroll
+  for (int t = 0; t < IT; ++t) places(at(i + t), 0, p[t], f[t]);
+  for (; i < items; i += step) {
+    At x[IT];
+    float acc[IT][V] = {};
+#pragma unroll
+    for (int t = 0; t < IT; ++t) x[t] = at(i + t);
+    for (int j0 = 0; j0 < a.k; j0 += U) {
+      Raw<Y, V> v[IT][U];
+      Raw<O, V> r[IT];
+#pragma unroll
+      for (int t = 0; t < IT; ++t) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if ((unsigned)p[t][u] < (unsigned)a.y_rows)
+            v[t][u].load(static_cast<const Y*>(a.y) + p[t][u] * a.y_stride + x[t].c);
+        if (j0 == 0 && a.add && x[t].in) r[t].load(static_cast<const O*>(a.add) + x[t].b * a.add_stride + x[t].c);
+      }
+#pragma unroll
+      for (int t = 0; t < IT; ++t) {
+        if (j0 + U < a.k) places(x[t], j0 + U, p_next[t], f_next[t]);
+        else places(at(i + step + t), 0, p_next[t], f_next[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < IT; ++t) {
+        if (j0 == 0 && a.add && x[t].in)
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[t][e] = r[t].at(e);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if ((unsigned)p[t][u] < (unsigned)a.y_rows)
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[t][e] = fmaf(f[t][u], v[t][u].at(e), acc[t][e]);
+          p[t][u] = p_next[t][u], f[t][u] = f_next[t][u];
+        }
+      }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if ((unsigned)p[u] < (unsigned)a.y_rows) v[u].load(y + p[u] * a.y_stride);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if ((unsigned)p[u] < (unsigned)a.y_rows)
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(f[u], v[u].at(e), acc[e]);
+    for (int t = 0; t < IT; ++t)
+      if (x[t].in) store_v<V>(static_cast<O*>(a.out) + x[t].b * a.out_stride + x[t].c, acc[t]);
   }
-  store_v<V>(static_cast<O*>(a.out) + b * a.out_stride + c, acc);
 }
 
+template <typename Y, typename O, int V, int U, int IT>
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s) {
+  tc::DeviceInfo d;
+  const cudaError_t e = tc::device_info(&d);
+  if (e != cudaSuccess) return e;
+  const int pieces = a.hidden / V, rows_per = pieces < 256 ? 256 / pieces : 1, chunks = (pieces + 255) / 256;
+  const long long items = (a.rows + rows_per - 1ll) / rows_per * chunks;
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  // two CTAs an SM fill it with 16-byte loads (3 to 12: up to 4 us more of 57 for 8,192 x 8 x 2,048); single elements want
+  // more threads
+  const long long blocks = (items + IT - 1) / IT, most = (V == 1 ? 8ll : 2ll) * d.sms;
+  return tc::launch_early(combine_kernel<Y, O, V, U, IT>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                          s, a, pieces, rows_per, chunks);
+}
 template <typename Y, typename O>
 cudaError_t combine(const CombineArgs& a, cudaStream_t s) {
   auto whole = [](const void* p, long long stride, size_t e) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * e % 16 == 0;
   };
-  const bool wide = a.hidden % 8 == 0 && whole(a.y, a.y_stride, sizeof(Y)) &&
-                    whole(a.add, a.add ? a.add_stride : 0, sizeof(O)) && whole(a.out, a.out_stride, sizeof(O));
-  const int pieces = wide ? a.hidden / 8 : a.hidden;
-  const long long blocks = ((long long)a.rows * pieces + 255) / 256;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), block(256);
-  if (wide) return tc::launch_early(combine_kernel<Y, O, 8>, grid, block, 0, s, a, pieces);
-  return tc::launch_early(combine_kernel<Y, O, 1>, grid, block, 0, s, a, pieces);
+  constexpr int N = sizeof(Y) == 4 ? 4 : 8;  // loads of a thread in flight
+  if (a.hidden % 8 == 0 && whole(a.y, a.y_stride, sizeof(Y)) &&
+      whole(a.add, a.add ? a.add_stride : 0, sizeof(O)) && whole(a.out, a.out_stride, sizeof(O))) {
+    if (a.k <= 2) return launch_combine<Y, O, 8, 2, N / 2>(a, s);
+    if (a.k <= 4) return launch_combine<Y, O, 8, 4, N / 4>(a, s);
+    return launch_combine<Y, O, 8, N, 1>(a, s);
+  }
+  return launch_combine<Y, O, 1, 8, 1>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_group_routes(const int32_t* ids, int routes, int experts, int32_t* offsets,
                                 int32_t* order, int32_t* pos, cudaStream_t s) {
-  GroupArgs a{ids, offsets, order, pos, routes, experts, 1, 32, 1};
+  GroupArgs a{ids, offsets, order, pos, routes, experts, 1, 32, 1, experts, 0};
+  while ((experts - 1) >> a.bits) ++a.bits;
   // a CTA holds 32 warps of counters where they fit, at least 3 (16,384 experts in 16 bits)
   const int room = 224 * 1024 - 4 * experts;
   auto plan = [&](int bytes) {
     const int most = room / (bytes * experts) < 32 ? room / (bytes * experts) : 32;
-    a.ctas = routes <= 32 * 32 ? 1 : 8;
+    a.ctas = routes <= kAlone ? 1 : routes <= kEight ? 8 : kCtas;
+    a.slice = (experts + a.ctas - 1) / a.ctas;
     const long long runs = (routes + 31ll) / 32;  // 32 routes each
     a.warps = (int)(runs < most ? (runs > 0 ? runs : 1) : most);
     const long long all = (long long)a.warps * a.ctas;

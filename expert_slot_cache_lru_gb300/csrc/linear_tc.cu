@@ -218,8 +218,7 @@ struct Epilogue {
       for (int i = 0; i < 16; ++i)
         if (i * by < 16 && in && (mask >> (first + i * by) & 1)) {
           const char* q = p + i * by * l.res_stride * es;
-          r[i / 4][i % 4] = f32 ? *reinterpret_cast<const uint32_t*>(q)
-                                : (uint32_t)*reinterpret_cast<const uint16_t*>(q) << 16;
+          r[i / 4][i % 4] = f32 ? *reinterpret_cast<const uint32_t*>(q) : *reinterpret_cast<const uint16_t*>(q);
         }
     }
   }
@@ -285,7 +284,7 @@ struct Epilogue {
       float y = act(lds(at) + bias[0]);
       if (GATED) y *= lds(at ^ 64) + ubias[0];
       y *= l.alpha;
-      if (l.res) y += __uint_as_float(r[i / 4][i % 4]);
+      if (l.res) y += __uint_as_float(f32 ? r[i / 4][i % 4] : r[i / 4][i % 4] << 16);
       if (in && (mask >> (first + BY * i) & 1)) {
         char* q = p + i * BY * l.out_stride * es;
         if (f32) *reinterpret_cast<float*>(q) = y;
@@ -358,7 +357,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     for (int i = tile0; ok && walk.seek(i, t); i += step) {
       // boxes of 32 rows, or all the CTA has room for at once
       const int hx = half(t.rows);
-      const bool all = hx > S::kX / 2;
+      const bool all = hx > S::kX - 32;
       const int boxes = l.order ? 0 : all ? S::kX / 32 : (hx + 31) / 32;
       const int bytes = CG * S::kSub * (128 * 128 + boxes * 4096);
       const int x0 = t.row + pair * hx, nt = t.n * CG + pair;
@@ -734,7 +733,7 @@ void consider(const Linear& l, int sms, long long tiles, Cut& best) {
   const long long all = tiles * tiles_n(l, CG);
   const int nk = (int)((l.k + 63ll) / 64);
   // a slab of 64 of K: its MMAs, its copies, the issuing warps' time
-  const int mmas = 2 * width, copies = (128 * 128 + width / CG * 128) / 68, issue = CG == 1 ? 250 : 400;
+  const int mmas = 2 * width, copies = (128 * 128 + (width / CG + 31) / 32 * 4096) / 68, issue = CG == 1 ? 250 : 400;
   const int slab = mmas > copies ? (mmas > issue ? mmas : issue) : (copies > issue ? copies : issue);
   for (int split = 1; split <= split_for(all, nk, CG, sms); split *= 2) {
     const long long per = sms / (CG * split), waves = (all + per - 1) / per;
