@@ -48,6 +48,7 @@ int check_linear(moe::Linear& l, int gated, int dtype) {
   if (!take_stride(l.x_stride, l.k) || !take_stride(l.w_stride, l.k) ||
       !take_stride(l.out_stride, l.n) || !take_stride(l.res_stride, l.n))
     return MOE_ERR_INVALID_ARG;
+  if (l.w_stride > (1ll << 62) / wide) return MOE_ERR_UNSUPPORTED;
   if (l.group_stride == 0) l.group_stride = wide * l.w_stride;
   if (l.group_stride < (wide - 1) * l.w_stride + l.k) return MOE_ERR_INVALID_ARG;
   if (l.rows == 0) return MOE_OK;

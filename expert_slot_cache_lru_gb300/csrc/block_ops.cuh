@@ -68,6 +68,8 @@ struct Linear {
   long long x_stride, w_stride, group_stride, res_stride, out_stride;
   const int32_t *order, *offsets;
   int x_rows, per_row, groups;
+  unsigned per_mul;  // r / per_row (launch_linear)
+  int per_shift;
   int rows, n, k, act;
   bool gated, f32;
   float alpha;

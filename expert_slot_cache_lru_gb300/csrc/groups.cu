@@ -19,7 +19,6 @@ namespace moe {
 namespace {
 
 constexpr unsigned kAll = lin::kAll;
-constexpr int kMaxPer = 16;  // experts per thread of a block of 1,024
 constexpr int kCtas = 16;  // of the largest cluster
 // Routes up to which one CTA takes them, and up to which eight do (256 experts: 4,096 routes 9.9 us alone, 7.7 on
 // eight, 8.6 on sixteen; 65,536 15.6 on eight, 12.3 on sixteen, whose scattered stores bound them).
@@ -45,15 +44,16 @@ __device__ __forceinline__ unsigned warp_scan(unsigned v) {
   return v;
 }
 
-// C: type of a warp's counters, which hold up to a CTA's routes
-template <typename C, int THREADS>
+// C: type of a warp's counters, which hold up to a CTA's routes; CTAS: a cluster's at most (one: all of it fits
+// the block); PER: experts of the slice per thread at most
+template <typename C, int THREADS, int CTAS, int PER>
 __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
   extern __shared__ unsigned smem[];
   unsigned* first = smem;                              // [experts]: a CTA's routes, then its first place
   C* count = reinterpret_cast<C*>(smem + a.experts);   // [warps][experts]
-  __shared__ unsigned sums[32], slice_total[kCtas];
+  __shared__ unsigned sums[32], slice_total[CTAS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
-  const int rank = a.ctas == 1 ? 0 : (int)tc::cluster_rank();
+  const int rank = CTAS == 1 ? 0 : (int)tc::cluster_rank();
   tc::pdl_trigger();
   for (int i = threadIdx.x; i < a.warps * E; i += THREADS) count[i] = 0;
   __syncthreads();
@@ -111,25 +111,25 @@ __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
     }
     first[e] = sum;
   }
-  if (a.ctas > 1) tc::cluster_sync();
+  if (CTAS > 1) tc::cluster_sync();
   else __syncthreads();
   // a thread's consecutive experts of the CTA's slice: routes of each CTA, and places within the slice
   const int per = (a.slice + THREADS - 1) / THREADS, e0 = rank * a.slice + threadIdx.x * per;
   const int e1 = min(min(e0 + per, (rank + 1) * a.slice), E);
-  unsigned before[kMaxPer], sum = 0;  // before: an expert's routes and all before it of the thread's
+  unsigned before[PER], sum = 0;  // before: an expert's routes and all before it of the thread's
 #pragma unroll
-  for (int j = 0; j < kMaxPer; ++j) {
+  for (int j = 0; j < PER; ++j) {
     before[j] = sum;
     if (j < per && e0 + j < e1) {
-      if (a.ctas == 1) {
+      if (CTAS == 1) {
         sum += first[e0 + j];
       } else {
-        unsigned n[kCtas];
+        unsigned n[CTAS];
 #pragma unroll
-        for (int c = 0; c < kCtas; ++c)
+        for (int c = 0; c < CTAS; ++c)
           n[c] = c < a.ctas ? tc::load_at(tc::peer_addr(tc::sa(first + e0 + j), c)) : 0;
 #pragma unroll
-        for (int c = 0; c < kCtas; ++c) sum += n[c];
+        for (int c = 0; c < CTAS; ++c) sum += n[c];
       }
     }
   }
@@ -140,51 +140,51 @@ __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
   const unsigned place = __shfl_sync(kAll, upto - in_warp, warp) + incl - sum;
   const unsigned total = __shfl_sync(kAll, upto, 31);  // of the slice
 #pragma unroll
-  for (int j = 0; j < kMaxPer; ++j)
+  for (int j = 0; j < PER; ++j)
     if (j < per && e0 + j < e1) {  // first place of the expert's routes in each CTA, within the slice
       unsigned at = place + before[j];
-      if (a.ctas == 1) {
+      if (CTAS == 1) {
         first[e0 + j] = at;
       } else {
-        unsigned n[kCtas];
+        unsigned n[CTAS];
 #pragma unroll
-        for (int c = 0; c < kCtas; ++c)
+        for (int c = 0; c < CTAS; ++c)
           n[c] = c < a.ctas ? tc::load_at(tc::peer_addr(tc::sa(first + e0 + j), c)) : 0;
 #pragma unroll
-        for (int c = 0; c < kCtas; ++c) {
+        for (int c = 0; c < CTAS; ++c) {
           if (c >= a.ctas) break;
           tc::store_at(tc::peer_addr(tc::sa(first + e0 + j), c), (int)at);
           at += n[c];
         }
       }
     }
-  if (a.ctas > 1) {
+  if (CTAS > 1) {
     if (threadIdx.x < a.ctas) tc::store_at(tc::peer_addr(tc::sa(slice_total + rank), threadIdx.x), (int)total);
     tc::cluster_sync();
   } else {
     if (threadIdx.x == 0) slice_total[0] = total;
     __syncthreads();
   }
-  unsigned base[kCtas], all = 0;  // places before each slice
+  unsigned base[CTAS], all = 0;  // places before each slice
 #pragma unroll
-  for (int c = 0; c < kCtas; ++c) {
+  for (int c = 0; c < CTAS; ++c) {
     base[c] = all;
     if (c < a.ctas) all += slice_total[c];
   }
-  if (a.ctas > 1) {
+  if (CTAS > 1) {
     for (int e = threadIdx.x; e < E; e += THREADS) {
       const int c = e / a.slice;
 #pragma unroll
-      for (int k = 1; k < kCtas; ++k)
+      for (int k = 1; k < CTAS; ++k)
         if (c == k) first[e] += base[k];
     }
   }
   unsigned mine_base = 0;
 #pragma unroll
-  for (int k = 1; k < kCtas; ++k)
+  for (int k = 1; k < CTAS; ++k)
     if (rank == k) mine_base = base[k];
 #pragma unroll
-  for (int j = 0; j < kMaxPer; ++j)
+  for (int j = 0; j < PER; ++j)
     if (j < per && e0 + j < e1) a.offsets[e0 + j] = (int32_t)(mine_base + place + before[j]);
   if (rank == 0 && threadIdx.x == 0) a.offsets[E] = (int32_t)all;
   __syncthreads();
@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
       a.order[i] = -1;
 }
 
-template <typename C, int THREADS>
+template <typename C, int THREADS, int CTAS, int PER>
 cudaError_t launch_group(const GroupArgs& a, int smem, cudaStream_t s) {
-  auto kern = group_kernel<C, THREADS>;
+  auto kern = group_kernel<C, THREADS, CTAS, PER>;
   static tc::Once once;
   cudaError_t e = tc::raise_smem(once, kern, 226 * 1024);
   if (e != cudaSuccess) return e;
@@ -406,9 +406,10 @@ cudaError_t launch_group_routes(const int32_t* ids, int routes, int experts, int
   int smem = plan(2);
   const bool narrow = (long long)a.warps * a.per_warp <= 65535;
   if (!narrow) smem = plan(4);
-  const bool small = routes <= 256 && experts <= 1024;
-  if (small) return launch_group<uint16_t, 256>(a, smem, s);
-  return narrow ? launch_group<uint16_t, 1024>(a, smem, s) : launch_group<uint32_t, 1024>(a, smem, s);
+  if (routes <= 256 && experts <= 1024) return launch_group<uint16_t, 256, 1, 4>(a, smem, s);
+  if (a.ctas == 1) return launch_group<uint16_t, 1024, 1, 16>(a, smem, s);  // few routes: 16 bits hold them
+  return narrow ? launch_group<uint16_t, 1024, kCtas, 2>(a, smem, s)
+                : launch_group<uint32_t, 1024, kCtas, 2>(a, smem, s);
 }
 
 cudaError_t launch_combine(const CombineArgs& a, int y_dtype, int dtype, cudaStream_t s) {

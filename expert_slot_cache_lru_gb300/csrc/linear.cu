@@ -239,17 +239,22 @@ cudaError_t launch_tiles(const Linear& l, int sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_linear(const Linear& l, cudaStream_t s) {
+cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
+  Linear l = call;
+  division_of(l.per_row, l.per_mul, l.per_shift);
   tc::DeviceInfo d;
   const cudaError_t e = tc::device_info(&d);
   if (e != cudaSuccess) return e;
   const bool whole = l.k % 8 == 0 && l.x_stride % 8 == 0 && l.w_stride % 8 == 0 && l.group_stride % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
-  // gathered rows are addressed in 32 bits of 16-byte pieces
-  const bool near = !l.order || (double)l.x_rows * l.x_stride / 8 < 4294967296.0;
   if (whole && l.offsets && l.rows <= kDotPlaces) return launch_dots<1>(l, s);
   if (whole && !l.offsets && l.rows <= kDotRows)
     return l.rows == 1 ? launch_dots<1>(l, s) : l.rows == 2 ? launch_dots<2>(l, s) : launch_dots<4>(l, s);
+  // What the tensor-core kernel's copies address: strides below 2^40 bytes, gathered rows in 32 bits of 16-byte
+  // pieces; and a tile's K within what its waits allow (512 cycles for 64 of K).
+  const long long most = 1ll << 38;
+  const bool near = l.x_stride < most && l.w_stride < most / (l.gated ? l.n : 1) && l.group_stride < most &&
+                    (!l.order || l.x_rows <= (1ll << 35) / l.x_stride) && l.k <= 1 << 26;
   if (whole && near && (!l.gated || l.n % 16 == 0)) return launch_linear_tc(l, d.sms, s);
   return l.gated ? launch_tiles<true>(l, d.sms, s) : launch_tiles<false>(l, d.sms, s);
 }

@@ -51,12 +51,22 @@ __device__ __forceinline__ void finish(const Linear& l, long long row, long long
   store_out(l, row * l.out_stride + n, v);
 }
 
-// The row of x behind place p, or -1 where there is none.
-__device__ __forceinline__ int source_row(const Linear& l, int p) {
-  if (!l.order) return p;
-  const int r = l.order[p];
-  const int b = r < 0 ? -1 : r / l.per_row;
-  return b < l.x_rows ? b : -1;
+// The row of x behind an entry of the order, or -1 where there is none: r / per_row by a product (per_mul and
+// per_shift from division_of).
+__device__ __forceinline__ int row_of(const Linear& l, int r) {
+  const int b = (int)((__umulhi(l.per_mul, (unsigned)r) + (unsigned)r) >> l.per_shift);
+  return r >= 0 && b < l.x_rows ? b : -1;
+}
+// ... behind place p
+__device__ __forceinline__ int source_row(const Linear& l, int p) { return l.order ? row_of(l, l.order[p]) : p; }
+
+// Factor and shift with (umulhi(mul, r) + r) >> shift == r / d for 0 <= r < 2^31: with 2^shift >= d the factor is
+// 2^32 (2^shift - d) / d + 1, rounded down, so that mul + 2^32 is 2^(32 + shift) / d to an excess of at most 1,
+// which r < 2^31 times makes less than a step of the quotient.
+inline void division_of(int d, unsigned& mul, int& shift) {
+  shift = 0;
+  while ((1ll << shift) < d) ++shift;
+  mul = (unsigned)((((1ull << shift) - d) << 32) / d + 1);
 }
 
 // Tiles of ragged groups in order, for a warp that asks for rising tile numbers.  A
@@ -73,6 +83,7 @@ struct Walk {
   const int32_t* offsets;
   int groups, total_rows, shift, gran, tn;  // tiles of up to 1 << shift rows
   int g0;         // first group of this chunk
+  int reach;      // where the groups so far end
   int base, end;  // tile numbers of this chunk
   int lo[4], hi[4], ahead[5], incl;
   int dense_tiles, dense_width;  // of tokens, where there are no groups
@@ -89,11 +100,28 @@ struct Walk {
   }
   __device__ __forceinline__ int tiles(int i) const { return parts(hi[i] - lo[i]) * tn; }
   __device__ __forceinline__ void take() {  // the chunk from `ahead`
-    int sum = 0;
+    // offsets within 0 .. total_rows; a group starts no earlier than those before it end, so that offsets
+    // that do not ascend make no more tiles than there can be
+    int most = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       lo[i] = min(max(ahead[i], 0), total_rows);
-      hi[i] = max(lo[i], min(ahead[i + 1], total_rows));
+      hi[i] = min(max(ahead[i + 1], 0), total_rows);
+      most = max(most, max(lo[i], hi[i]));
+    }
+    int upto = most;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, upto, o);
+      if ((int)(threadIdx.x & 31) >= o) upto = max(upto, v);
+    }
+    const int before = __shfl_up_sync(kAll, upto, 1);
+    int from = (threadIdx.x & 31) ? max(reach, before) : reach, sum = 0;
+    reach = max(reach, __shfl_sync(kAll, upto, 31));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = max(lo[i], from);
+      from = hi[i] = max(hi[i], lo[i]);
       sum += tiles(i);
     }
     incl = sum;
@@ -115,7 +143,7 @@ struct Walk {
     gran = gran_;
     tn = tn_;
     if (dense_tiles) return;
-    g0 = base = 0;
+    g0 = base = reach = 0;
     load(0);
     take();
     load(128);
@@ -163,6 +191,7 @@ struct Walk {
       }
       if (!found) r -= n;
     }
+    if (!found) return false;
     const int R = h0 - l0, T = parts(R);
     out.group = g;
     place(r, T, ((R - 1) / T + gran) / gran * gran, l0, h0, out);  // ceil(R / T), up to a multiple of gran

@@ -32,6 +32,7 @@ using namespace tc;
 using namespace lin;
 
 constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kRowWarp = 10, kThreads = 384;
+constexpr long long kLandCycles = 2000 * 1000;
 constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
 
 template <int NT, int CG>
@@ -342,19 +343,22 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
 
   // the part of a tile's tokens that a CTA loads, a multiple of 8
   auto half = [](int rows) { return (rows + 15) / 16 * 16 / CG; };
+  // a warp's tile and its next one, looked for while the first is under way
   Walk walk;
-  Tile t;
+  Tile t, next;
+  bool more = false, more_next = false;
   if (warp < kEpiWarps && a.split > 1) {
     // a split's sums are exchanged below
   } else {
     walk.start(l, a.shift, 16, a.tn, a.tiles, a.width);
+    more = walk.seek(tile0, t);
   }
 
   if (warp == kTmaWarp || (warp == kRowWarp && !l.order)) {
     // two warps, since an instruction takes one about 100 cycles: the weights' copies, the tokens'
     int it = 0, s = 0;
     bool ok = true;
-    for (int i = tile0; ok && walk.seek(i, t); i += step) {
+    for (int i = tile0; ok && more; t = next, more = more_next) {
       // boxes of 32 rows, or all the CTA has room for at once
       const int hx = half(t.rows);
       const bool all = hx > S::kX - 32;
@@ -390,12 +394,17 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         }
         __syncwarp();
         s = s + 1 == ST ? 0 : s + 1;
+        if (ks == k_lo) more_next = walk.seek(i += step, next);
       }
     }
-    // the copies in flight land before the CTA ends, whichever warp may have given up
-    if (pair == 0)
+    // The copies in flight land before the CTA ends, whichever warp may have given up.  A stage that others did not
+    // get to is never full: this wait is a thousand times what a copy takes.
+    if (pair == 0) {
+      const long long t0 = clock64();
       for (int i = it > ST ? it - ST : 0; i < it; ++i)
-        if (!drain_bar(&c.full[i % ST], (i / ST) & 1)) break;
+        while (!mbar_test(&c.full[i % ST], (i / ST) & 1) && clock64() - t0 < kLandCycles) {
+        }
+    }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     if (pair == 0) {
@@ -403,7 +412,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       uint32_t full_par = 0;
       bool ok = true;
       const uint64_t w_base = desc_tile(sa(stg)), x_base = desc_tile(sa(stg) + 128 * 128);
-      for (int i = tile0; ok && walk.seek(i, t); i += step, ++u) {
+      for (int i = tile0; ok && more; t = next, more = more_next, ++u) {
         const int b = u & 1;
         if (u >= 2 && !warp_wait(&c.acc_empty[b], (u / 2 - 1) & 1, &c.abort_flag, a.l.status)) break;
         const uint32_t id = idesc(128 * CG, half(t.rows) * CG);
@@ -436,6 +445,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           }
           __syncwarp();
           if (++s == ST) s = 0, full_par ^= 1;
+          if (k == 0) more_next = walk.seek(i += step, next);
         }
         if (!ok) break;
         if (elect_one()) mma_commit<CG>(&c.acc_full[b], both);
@@ -451,7 +461,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       int s = 0;
       uint32_t par = 0;
       bool ok = true;
-      for (int i = tile0; ok && walk.seek(i, t); i += step)
+      for (int i = tile0; ok && more; more = walk.seek(i += step, t))
         for (int k = 0; ok && k < n_k; ++k) {
           ok = warp_wait(&c.landed[s], par, &c.abort_flag, a.l.status);
           fence_async_smem();
@@ -473,16 +483,19 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       const int gw = warp - kRowWarp, chunk = lane & 7, r0 = 4 * gw + (lane >> 3);
       int it = 0, s = 0;
       bool ok = true;
-      for (int i = tile0; ok && walk.seek(i, t); i += step) {
-        const int hx = half(t.rows);
-        uint32_t row[kPer];  // in 16-byte pieces
+      int order[kPer];  // of the tile's rows, loaded while the one before is copied
+      auto look_up = [&](const Tile& z) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          // past the tile its last row again (one row for all tiles would be one L2 slice's); places
-          // without a row load row 0, and are not stored
-          const int r = min(pair * hx + r0 + 8 * j, t.rows - 1);
-          row[j] = (uint32_t)(max(source_row(l, t.row + r), 0) * (l.x_stride / 8));
-        }
+        for (int j = 0; j < kPer; ++j)
+          // past the tile its last row again (one row for all tiles would be one L2 slice's)
+          order[j] = l.order[z.row + min(pair * half(z.rows) + r0 + 8 * j, z.rows - 1)];
+      };
+      if (more) look_up(t);
+      for (int i = tile0; ok && more; t = next, more = more_next) {
+        const int hx = half(t.rows);
+        uint32_t row[kPer];  // in 16-byte pieces; places without a row load row 0, and are not stored
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) row[j] = (uint32_t)(max(row_of(l, order[j]), 0) * (l.x_stride / 8));
         const uint4* from = reinterpret_cast<const uint4*>(l.x) + (long long)k_lo * S::kSub * 8 + chunk;
         for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
           if (it >= ST && !warp_wait(&c.empty[s], (it / ST - 1) & 1, &c.abort_flag, a.l.status)) {
@@ -502,6 +515,10 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           }
           copies_arrive(&c.landed[s]);
           s = s + 1 == ST ? 0 : s + 1;
+          if (ks == k_lo) {
+            more_next = walk.seek(i += step, next);
+            if (more_next) look_up(next);
+          }
         }
       }
       copies_wait();
@@ -514,7 +531,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     int u = 0;
     const int quarter = warp & 3;
     Epilogue e(l, sa(stg) + ST * S::kStage + warp * 2048, lane);
-    for (int i = tile0; walk.seek(i, t); i += step, ++u) {
+    for (int i = tile0; more; more = walk.seek(i += step, t), ++u) {
       const int b = u & 1;
       e.start(l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter
                       : ((long long)t.n * CG + pair) * 128 + 32 * quarter,
@@ -731,13 +748,14 @@ void consider(const Linear& l, int sms, long long tiles, Cut& best) {
   const int width = (int)((l.rows + tiles - 1) / tiles + 15) / 16 * 16;
   tiles = (l.rows + (long long)width - 1) / width;
   const long long all = tiles * tiles_n(l, CG);
-  const int nk = (int)((l.k + 63ll) / 64);
+  constexpr int kSub = Shape<NT, CG>::kSub;
+  const int nk = (int)((l.k + 64ll * kSub - 1) / (64 * kSub));  // stages: each part of K has one at least
   // a slab of 64 of K: its MMAs, its copies, the issuing warps' time
   const int mmas = 2 * width, copies = (128 * 128 + (width / CG + 31) / 32 * 4096) / 68, issue = CG == 1 ? 250 : 400;
   const int slab = mmas > copies ? (mmas > issue ? mmas : issue) : (copies > issue ? copies : issue);
   for (int split = 1; split <= split_for(all, nk, CG, sms); split *= 2) {
     const long long per = sms / (CG * split), waves = (all + per - 1) / per;
-    const long long cost = waves * ((nk + split - 1) / split) * slab + width * 40 + (split > 1 ? 3000 + 60 * NT : 0);
+    const long long cost = waves * ((nk + split - 1) / split) * kSub * slab + width * 40 + (split > 1 ? 3000 + 60 * NT : 0);
     if (best.nt == 0 || cost < best.cost) best = {NT, CG, (int)tiles, width, split, cost};
   }
 }
