@@ -14,10 +14,30 @@ __device__ __forceinline__ float sigmoid(float z) {
   const float e = expf(-fabsf(z));
   return __fdividef(z < 0.f ? e : 1.f, 1.f + e);
 }
+// z Phi(z) by the upper tail Q(a) = e^(-a^2 / 2) R(a), a = |z|: no cancellation in Phi's lower tail.  R is the
+// smooth scaled tail erfcx(a / sqrt 2) / 2, here t times a polynomial of degree 8 in t = 1 / (1 + 0.35 a), fitted for least
+// relative error over 0 .. 16 (2^-25; 5 2^-24 in fp32 steps); the exponent's rounding a^2 - fl(a^2) is put back.
+// Less than half of normcdff's instructions (28 to 67 cycles a lane).
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fminf(fabsf(z), 16.f);  // Q(16) is below fp32; a NaN comes back with z
+  const float d = fmaf(0.35f, a, 1.f), t0 = __fdividef(1.f, d), t = fmaf(t0, fmaf(-d, t0, 1.f), t0);
+  float r = -0.029164928942918777f;
+  r = fmaf(r, t, 0.1440657675266266f);
+  r = fmaf(r, t, -0.25591233372688293f);
+  r = fmaf(r, t, 0.1594051569700241f);
+  r = fmaf(r, t, -0.023272467777132988f);
+  r = fmaf(r, t, 0.10557854920625687f);
+  r = fmaf(r, t, 0.11981452256441116f);
+  r = fmaf(r, t, 0.1398644745349884f);
+  r = fmaf(r, t, 0.13962124288082123f);
+  const float s = a * a, lost = fmaf(a, a, -s);
+  const float q = r * t * expf(-0.5f * s) * fmaf(-0.5f, lost, 1.f);
+  return z * (z < 0.f ? q : 1.f - q);
+}
 template <int ACT>
 __device__ __forceinline__ float act1(float z) {
   if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid(z);
-  if constexpr (ACT == MOE_ACT_GELU) return z * normcdff(z);
+  if constexpr (ACT == MOE_ACT_GELU) return gelu(z);
   // (1 + tanh u) / 2 is the sigmoid of 2 u, which does not cancel
   if constexpr (ACT == MOE_ACT_GELU_TANH) return z * sigmoid(1.5957691216f * fmaf(0.044715f * z, z * z, z));
   if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;

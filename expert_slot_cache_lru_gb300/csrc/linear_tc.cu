@@ -41,7 +41,8 @@ struct Shape {
   static constexpr int kSub = NT == 256 ? 1 : 2;   // 64-element slabs of K in a stage
   static constexpr int kSlab = 128 * 128 + kX * 128;
   static constexpr int kStage = kSub * kSlab;
-  static constexpr int kTurn = kEpiWarps * 2048;         // the epilogue's
+  static constexpr int W = NT == 32 ? 16 : 32;           // tokens the epilogue takes at a time
+  static constexpr int kTurn = kEpiWarps * W * 128;      // their sums
   static constexpr int kFit = (226 * 1024 - 2048 - kTurn) / kStage;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr int kChains = 256 / NT < 4 ? 256 / NT : 4;
@@ -154,17 +155,19 @@ __device__ __forceinline__ float lds(uint32_t saddr) {
   return v;
 }
 
-// The epilogue of a warp: blocks of 16 tokens, its 32 lanes' sums turned in shared memory so that
+// The epilogue of a warp: blocks of W tokens, its 32 lanes' sums turned in shared memory so that
 // a lane finishes four neighbouring results of a token (1 store of 8 or 16 bytes, and as
 // large a load of the residual, for four scattered ones).  Rows of 32 floats; odd tokens
 // have their halves exchanged, which keeps the reads of 16 gate or up sums off each other's banks.
-// A lane's tokens of a block are `step` apart, an even number, so its places are fixed.
+// A lane's tokens of a block are `step` apart, an even number, so its places are fixed.  Blocks of 32 have half
+// the chain of latencies of 16 (8,192 x 8,192 x 512: 84 us, so T512).
+template <int W>
 struct Epilogue {
   const Linear& l;
   const bool gated, f32;
   const int lane, token, step;  // first of the lane's tokens in a block
   const uint32_t put0, put1;    // shared memory: this lane's sums of even and odd tokens
-  const uint32_t get_a, get_u;  // the four sums of its first token, and their up sums
+  const uint32_t get_a;         // the four sums of its first token; their up sums are 64 bytes on or back
   const long long out_step, res_step, es;  // bytes between the lane's rows, of an element
   // Where the lanes' results are all below n and aligned: four of a token each.  Else one of each token (of
   // every second one if gated), neighbours in neighbouring lanes.
@@ -177,7 +180,7 @@ struct Epilogue {
       : l(l_), gated(l_.gated), f32(l_.f32), lane(lane_), token(l_.gated ? lane_ >> 2 : lane_ >> 3),
         step(l_.gated ? 8 : 4), put0(buf + 4 * lane_), put1(buf + 128 + 4 * (lane_ ^ 16)),
         get_a(buf + token * 128 + 16 * ((l_.gated ? lane_ & 3 : lane_ & 7) ^ (token & 1 ? 4 : 0))),
-        get_u(get_a ^ 64), out_step(step * l_.out_stride * (l_.f32 ? 4 : 2)),
+        out_step(step * l_.out_stride * (l_.f32 ? 4 : 2)),
         res_step(step * l_.res_stride * (l_.f32 ? 4 : 2)), es(l_.f32 ? 4 : 2) {}
 
   // n0: first result of the warp's lanes; row: the tile's first
@@ -196,14 +199,23 @@ struct Epilogue {
       ubias[j] = here && gated ? __bfloat162float(b[l.n + j]) : 0.f;
     }
   }
-  // The residual of the lane's results of the block at token n0; it stays in the bits it was
-  // loaded in until it is used, so that a load ahead is not waited for.
-  __device__ __forceinline__ void fetch(int n0, uint32_t mask, uint32_t (&r)[4][4]) const {
+  // The residual of the warp's blocks from token n0 on into L2, while the sums are made (2,048 x 2,048 x 2,048: 23.9 us,
+  // so 21.7).
+  __device__ __forceinline__ void prefetch(int n0, int rows) const {
+    if (!wide) return;
+    for (; n0 < rows; n0 += 2 * W)
+      for (int t = token; t < W; t += step)
+        if (n0 + t < rows)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(res + (n0 + t - token) * l.res_stride * es));
+  }
+  // The residual of the lane's results of the block at token n0, in the bits it is loaded in until it is used:
+  // nothing waits for it before.
+  __device__ __forceinline__ void fetch(int n0, uint32_t mask, uint32_t (&r)[W / 4][4]) const {
     const char* p = res + n0 * l.res_stride * es;
     if (wide) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if ((k < 2 || !gated) && (mask >> (token + k * step) & 1)) {
+      for (int k = 0; k < W / 4; ++k)
+        if ((k < W / 8 || !gated) && (mask >> (token + k * step) & 1)) {
           const char* q = p + k * res_step;
           if (f32) {
             const uint4 u = *reinterpret_cast<const uint4*>(q);
@@ -216,29 +228,45 @@ struct Epilogue {
     } else {
       const int first = gated ? lane >> 4 : 0, by = gated ? 2 : 1;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i * by < 16 && in && (mask >> (first + i * by) & 1)) {
+      for (int i = 0; i < W; ++i)
+        if (i * by < W && in && (mask >> (first + i * by) & 1)) {
           const char* q = p + i * by * l.res_stride * es;
           r[i / 4][i % 4] = f32 ? *reinterpret_cast<const uint32_t*>(q) : *reinterpret_cast<const uint16_t*>(q);
         }
     }
   }
-  __device__ __forceinline__ void turn(const uint32_t (&v)[16]) const {
+  __device__ __forceinline__ void turn(const uint32_t (&v)[W]) const {
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
+    for (int i = 0; i < W; i += 2) {
       sts(put0 + i * 128, v[i]);
       sts(put1 + i * 128, v[i + 1]);
     }
   }
+  // A block, 16 tokens at a time.
   template <bool GATED, typename A>
-  __device__ __forceinline__ void finish(A act, int n0, uint32_t mask, const uint32_t (&r)[4][4]) const {
-    if (!wide) return finish_narrow<GATED>(act, n0, mask, r);
-    constexpr int M = GATED ? 2 : 4;
+  __device__ __forceinline__ void finish(A act, int n0, uint32_t mask, uint32_t (&r)[W / 4][4]) const {
     char* p = out + n0 * l.out_stride * es;
+#pragma unroll 1
+    for (int half = 0; half < W / 16; ++half) {
+      if (wide) finish_wide<GATED>(act, p, half * 2048, mask, r);
+      else finish_narrow<GATED>(act, p, half * 2048, mask, r);
+      p += 16 * l.out_stride * es;
+      mask >>= 16;
+      if (W > 16 && l.res) {
+#pragma unroll
+        for (int k = 0; k < W / 8; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[k][j] = GATED && k >= W / 16 ? 0 : r[k + (GATED ? W / 16 : W / 8)][j];
+      }
+    }
+  }
+  template <bool GATED, typename A>
+  __device__ __forceinline__ void finish_wide(A act, char* p, int at, uint32_t mask, const uint32_t (&r)[W / 4][4]) const {
+    constexpr int M = GATED ? 2 : 4;
     float y[M][4];
 #pragma unroll
     for (int k = 0; k < M; ++k) {
-      const float4 g = lds4(get_a + k * (GATED ? 1024 : 512));
+      const float4 g = lds4(get_a + at + k * (GATED ? 1024 : 512));
       y[k][0] = g.x, y[k][1] = g.y, y[k][2] = g.z, y[k][3] = g.w;
     }
 #pragma unroll
@@ -248,7 +276,7 @@ struct Epilogue {
     if constexpr (GATED) {
 #pragma unroll
       for (int k = 0; k < M; ++k) {
-        const float4 u = lds4(get_u + k * 1024);
+        const float4 u = lds4((get_a + at + k * 1024) ^ 64);
         y[k][0] *= u.x + ubias[0], y[k][1] *= u.y + ubias[1], y[k][2] *= u.z + ubias[2], y[k][3] *= u.w + ubias[3];
       }
     }
@@ -273,23 +301,28 @@ struct Epilogue {
     }
   }
   template <bool GATED, typename A>
-  __device__ __forceinline__ void finish_narrow(A act, int n0, uint32_t mask, const uint32_t (&r)[4][4]) const {
+  __device__ __forceinline__ void finish_narrow(A act, char* p, int half, uint32_t mask,
+                                                const uint32_t (&r)[W / 4][4]) const {
     constexpr int BY = GATED ? 2 : 1;
     const int first = GATED ? lane >> 4 : 0;
-    char* p = out + n0 * l.out_stride * es;
+    const long long by = BY * l.out_stride * es;
+    uint32_t bit = 1u << first;
+    // sums of token first + BY * i; gated, the up lanes' tokens are odd and turned
+    uint32_t at = half + (GATED ? put0 - 4 * lane + first * 128 + 4 * ((lane & 15) ^ (first ? 16 : 0)) : put0);
+    const uint32_t odd = GATED ? 0 : (4 * lane ^ 64) - 4 * lane;  // of an odd token's place, not gated
 #pragma unroll
-    for (int i = 0; i < 16 / BY; ++i) {
-      // sums of token first + BY * i; gated, the up lanes' tokens are odd and turned
-      const uint32_t at = GATED ? put0 - 4 * lane + (2 * i + first) * 128 + 4 * ((lane & 15) ^ (first ? 16 : 0))
-                                : (i & 1 ? put1 - 128 : put0) + i * 128;
-      float y = act(lds(at) + bias[0]);
-      if (GATED) y *= lds(at ^ 64) + ubias[0];
-      y *= l.alpha;
-      if (l.res) y += __uint_as_float(f32 ? r[i / 4][i % 4] : r[i / 4][i % 4] << 16);
-      if (in && (mask >> (first + BY * i) & 1)) {
-        char* q = p + i * BY * l.out_stride * es;
-        if (f32) *reinterpret_cast<float*>(q) = y;
-        else *reinterpret_cast<__nv_bfloat16*>(q) = __float2bfloat16_rn(y);
+    for (int k = 0; k < 4 / BY; ++k, at += 512 * BY) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j, p += by, bit <<= BY) {
+        const uint32_t here = at + j * 128 * BY + (j & 1 ? odd : 0);
+        float y = act(lds(here) + bias[0]);
+        if (GATED) y *= lds(here ^ 64) + ubias[0];
+        y *= l.alpha;
+        if (l.res) y += __uint_as_float(f32 ? r[k][j] : r[k][j] << 16);
+        if (in && (mask & bit)) {
+          if (f32) *reinterpret_cast<float*>(p) = y;
+          else *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y);
+        }
       }
     }
   }
@@ -300,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
               const __grid_constant__ CUtensorMap xmap_all, const __grid_constant__ Args a) {
   using S = Shape<NT, CG>;
-  constexpr int ST = S::kStages, W = 16;
+  constexpr int ST = S::kStages, W = S::W;
   extern __shared__ uint8_t raw[];
   uint8_t* stg = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ Ctl<ST> c;
@@ -530,21 +563,21 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   } else {
     int u = 0;
     const int quarter = warp & 3;
-    Epilogue e(l, sa(stg) + ST * S::kStage + warp * 2048, lane);
+    Epilogue<W> e(l, sa(stg) + ST * S::kStage + warp * W * 128, lane);
     for (int i = tile0; more; more = walk.seek(i += step, t), ++u) {
       const int b = u & 1;
       e.start(l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter
                       : ((long long)t.n * CG + pair) * 128 + 32 * quarter,
               t.row, t.group, a.wide);
-      auto rows_of = [&](int n0) {  // which of 16 tokens have a row
-        const uint32_t in = n0 + 16 <= t.rows ? 0xffffu : n0 < t.rows ? (1u << (t.rows - n0)) - 1 : 0u;
+      auto rows_of = [&](int n0) {  // which of W tokens have a row
+        const int left = t.rows - n0;
+        const uint32_t in = left >= W ? 0xffffffffu >> (32 - W) : left > 0 ? (1u << left) - 1 : 0u;
         if (!l.order) return in;
         return __ballot_sync(kAll, (in >> lane & 1) && source_row(l, t.row + n0 + lane) >= 0);
       };
-      int n0 = (warp >> 2) * 16;
+      int n0 = (warp >> 2) * W;
       uint32_t mask = rows_of(n0);
-      uint32_t r[4][4], r_next[4][4];
-      if (l.res) e.fetch(n0, mask, r);
+      if (l.res) e.prefetch(n0, t.rows);
       if (threadIdx.x == 0)
         c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], (u / 2) & 1, &c.abort_flag, a.l.status);
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -552,23 +585,20 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + b * S::kChains * NT;
 #pragma unroll 1
-      for (; n0 < t.rows; n0 += 32) {
-        const uint32_t next = rows_of(n0 + 32);
-        if (l.res) e.fetch(n0 + 32, next, r_next);
-        uint32_t v[16];
+      for (; n0 < t.rows; n0 += 2 * W) {
+        uint32_t r[W / 4][4];
+        if (l.res) e.fetch(n0, mask, r);
+        const uint32_t next = rows_of(n0 + 2 * W);
+        uint32_t v[W];
         read_sums<NT>(acc + n0, n_chains, v);
         __syncwarp();
         e.turn(v);
         __syncwarp();
         with_act(l.act, [&](auto act) {
-          if (e.gated) e.finish<true>(act, n0, mask, r);
-          else e.finish<false>(act, n0, mask, r);
+          if (e.gated) e.template finish<true>(act, n0, mask, r);
+          else e.template finish<false>(act, n0, mask, r);
         });
         mask = next;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) r[k][j] = r_next[k][j];
       }
       fence_before();
       __syncwarp();
