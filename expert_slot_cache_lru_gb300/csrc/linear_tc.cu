@@ -104,6 +104,10 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(bar)) : "memory");
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t w, uint64_t x, uint32_t id, uint32_t acc) {
   if constexpr (CG == 1)
@@ -350,20 +354,25 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   const uint16_t both = (uint16_t)(((1 << CG) - 1) << first);
 
   pdl_trigger();
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&c.full[i], l.order ? CG : 1);  // with the second CTA's gathered rows handed on
-      mbar_init(&c.empty[i], 1);
-      mbar_init(&c.landed[i], 64);
-    }
-    for (int i = 0; i < 2; ++i) {
+  if (threadIdx.x < ST) {
+    const int i = threadIdx.x;
+    mbar_init(&c.full[i], l.order ? CG : 1);  // with the second CTA's gathered rows handed on
+    mbar_init(&c.empty[i], 1);
+    mbar_init(&c.landed[i], 64);
+    if (i < 2) {
       mbar_init(&c.acc_full[i], 1);
       mbar_init(&c.acc_empty[i], kEpiWarps * CG);
     }
-    mbar_init(&c.drain, 1);
-    mbar_init(&c.sums, 1);
-    c.abort_flag = 0;
+    if (i == 0) {
+      mbar_init(&c.drain, 1);
+      mbar_init(&c.sums, 1);
+      c.abort_flag = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kTmaWarp && elect_one()) {  // the maps are on their way when the first copy reads them
+    prefetch_map(&wmap);
+    prefetch_map(l.order ? &wmap : &xmap_all);
   }
   if (warp == kMmaWarp) tmem_alloc<CG>(&c.tmem, S::kCols);
   fence_before();
@@ -372,7 +381,6 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   else if (a.split > 1) cluster_arrive();  // waited for before anything goes to a peer
   fence_after();
   const uint32_t tmem = c.tmem;
-  pdl_wait();
 
   // the part of a tile's tokens that a CTA loads, a multiple of 8
   auto half = [](int rows) { return (rows + 15) / 16 * 16 / CG; };
@@ -380,12 +388,12 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   Walk walk;
   Tile t, next;
   bool more = false, more_next = false;
-  if (warp < kEpiWarps && a.split > 1) {
-    // a split's sums are exchanged below
-  } else {
+  if (l.offsets) pdl_wait();
+  if (warp >= kEpiWarps || a.split == 1) {  // a split's sums are exchanged below
     walk.start(l, a.shift, 16, a.tn, a.tiles, a.width);
     more = walk.seek(tile0, t);
   }
+  if (!l.offsets) pdl_wait();
 
   if (warp == kTmaWarp || (warp == kRowWarp && !l.order)) {
     // two warps, since an instruction takes one about 100 cycles: the weights' copies, the tokens'
