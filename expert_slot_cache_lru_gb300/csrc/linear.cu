@@ -3,7 +3,8 @@
 //
 // A few rows are bound by the weights' bytes: a CTA takes a few rows of weights, its warps a slice of K each, 16 bytes
 // a lane and load, all loads of a slice in flight together and x in registers beside them.  Grouped, a place is a
-// row of its own: its group is looked up by the whole block at once.
+// row of its own: its group is looked up by the whole block at once.  Three to 16 rows take the warps' own MMAs, straight
+// from registers: the weights' bytes bound them too, and a tile of the large kernel has its pipeline to fill first.
 //
 // Tiles of 64 rows x 64 results (of both matrices if gated), 4 x 4 results per thread, operands through
 // shared memory as fp32: bound by its FMAs.
@@ -15,13 +16,14 @@ namespace {
 
 using namespace lin;
 
-constexpr int kDotThreads = 128, kDotRows = 4, kDotPlaces = 16;
+constexpr int kDotThreads = 128, kDotRows = 2, kDotPlaces = 16;
+constexpr int kStreamWarps = 16, kStreamRows = 16;
 // Rows of weights of a CTA's part and 256-element pieces of K of a warp, for R rows of x: the best of
-// 4 and 8 and of 1, 2 and 4 at 4,096 x 4,096 (8.1, 7.9 and 10.1 us; with more in flight per thread
-// and fewer threads 9 to 13).
+// 4 and 8 and of 1, 2 and 4 at 4,096 x 4,096 (8.1 and 7.9 us; with more in flight per thread and fewer threads 9
+// to 13).
 template <int R>
 struct Dots {
-  static constexpr int NB = R == 4 ? 8 : 4, U = R == 1 ? 2 : 1;
+  static constexpr int NB = 4, U = R == 1 ? 2 : 1;
 };
 
 template <bool GATED>
@@ -120,7 +122,7 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
   return v[0];
 }
 
-// R rows of x (the last again where there are fewer; grouped: the place blockIdx.y alone).  A CTA takes NB rows of
+// R rows of x (grouped: the place blockIdx.y alone).  A CTA takes NB rows of
 // weights per part of n (of each matrix half as many if gated); `kw` of its warps share a part, each a
 // slice of K at a time, the slices of x in registers.
 template <int R, bool GATED>
@@ -136,14 +138,13 @@ __global__ void __launch_bounds__(kDotThreads) dot_kernel(const Linear l, int kw
   long long row0 = 0;  // of out
   const __nv_bfloat16* x = l.x;
   if (l.offsets) {
-    const int p = blockIdx.y;
+    const int p = blockIdx.y, src = source_row(l, p);  // on its way beside the offsets
     __syncthreads();
     for (int g = threadIdx.x; g < l.groups; g += kDotThreads)
       if (l.offsets[g] <= p && p < l.offsets[g + 1]) found = g;  // one at most where offsets ascend
     __syncthreads();
     group = found;
-    const int src = group < 0 ? -1 : source_row(l, p);
-    if (src < 0) return;
+    if (group < 0 || src < 0) return;
     x += src * l.x_stride;
     row0 = p;
   }
@@ -228,6 +229,108 @@ cudaError_t launch_dots(const Linear& l, cudaStream_t s) {
   return tc::launch_early(dot_kernel<R, false>, grid, block, 0, s, l, kw);
 }
 
+// Sums of a warp's 16 rows of weights and 8 tokens over 16 of K, fp32 += bf16 x bf16.
+__device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Up to 8 TN rows of x (the last again where there are fewer).  A CTA takes 16 rows of weights (8 gate rows and
+// their up rows), its warps 32 of K in turn, from memory to registers in the order of the MMA's operands: which
+// of K an operand's place holds is free as long as it is the same for both, so lane 4 g + t loads 16 bytes of row g,
+// from t * 8 on, and these are its places of two MMAs.
+template <int TN, bool GATED>
+__global__ void __launch_bounds__(kStreamWarps * 32) stream_kernel(const Linear l) {
+  constexpr int U = 4, OUT = GATED ? 8 : 16;  // U: steps of K in flight
+  constexpr int kValues = OUT * 8 * TN, kPer = (kValues + kStreamWarps * 32 - 1) / (kStreamWarps * 32);
+  __shared__ float sums[kStreamWarps][TN][16][9];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  tc::pdl_trigger();
+  tc::pdl_wait();
+  const long long n0 = (long long)blockIdx.x * OUT;
+  const long long ra = n0 + g < l.n ? n0 + g : l.n - 1, rb = GATED ? ra + l.n : n0 + g + 8 < l.n ? n0 + g + 8 : l.n - 1;
+  const uint4* wa = reinterpret_cast<const uint4*>(l.w + ra * l.w_stride) + t;
+  const uint4* wb = reinterpret_cast<const uint4*>(l.w + rb * l.w_stride) + t;
+  const uint4* xr[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) xr[j] = reinterpret_cast<const uint4*>(l.x + min(8 * j + g, l.rows - 1) * l.x_stride) + t;
+  const int pieces = l.k / 8;  // of 16 bytes; a step is four
+  float c[TN][4] = {};
+  auto add = [&](const uint4& a, const uint4& b, const uint4 (&v)[TN]) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      mma_16x8(c[j], a.x, b.x, a.y, b.y, v[j].x, v[j].y);
+      mma_16x8(c[j], a.z, b.z, a.w, b.w, v[j].z, v[j].w);
+    }
+  };
+  constexpr int kStep = 4 * kStreamWarps;
+  int i = 4 * warp;
+  for (; i + kStep * (U - 1) + 4 <= pieces; i += kStep * U) {
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) a[u] = wa[i + kStep * u], b[u] = wb[i + kStep * u];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint4 v[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) v[j] = xr[j][i + kStep * u];
+      add(a[u], b[u], v);
+    }
+  }
+  for (; i < pieces; i += kStep) {
+    uint4 a = make_uint4(0, 0, 0, 0), b = a, v[TN];
+    const bool in = i + t < pieces;
+    if (in) a = wa[i], b = wb[i];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (in) v[j] = xr[j][i];
+    }
+    add(a, b, v);
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    sums[warp][j][g][2 * t] = c[j][0];
+    sums[warp][j][g][2 * t + 1] = c[j][1];
+    sums[warp][j][g + 8][2 * t] = c[j][2];
+    sums[warp][j][g + 8][2 * t + 1] = c[j][3];
+  }
+  __syncthreads();
+  with_act(l.act, [&](auto act) {
+#pragma unroll
+    for (int z = 0; z < kPer; ++z) {
+      const int i = threadIdx.x + z * kStreamWarps * 32, r = i % OUT, token = i / OUT;
+      const long long n = n0 + r;
+      if (i >= kValues || token >= l.rows || n >= l.n) continue;
+      float y = 0.f, up = 0.f;
+#pragma unroll
+      for (int k = 0; k < kStreamWarps; ++k) {
+        y += sums[k][token / 8][r][token % 8];
+        if (GATED) up += sums[k][token / 8][r + 8][token % 8];
+      }
+      if (l.bias) {
+        y += __bfloat162float(l.bias[n]);
+        if (GATED) up += __bfloat162float(l.bias[l.n + n]);
+      }
+      y = act(y);
+      if (GATED) y *= up;
+      finish(l, token, n, y);
+    }
+  });
+}
+
+template <int TN>
+cudaError_t launch_stream(const Linear& l, cudaStream_t s) {
+  const int per = l.gated ? 8 : 16;
+  const dim3 grid((unsigned)((l.n + (long long)per - 1) / per)), block(kStreamWarps * 32);
+  if (l.gated) return tc::launch_early(stream_kernel<TN, true>, grid, block, 0, s, l);
+  return tc::launch_early(stream_kernel<TN, false>, grid, block, 0, s, l);
+}
+
 template <bool GATED>
 cudaError_t launch_tiles(const Linear& l, int sms, cudaStream_t s) {
   const int tn = (int)((l.n + 63ll) / 64);
@@ -248,8 +351,13 @@ cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
   const bool whole = l.k % 8 == 0 && l.x_stride % 8 == 0 && l.w_stride % 8 == 0 && l.group_stride % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
   if (whole && l.offsets && l.rows <= kDotPlaces) return launch_dots<1>(l, s);
-  if (whole && !l.offsets && l.rows <= kDotRows)
-    return l.rows == 1 ? launch_dots<1>(l, s) : l.rows == 2 ? launch_dots<2>(l, s) : launch_dots<4>(l, s);
+  if (whole && !l.offsets && l.rows <= kDotRows) return l.rows == 1 ? launch_dots<1>(l, s) : launch_dots<2>(l, s);
+  // The streaming kernel where its CTAs, one per 16 rows of weights, are at most two an SM and K gives each no more than
+  // a few rounds (4,096 x 4,096: 9.2 us for 4 rows, 9.9 for 16, and 11.2 and 12.2 in the tiles below; 8 x 2 x 512 x 2,048
+  // gated: 4.2 and 6.5); else the tiles (16 x 16,384 x 2,048: 14.1 us, here 19.3; 16 x 1,024 x 8,192: 11.3 and 13.8).
+  const long long blocks = (l.n + (l.gated ? 7ll : 15ll)) / (l.gated ? 8 : 16);
+  if (whole && !l.offsets && l.rows <= kStreamRows && blocks <= 2ll * d.sms && l.k <= 4096)
+    return l.rows <= 8 ? launch_stream<1>(l, s) : launch_stream<2>(l, s);
   // What the tensor-core kernel's copies address: strides below 2^40 bytes, gathered rows in 32 bits of 16-byte
   // pieces; and a tile's K within what its waits allow (512 cycles for 64 of K).
   const long long most = 1ll << 38;

@@ -33,24 +33,40 @@ extern "C" __attribute__((visibility("default"))) int product(
 """
 
 
-@pytest.fixture(scope="module", params=[0, 4000, 12000])
-def impatient(request, tmp_path_factory):
-    d = tmp_path_factory.mktemp("impatient")
-    shim, lib = str(d / "shim.cu"), str(d / "libimpatient.so")
+def build(d, name, *flags):
+    """The tensor-core kernel by itself, whatever rows the library gives it."""
+    shim, lib = str(d / "shim.cu"), str(d / f"lib{name}.so")
     with open(shim, "w") as f:
         f.write(SHIM)
     subprocess.run([os.environ.get("NVCC", "nvcc"), "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17",
-                    "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-shared", "--threads", "0",
-                    f"-DMOE_TC_WAIT_CYCLES={request.param}", "-I", CSRC, shim, os.path.join(CSRC, "linear_tc.cu"),
-                    os.path.join(CSRC, "tc_host.cu"), "-o", lib], check=True)
+                    "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-shared", "--threads", "0", *flags,
+                    "-I", CSRC, shim, os.path.join(CSRC, "linear_tc.cu"), os.path.join(CSRC, "tc_host.cu"), "-o", lib],
+                   check=True)
     lib = C.CDLL(lib)
-    lib.cycles = request.param
     lib.product.argtypes = [C.c_void_p] * 5 + [C.c_int] * 8 + [C.c_void_p] * 2
     return lib
 
 
-def give_up(lib, full, out, run, what):
-    """full: a whole product into out; run: one that may give up."""
+@pytest.fixture(scope="module")
+def patient(tmp_path_factory):
+    return build(tmp_path_factory.mktemp("patient"), "patient")
+
+
+@pytest.fixture(scope="module", params=[0, 4000, 12000])
+def impatient(request, tmp_path_factory):
+    lib = build(tmp_path_factory.mktemp("impatient"), "impatient", f"-DMOE_TC_WAIT_CYCLES={request.param}")
+    lib.cycles = request.param
+    return lib
+
+
+def give_up(lib, patient, out, run, what):
+    """run(library, status): one product into out."""
+    def full():
+        st = torch.zeros(1, dtype=torch.int64, device="cuda")
+        out.fill_(float("nan"))
+        assert run(patient, st) == 0 and st.item() == 0
+        return out
+
     want = full().clone()
     again = full().clone()
     keep = want.isnan()                       # no place of a group
@@ -59,7 +75,7 @@ def give_up(lib, full, out, run, what):
     for _ in range(3):
         out.fill_(float("nan"))
         st = torch.zeros(1, dtype=torch.int64, device="cuda")
-        assert run(st) == 0
+        assert run(lib, st) == 0
         torch.cuda.synchronize()              # the context is as it was
         untouched = out.isnan()
         assert torch.equal(out[~untouched], want[~untouched]) and untouched[keep].all()
@@ -76,26 +92,25 @@ def give_up(lib, full, out, run, what):
 @pytest.mark.parametrize("B,N,K,gated", [(16, 128, 256, 0), (16, 4096, 4096, 0), (30, 512, 2048, 1), (64, 4096, 4096, 0),
                                          (600, 768, 2048, 1), (512, 2048, 2048, 0), (700, 20000, 512, 0),
                                          (2048, 8192, 1024, 0), (3000, 4096, 2048, 1)])
-def test_a_wait_that_runs_out(m, impatient, B, N, K, gated):  # noqa: F811
+def test_a_wait_that_runs_out(impatient, patient, B, N, K, gated):
     g = gen(B, N, K)
     x, w = normal(g, B, K), normal(g, N * (1 + gated), K, std=K ** -0.5)
     out = torch.empty(B, N, device="cuda")
     sms = torch.cuda.get_device_properties(0).multi_processor_count
 
-    def full():
-        out.fill_(float("nan"))
-        m.moe_linear(x, w, None, None, out, B, N, K, gated=gated, dtype=m.MOE_T_F32)
-        return out
+    def run(lib, st):
+        return lib.product(x.data_ptr(), w.data_ptr(), out.data_ptr(), None, None, B, 1, 1, B, N, K, gated, sms,
+                           st.data_ptr(), torch.cuda.current_stream().cuda_stream)
 
-    give_up(impatient, full, out, lambda st: impatient.product(
-        x.data_ptr(), w.data_ptr(), out.data_ptr(), None, None, B, 1, 1, B, N, K, gated, sms, st.data_ptr(),
-        torch.cuda.current_stream().cuda_stream), f"{B} x {N} x {K}")
+    give_up(impatient, patient, out, run, f"{B} x {N} x {K}")
+    y, dy = ref.product(x, w, None, "none", bool(gated), chain(K, True))
+    ref.check(out, y, dy, torch.float32)
 
 
 @pytest.mark.parametrize("E,mean,N,K,gated", [(64, 4, 256, 512, 1), (300, 2, 512, 1024, 0), (16, 300, 512, 1024, 1),
                                               (40, 90, 1000, 2048, 0)])
 @pytest.mark.parametrize("gather", [True, False])
-def test_a_wait_of_the_groups_that_runs_out(m, impatient, E, mean, N, K, gated, gather):  # noqa: F811
+def test_a_wait_of_the_groups_that_runs_out(impatient, patient, E, mean, N, K, gated, gather):
     r = np.random.default_rng([E, mean])
     counts = r.poisson(mean, E)
     placed = int(counts.sum())
@@ -108,14 +123,12 @@ def test_a_wait_of_the_groups_that_runs_out(m, impatient, E, mean, N, K, gated, 
     out = torch.empty(rows, N, device="cuda")
     sms = torch.cuda.get_device_properties(0).multi_processor_count
 
-    def full():
-        out.fill_(float("nan"))
-        m.moe_grouped_linear(x, rows, order, per, offsets, E, w, None, out, rows, N, K, gated=gated, dtype=m.MOE_T_F32)
-        return out
+    def run(lib, st):
+        return lib.product(x.data_ptr(), w.data_ptr(), out.data_ptr(), order.data_ptr() if gather else None,
+                           offsets.data_ptr(), rows, per, E, rows, N, K, gated, sms, st.data_ptr(),
+                           torch.cuda.current_stream().cuda_stream)
 
-    give_up(impatient, full, out, lambda st: impatient.product(
-        x.data_ptr(), w.data_ptr(), out.data_ptr(), order.data_ptr() if gather else None, offsets.data_ptr(), rows, per,
-        E, rows, N, K, gated, sms, st.data_ptr(), torch.cuda.current_stream().cuda_stream), f"{E} groups of {mean}")
+    give_up(impatient, patient, out, run, f"{E} groups of {mean}")
 
 
 @pytest.mark.parametrize("per_row", [1, 3, 7, 8, 1000])
