@@ -215,10 +215,9 @@ __global__ void __launch_bounds__(THREADS, 1) group_kernel(const GroupArgs a) {
 template <typename C, int THREADS, int CTAS, int PER>
 cudaError_t launch_group(const GroupArgs& a, int smem, cudaStream_t s) {
   auto kern = group_kernel<C, THREADS, CTAS, PER>;
-  static tc::Once once;
+  static tc::Once once, wide;
   cudaError_t e = tc::raise_smem(once, kern, 226 * 1024);
-  if (e != cudaSuccess) return e;
-  if (a.ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && CTAS > 8) e = tc::set_once(wide, kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.ctas);

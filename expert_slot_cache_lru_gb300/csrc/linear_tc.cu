@@ -789,11 +789,12 @@ void consider(const Linear& l, int sms, long long tiles, Cut& best) {
   constexpr int kSub = Shape<NT, CG>::kSub;
   const int nk = (int)((l.k + 64ll * kSub - 1) / (64 * kSub));  // stages: each part of K has one at least
   // a slab of 64 of K: its MMAs, its copies, the issuing warps' time
-  const int mmas = 2 * width, copies = (128 * 128 + (width / CG + 31) / 32 * 4096) / 68, issue = CG == 1 ? 250 : 400;
+  const int mmas = 2 * width, copies = (128 * 128 + (width / CG + 31) / 32 * 4096) / 66, issue = kSub == 2 ? 250 : 400;
   const int slab = mmas > copies ? (mmas > issue ? mmas : issue) : (copies > issue ? copies : issue);
+  const int start = CG == 2 && kSub == 2 ? 600 : 0;  // as measured beside the others
   for (int split = 1; split <= split_for(all, nk, CG, sms); split *= 2) {
     const long long per = sms / (CG * split), waves = (all + per - 1) / per;
-    const long long cost = waves * ((nk + split - 1) / split) * kSub * slab + width * 40 + (split > 1 ? 3000 + 60 * NT : 0);
+    const long long cost = waves * ((nk + split - 1) / split) * kSub * slab + width * 40 + start + (split > 1 ? 3000 + 60 * NT : 0);
     if (best.nt == 0 || cost < best.cost) best = {NT, CG, (int)tiles, width, split, cost};
   }
 }
@@ -818,7 +819,9 @@ cudaError_t launch_linear_tc(const Linear& l, int sms, cudaStream_t s) {
   }
   consider<32, 1>(l, sms, cut);
   consider<128, 1>(l, sms, cut);
+  consider<128, 2>(l, sms, cut);
   consider<256, 2>(l, sms, cut);
+  if (cut.nt == 128 && cut.cg == 2) return launch<128, 2>(l, cut, sms, s);
   if (cut.nt == 32) return launch<32, 1>(l, cut, sms, s);
   if (cut.nt == 128) return launch<128, 1>(l, cut, sms, s);
   return launch<256, 2>(l, cut, sms, s);

@@ -347,21 +347,26 @@ cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
-// A kernel's dynamic shared-memory limit, set by its first launch on each device
-// (devices past the 64th set it every time).
+// A kernel's attribute, set by its first launch on each device (devices past the 64th
+// set it every time).
 struct Once {
   std::atomic<unsigned long long> done{0};
 };
 template <typename K>
-cudaError_t raise_smem(Once& once, K kern, int bytes) {
+cudaError_t set_once(Once& once, K kern, cudaFuncAttribute attribute, int value) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (once.done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(kern, attribute, value);
   if (e == cudaSuccess) once.done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+// Its dynamic shared-memory limit.
+template <typename K>
+cudaError_t raise_smem(Once& once, K kern, int bytes) {
+  return set_once(once, kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 }  // namespace tc

@@ -266,6 +266,28 @@ def test_two_streams_at_once(m):  # noqa: F811
     assert all(torch.equal(a.out, b) for a, b in zip(sides, alone))
 
 
+@pytest.mark.parametrize("R,E", [(8, 256), (900, 2000), (9000, 256), (70000, 256), (70000, 16384)])
+def test_order_captured(m, R, E):  # noqa: F811
+    """Every cluster size inside a graph, with ids that change between replays."""
+    ids = torch.empty(R, dtype=torch.int32, device="cuda")
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    order, pos = torch.empty_like(ids), torch.empty_like(ids)
+    graph = torch.cuda.CUDAGraph()
+    ids.fill_(-1)
+    m.moe_group_routes(ids, R, E, off, order, pos)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        m.moe_group_routes(ids, R, E, off, order, pos)
+    for turn in range(3):
+        new = np.random.default_rng([R, turn]).integers(-1, E, R).astype(np.int32)
+        ids.copy_(torch.from_numpy(new))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.group(new, E)
+        for got, w in zip((off, order, pos), want):
+            assert np.array_equal(got.cpu().numpy(), w)
+
+
 def test_captured_on_two_streams(m):  # noqa: F811
     """Two graphs of the same calls, replayed at once."""
     g = gen(7)
