@@ -813,8 +813,10 @@ void consider(const Linear& l, int sms, Cut& best) {
 cudaError_t launch_linear_tc(const Linear& l, int sms, cudaStream_t s) {
   Cut cut{0, 0, 0, 0, 1, 0};
   if (l.offsets) {
-    // rows a group has on average decide; ragged sizes fill either tile as they come
-    if (l.rows / l.groups < 24) return launch<32, 1>(l, cut, sms, s);
+    // The rows a group has on average decide; ragged sizes fill either tile as they come.  256 experts, gate and up of
+    // 512 x 2,048, 32 / 64 / 128 / 256 rows on average: 148 / 166 / 204 / 283 us in tiles of up to 128 tokens, 161 / 175 /
+    // 201 / 254 in tiles of 256 (176 to 830 in lone CTAs' of 32, which tie below 8 rows).
+    if (l.rows / l.groups < 100) return launch<128, 2>(l, cut, sms, s);
     return launch<256, 2>(l, cut, sms, s);
   }
   consider<32, 1>(l, sms, cut);

@@ -91,7 +91,8 @@ def give_up(lib, patient, out, run, what):
 # one CTA a tile, K in two and four parts, tiles of 128, pairs, one and several tiles a CTA
 @pytest.mark.parametrize("B,N,K,gated", [(16, 128, 256, 0), (16, 4096, 4096, 0), (30, 512, 2048, 1), (64, 4096, 4096, 0),
                                          (600, 768, 2048, 1), (512, 2048, 2048, 0), (700, 20000, 512, 0),
-                                         (2048, 8192, 1024, 0), (3000, 4096, 2048, 1)])
+                                         (2048, 8192, 1024, 0), (3000, 4096, 2048, 1),
+                                         (2000, 128, 1024, 0)])
 def test_a_wait_that_runs_out(impatient, patient, B, N, K, gated):
     g = gen(B, N, K)
     x, w = normal(g, B, K), normal(g, N * (1 + gated), K, std=K ** -0.5)
