@@ -132,19 +132,29 @@ __global__ void __launch_bounds__(kDotThreads) dot_kernel(const Linear l, int kw
   __shared__ float sums[kWarps][NB * R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   tc::pdl_trigger();
-  if (threadIdx.x == 0) found = -1;
+  if (threadIdx.x == 0) found = 0;
   tc::pdl_wait();
   int group = 0;
   long long row0 = 0;  // of out
   const __nv_bfloat16* x = l.x;
   if (l.offsets) {
-    const int p = blockIdx.y, src = source_row(l, p);  // on its way beside the offsets
+    // the last group that starts at p or before: as many offsets as are not above p, counted by the block, all loads
+    // in flight
+    const int p = blockIdx.y, src = source_row(l, p);
+    int below = 0;
     __syncthreads();
-    for (int g = threadIdx.x; g < l.groups; g += kDotThreads)
-      if (l.offsets[g] <= p && p < l.offsets[g + 1]) found = g;  // one at most where offsets ascend
+    for (int g0 = threadIdx.x; g0 <= l.groups; g0 += 4 * kDotThreads) {
+      int at[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) at[u] = g0 + u * kDotThreads <= l.groups ? l.offsets[g0 + u * kDotThreads] : 0x7fffffff;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) below += at[u] <= p;
+    }
+    below = __reduce_add_sync(kAll, below);
+    if (lane == 0 && below) atomicAdd(&found, below);
     __syncthreads();
-    group = found;
-    if (group < 0 || src < 0) return;
+    group = found - 1;
+    if (group < 0 || group >= l.groups || src < 0) return;
     x += src * l.x_stride;
     row0 = p;
   }
