@@ -1,13 +1,13 @@
 // linear.cu -- the bf16 products (formulas in moe_cache.h): which kernel takes a
-// call, the dot products of a few rows, and the CUDA-core tiles for operands of any layout.
+// call, the dot products of a few rows, and the tiles for operands of any layout.
 //
 // A few rows are bound by the weights' bytes: a CTA takes a few rows of weights, its warps a slice of K each, 16 bytes
 // a lane and load, all loads of a slice in flight together and x in registers beside them.  Grouped, a place is a
 // row of its own: its group is looked up by the whole block at once.  Three to 16 rows take the warps' own MMAs, straight
 // from registers: the weights' bytes bound them too, and a tile of the large kernel has its pipeline to fill first.
 //
-// Tiles of 64 rows x 64 results (of both matrices if gated), 4 x 4 results per thread, operands through
-// shared memory as fp32: bound by its FMAs.
+// Layouts the large kernel's copies cannot address (rows that are no whole 16-byte pieces, gated widths that are no
+// multiple of 16) take tiles of the warps' MMAs too, bound by loads of two bytes a lane.
 #include "linear.cuh"
 #include "tc.cuh"
 
@@ -16,7 +16,8 @@ namespace {
 
 using namespace lin;
 
-constexpr int kDotThreads = 128, kDotRows = 2, kDotPlaces = 16;
+constexpr int kDotThreads = 128, kDotRows = 2, kDotPlaces = 24;
+constexpr int kDotCtas = 8;  // an SM; bounds the registers to 64 (4,096 x 4,096: 7.4 us, with 77 8.0)
 constexpr int kStreamWarps = 16, kStreamRows = 16;
 // Rows of weights of a CTA's part and 256-element pieces of K of a warp, for R rows of x: the best of
 // 4 and 8 and of 1, 2 and 4 at 4,096 x 4,096 (8.1 and 7.9 us; with more in flight per thread and fewer threads 9
@@ -26,71 +27,102 @@ struct Dots {
   static constexpr int NB = 4, U = R == 1 ? 2 : 1;
 };
 
+// c += a b^T over 16 of K for 16 rows of a and 8 of b (fp32 += bf16 x bf16).  Lane 4 g + t has rows g and g + 8 of a and
+// row g of b, of each the places 2 t, 2 t + 1 and 2 t + 8, 2 t + 9 of K; of c columns 2 t, 2 t + 1.
+__device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Operands of any layout: tiles of 128 rows x 128 rows of weights (gated: 64 results, their gate and up rows in turns of
+// eight, which puts a result's halves into one lane), 32 of K at a time, loaded an element a lane (the next 32 into
+// registers while these are multiplied) and from shared memory into the warps' MMAs, 32 x 64 a warp.
+constexpr int kPitch = 40;  // elements; rows 20 banks apart keep a fragment's 32 words apart
 template <bool GATED>
 __global__ void __launch_bounds__(256) tile_kernel(const Linear l, int tn) {
-  constexpr int M = GATED ? 2 : 1;
-  __shared__ float xs[32][65], ws[M][32][65];
-  __shared__ int src[64];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  __shared__ __align__(16) uint16_t xs[128][kPitch], ws[128][kPitch];
+  __shared__ int src[128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int wm = (warp & 3) * 32, wn = (warp >> 2) * 64;
   tc::pdl_trigger();
   tc::pdl_wait();
   Walk walk;
-  walk.start(l, 6, 1, tn);
+  walk.start(l, 7, 1, tn);
   Tile t;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(l.x);
   for (long long i = blockIdx.x; i < 0x40000000 && walk.seek((int)i, t); i += gridDim.x) {
-    const long long n0 = t.n * 64ll;
-    const __nv_bfloat16* w = l.w + t.group * l.group_stride;
+    const long long n0 = t.n * (GATED ? 64ll : 128ll);
+    const uint16_t* w = reinterpret_cast<const uint16_t*>(l.w) + t.group * l.group_stride;
     __syncthreads();
-    if (threadIdx.x < 64) src[threadIdx.x] = (int)threadIdx.x < t.rows ? source_row(l, t.row + threadIdx.x) : -1;
+    if (threadIdx.x < 128) src[threadIdx.x] = (int)threadIdx.x < t.rows ? source_row(l, t.row + threadIdx.x) : -1;
     __syncthreads();
-    float acc[M][4][4] = {};
-    for (long long k0 = 0; k0 < l.k; k0 += 32) {
-      for (int j = threadIdx.x; j < 64 * 32; j += 256) {
-        const int r = j >> 5, k = j & 31;
-        const bool in = k0 + k < l.k;
-        xs[k][r] = in && src[r] >= 0 ? __bfloat162float(l.x[src[r] * l.x_stride + k0 + k]) : 0.f;
+    uint16_t xv[16], wv[16];
+    auto load = [&](long long k) {  // this lane's k of rows warp, warp + 8, ..
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-          ws[m][k][r] = in && n0 + r < l.n
-                            ? __bfloat162float(w[(m * (long long)l.n + n0 + r) * l.w_stride + k0 + k])
-                            : 0.f;
+      for (int u = 0; u < 16; ++u) {
+        const int r = warp + 8 * u, from = src[r];
+        // gated: rows 16 f .. 16 f + 7 of the tile are gate rows, the next eight their up rows
+        const long long n = n0 + (GATED ? r / 16 * 8 + r % 8 : r);
+        xv[u] = from >= 0 && k < l.k ? x[from * l.x_stride + k] : 0;
+        wv[u] = n < l.n && k < l.k ? w[(n + (GATED && r & 8 ? l.n : 0)) * l.w_stride + k] : 0;
+      }
+    };
+    float acc[2][8][4] = {};
+    load(lane);
+    for (long long k0 = 0; k0 < l.k; k0 += 32) {
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        xs[warp + 8 * u][lane] = xv[u];
+        ws[warp + 8 * u][lane] = wv[u];
       }
       __syncthreads();
-#pragma unroll 8
-      for (int k = 0; k < 32; ++k) {
-        float xv[4];
+      if (k0 + 32 < l.k) load(k0 + 32 + lane);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) xv[a] = xs[k][ty + 16 * a];
+      for (int k = 0; k < 32; k += 16) {
+        uint32_t a[2][4];
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float wv = ws[m][k][tx + 16 * b];
+          for (int q = 0; q < 4; ++q)
+            a[m][q] = *reinterpret_cast<const uint32_t*>(&xs[wm + 16 * m + g + 8 * (q & 1)][k + 2 * t4 + 8 * (q >> 1)]);
 #pragma unroll
-            for (int a = 0; a < 4; ++a) acc[m][a][b] = fmaf(xv[a], wv, acc[m][a][b]);
-          }
+        for (int n = 0; n < 8; ++n) {
+          const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&ws[wn + 8 * n + g][k + 2 * t4]);
+          const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&ws[wn + 8 * n + g][k + 2 * t4 + 8]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) mma_16x8(acc[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b0, b1);
+        }
       }
       __syncthreads();
     }
     with_act(l.act, [&](auto act) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const long long n = n0 + tx + 16 * b;
-        if (n >= l.n) continue;
-        float bias[M] = {};
-        if (l.bias)
+      for (int n = 0; n < 8; n += GATED ? 2 : 1)
 #pragma unroll
-          for (int m = 0; m < M; ++m)
-            bias[m] = __bfloat162float(l.bias[((long long)t.group * M + m) * l.n + n]);
+        for (int e = 0; e < 2; ++e) {
+          const long long at = n0 + (GATED ? wn / 2 + 4 * n : wn + 8 * n) + 2 * t4 + e;
+          if (at >= l.n) continue;
+          float bias = 0.f, ubias = 0.f;
+          if (l.bias) {
+            const __nv_bfloat16* b = l.bias + (long long)t.group * l.n * (GATED ? 2 : 1) + at;
+            bias = __bfloat162float(b[0]);
+            if (GATED) ubias = __bfloat162float(b[l.n]);
+          }
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int r = ty + 16 * a;
-          if (src[r] < 0) continue;
-          float y = act(acc[0][a][b] + bias[0]);
-          if (GATED) y *= acc[M - 1][a][b] + bias[M - 1];
-          finish(l, t.row + r, n, y);
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = wm + 16 * m + g + 8 * h;
+              if (src[r] < 0) continue;
+              float y = act(acc[m][n][2 * h + e] + bias);
+              if (GATED) y *= acc[m][n + (GATED ? 1 : 0)][2 * h + e] + ubias;
+              finish(l, t.row + r, at, y);
+            }
         }
-      }
     });
   }
 }
@@ -126,7 +158,7 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
 // weights per part of n (of each matrix half as many if gated); `kw` of its warps share a part, each a
 // slice of K at a time, the slices of x in registers.
 template <int R, bool GATED>
-__global__ void __launch_bounds__(kDotThreads) dot_kernel(const Linear l, int kw) {
+__global__ void __launch_bounds__(kDotThreads, kDotCtas) dot_kernel(const Linear l, int kw) {
   constexpr int kWarps = kDotThreads / 32, U = Dots<R>::U, NB = Dots<R>::NB, H = GATED ? NB / 2 : NB;  // H results a part
   __shared__ int found;
   __shared__ float sums[kWarps][NB * R];
@@ -227,26 +259,19 @@ __global__ void __launch_bounds__(kDotThreads) dot_kernel(const Linear l, int kw
 }
 
 template <int R>
-cudaError_t launch_dots(const Linear& l, cudaStream_t s) {
+cudaError_t launch_dots(const Linear& l, long long sms, cudaStream_t s) {
   constexpr int kWarps = kDotThreads / 32;
-  // slices of K as there are whole ones; two at most where a CTA has its group to look up first (one token's 8
-  // experts: 9.3 us for 10.5)
+  // Slices of K as there are whole ones; where a CTA has its group to look up first, as long as all CTAs run at once (two
+  // places of 2 x 512 x 2,048: 5.1 us in four slices, 6.5 in two; eight: 9.6 and 8.8).
+  const int H = l.gated ? Dots<R>::NB / 2 : Dots<R>::NB;
+  auto ctas = [&](int k) { return (l.n + (long long)(kWarps / k) * H - 1) / ((kWarps / k) * H) * l.rows; };
   int kw = 1;
-  while (kw < (l.offsets ? 2 : kWarps) && l.k >= 2 * kw * 256 * Dots<R>::U) kw *= 2;
+  while (kw < kWarps && l.k >= 2 * kw * 256 * Dots<R>::U && (!l.offsets || kw < 2 || ctas(2 * kw) <= kDotCtas * sms))
+    kw *= 2;
   const long long per = (long long)(kWarps / kw) * (l.gated ? Dots<R>::NB / 2 : Dots<R>::NB), blocks = (l.n + per - 1) / per;
   const dim3 grid((unsigned)blocks, l.offsets ? l.rows : 1), block(kDotThreads);
   if (l.gated) return tc::launch_early(dot_kernel<R, true>, grid, block, 0, s, l, kw);
   return tc::launch_early(dot_kernel<R, false>, grid, block, 0, s, l, kw);
-}
-
-// Sums of a warp's 16 rows of weights and 8 tokens over 16 of K, fp32 += bf16 x bf16.
-__device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Up to 8 TN rows of x (the last again where there are fewer).  A CTA takes 16 rows of weights (8 gate rows and
@@ -341,10 +366,44 @@ cudaError_t launch_stream(const Linear& l, cudaStream_t s) {
   return tc::launch_early(stream_kernel<TN, false>, grid, block, 0, s, l);
 }
 
+// A few rows of any layout: a warp per result's weights, an element a lane, four rows of x at a time.
+template <bool GATED>
+__global__ void __launch_bounds__(256) any_kernel(const Linear l) {
+  const int lane = threadIdx.x & 31;
+  const long long n = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  tc::pdl_trigger();
+  tc::pdl_wait();
+  if (n >= l.n) return;
+  const __nv_bfloat16 *w = l.w + n * l.w_stride, *up = w + (long long)l.n * l.w_stride;
+  for (int r0 = 0; r0 < l.rows; r0 += 4) {
+    float a[4] = {}, b[4] = {};
+    const __nv_bfloat16* x[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = l.x + min(r0 + r, l.rows - 1) * l.x_stride;
+#pragma unroll 8
+    for (int k = lane; k < l.k; k += 32) {
+      const float wv = __bfloat162float(w[k]), uv = GATED ? __bfloat162float(up[k]) : 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float xv = __bfloat162float(x[r][k]);
+        a[r] = fmaf(wv, xv, a[r]);
+        if (GATED) b[r] = fmaf(uv, xv, b[r]);
+      }
+    }
+    const float sum = lane_sums(a), usum = GATED ? lane_sums(b) : 0.f;  // row lane / 8's
+    if (lane % 8 == 0 && r0 + lane / 8 < l.rows)
+      with_act(l.act, [&](auto act) {
+        float y = act(sum + (l.bias ? __bfloat162float(l.bias[n]) : 0.f));
+        if (GATED) y *= usum + (l.bias ? __bfloat162float(l.bias[l.n + n]) : 0.f);
+        finish(l, r0 + lane / 8, n, y);
+      });
+  }
+}
+
 template <bool GATED>
 cudaError_t launch_tiles(const Linear& l, int sms, cudaStream_t s) {
-  const int tn = (int)((l.n + 63ll) / 64);
-  const long long most = most_tiles(l, 6, tn);
+  const int per = GATED ? 64 : 128, tn = (int)((l.n + (long long)per - 1) / per);
+  const long long most = most_tiles(l, 7, tn);
   if (most > 0x3fffffff) return cudaErrorInvalidValue;
   const long long grid = most < 8ll * sms ? most : 8ll * sms;
   return tc::launch_early(tile_kernel<GATED>, dim3((unsigned)grid), dim3(256), 0, s, l, tn);
@@ -360,8 +419,8 @@ cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool whole = l.k % 8 == 0 && l.x_stride % 8 == 0 && l.w_stride % 8 == 0 && l.group_stride % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
-  if (whole && l.offsets && l.rows <= kDotPlaces) return launch_dots<1>(l, s);
-  if (whole && !l.offsets && l.rows <= kDotRows) return l.rows == 1 ? launch_dots<1>(l, s) : launch_dots<2>(l, s);
+  if (whole && l.offsets && l.rows <= kDotPlaces) return launch_dots<1>(l, d.sms, s);
+  if (whole && !l.offsets && l.rows <= kDotRows) return l.rows == 1 ? launch_dots<1>(l, d.sms, s) : launch_dots<2>(l, d.sms, s);
   // The streaming kernel where its CTAs, one per 16 rows of weights, are at most two an SM and K gives each no more than
   // a few rounds (4,096 x 4,096: 9.2 us for 4 rows, 9.9 for 16, and 11.2 and 12.2 in the tiles below; 8 x 2 x 512 x 2,048
   // gated: 4.2 and 6.5); else the tiles (16 x 16,384 x 2,048: 14.1 us, here 19.3; 16 x 1,024 x 8,192: 11.3 and 13.8).
@@ -374,6 +433,11 @@ cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
   const bool near = l.x_stride < most && l.w_stride < most / (l.gated ? l.n : 1) && l.group_stride < most &&
                     (!l.order || l.x_rows <= (1ll << 35) / l.x_stride) && l.k <= 1 << 26;
   if (whole && near && (!l.gated || l.n % 16 == 0)) return launch_linear_tc(l, d.sms, s);
+  if (!l.offsets && l.rows <= kStreamRows && l.k <= 1 << 30) {
+    const dim3 grid((unsigned)((l.n + 7ll) / 8)), block(256);
+    if (l.gated) return tc::launch_early(any_kernel<true>, grid, block, 0, s, l);
+    return tc::launch_early(any_kernel<false>, grid, block, 0, s, l);
+  }
   return l.gated ? launch_tiles<true>(l, d.sms, s) : launch_tiles<false>(l, d.sms, s);
 }
 
