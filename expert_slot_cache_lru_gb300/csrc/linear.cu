@@ -268,7 +268,7 @@ cudaError_t launch_dots(const Linear& l, long long sms, cudaStream_t s) {
   int kw = 1;
   while (kw < kWarps && l.k >= 2 * kw * 256 * Dots<R>::U && (!l.offsets || kw < 2 || ctas(2 * kw) <= kDotCtas * sms))
     kw *= 2;
-  const long long per = (long long)(kWarps / kw) * (l.gated ? Dots<R>::NB / 2 : Dots<R>::NB), blocks = (l.n + per - 1) / per;
+  const long long per = (long long)(kWarps / kw) * H, blocks = (l.n + per - 1) / per;
   const dim3 grid((unsigned)blocks, l.offsets ? l.rows : 1), block(kDotThreads);
   if (l.gated) return tc::launch_early(dot_kernel<R, true>, grid, block, 0, s, l, kw);
   return tc::launch_early(dot_kernel<R, false>, grid, block, 0, s, l, kw);
@@ -420,7 +420,8 @@ cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
   const bool whole = l.k % 8 == 0 && l.x_stride % 8 == 0 && l.w_stride % 8 == 0 && l.group_stride % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
   if (whole && l.offsets && l.rows <= kDotPlaces) return launch_dots<1>(l, d.sms, s);
-  if (whole && !l.offsets && l.rows <= kDotRows) return l.rows == 1 ? launch_dots<1>(l, d.sms, s) : launch_dots<2>(l, d.sms, s);
+  if (whole && !l.offsets && l.rows <= kDotRows)
+    return l.rows == 1 ? launch_dots<1>(l, d.sms, s) : launch_dots<2>(l, d.sms, s);
   // The streaming kernel where its CTAs, one per 16 rows of weights, are at most two an SM and K gives each no more than
   // a few rounds (4,096 x 4,096: 9.2 us for 4 rows, 9.9 for 16, and 11.2 and 12.2 in the tiles below; 8 x 2 x 512 x 2,048
   // gated: 4.2 and 6.5); else the tiles (16 x 16,384 x 2,048: 14.1 us, here 19.3; 16 x 1,024 x 8,192: 11.3 and 13.8).

@@ -6,16 +6,18 @@
 // ragged group costs what its rows cost, and one tile shape serves groups of any size.
 // A stage of the pipeline is 128 bytes of every row (64 of K, four MMAs).  CTAs (or pairs)
 // are persistent and take tiles in turn; the groups' offsets are read on the device.  Warps:
-//   0..7  epilogue: tensor memory -> bias, activation, gate, residual -> out.  Warp w reads
-//         lanes 32 (w % 4) .. (its results' n), blocks w / 4, w / 4 + 2, .. of the tokens.  Two
-//         accumulators alternate, so the next tile's MMAs run beside it;
-//   8     TMA loads: weights as boxes, tokens as boxes of 32 rows or of all;
+//   0..7  epilogue: tensor memory -> shared memory -> bias, activation, gate, residual -> out.
+//         Warp w takes lanes 32 (w % 4) .. (its results' n), blocks w / 4, w / 4 + 2, .. of the
+//         tokens.  Two accumulators alternate, so the next tile's MMAs run beside it;
+//   8     TMA loads of the weights (tokens: boxes of 32 rows, or of all);
 //   9     MMAs (the first CTA's of a pair);
-//   10,11 tokens by the order's indices, where there is one.
+//   10,11 tokens by the order's indices, where there is one; else their boxes, and half of a gated
+//         tile's weights.
 // Gated products: a CTA's 128 rows are 64 gate rows and their 64 up rows in runs of 16
-// (boxes of 16 gate and 16 up rows), so that lane l and lane l + 16 of a warp hold the two
-// halves of a result: of two tokens the gate lanes finish one, the up lanes the other, after
-// one exchange.
+// (boxes of 16 gate and 16 up rows), so that the two halves of a result are one warp's.
+// What bounds it: 8,192 x 8,192 x 4,096 with bias, tanh GELU and residual 305 us, the tensor pipe busy 92% of
+// the cycles (plain 281 us, 1,957 TFLOP/s); experts' gate and up (256 of 2 x 512 x 2,048, 65,536 gathered
+// rows) 255 to 275 us, 11.4 TB/s from L2 to the SMs; down products (4,096 x 1,024) HBM, 96%.
 // Sums: the tensor cores add with truncation, an error that grows with the chain of additions;
 // where the tensor memory has room the sum is taken in up to four parts of K.
 // Where tiles are few, `split` CTAs (pairs) of a cluster share a tile: each sums its part of K,
@@ -38,7 +40,8 @@ constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
 template <int NT, int CG>
 struct Shape {
   static constexpr int kX = NT / CG;                     // token rows a CTA loads
-  static constexpr int kSub = NT == 256 ? 1 : 2;   // 64-element slabs of K in a stage
+  // 64-element slabs of K in a stage: two where a stage's MMAs would not outlast its issue
+  static constexpr int kSub = NT == 256 ? 1 : 2;
   static constexpr int kSlab = 128 * 128 + kX * 128;
   static constexpr int kStage = kSub * kSlab;
   static constexpr int W = NT == 32 ? 16 : 32;           // tokens the epilogue takes at a time
@@ -164,7 +167,7 @@ __device__ __forceinline__ float lds(uint32_t saddr) {
 // large a load of the residual, for four scattered ones).  Rows of 32 floats; odd tokens
 // have their halves exchanged, which keeps the reads of 16 gate or up sums off each other's banks.
 // A lane's tokens of a block are `step` apart, an even number, so its places are fixed.  Blocks of 32 have half
-// the chain of latencies of 16 (8,192 x 8,192 x 512: 84 us, so T512).
+// the chain of latencies of 16 (8,192 x 8,192 x 512: 84 us, so 72).
 template <int W>
 struct Epilogue {
   const Linear& l;
@@ -265,7 +268,8 @@ struct Epilogue {
     }
   }
   template <bool GATED, typename A>
-  __device__ __forceinline__ void finish_wide(A act, char* p, int at, uint32_t mask, const uint32_t (&r)[W / 4][4]) const {
+  __device__ __forceinline__ void finish_wide(A act, char* p, int at, uint32_t mask,
+                                              const uint32_t (&r)[W / 4][4]) const {
     constexpr int M = GATED ? 2 : 4;
     float y[M][4];
 #pragma unroll
@@ -395,8 +399,10 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   }
   if (!l.offsets) pdl_wait();
 
-  if (warp == kTmaWarp || (warp == kRowWarp && !l.order)) {
-    // two warps, since an instruction takes one about 100 cycles: the weights' copies, the tokens'
+  if (warp == kTmaWarp || (warp >= kRowWarp && !l.order && (warp == kRowWarp || l.gated))) {
+    // Two or three warps, since an instruction takes one about 100 cycles: the weights' copies, the tokens', and half of
+    // a gated tile's weights.
+    const int j_lo = warp == kTmaWarp ? 0 : 2, j_hi = warp == kTmaWarp && !l.order ? 2 : 4;
     int it = 0, s = 0;
     bool ok = true;
     for (int i = tile0; ok && more; t = next, more = more_next) {
@@ -419,10 +425,9 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           for (int q = 0; q < S::kSub; ++q) {
             uint8_t* p = stg + (size_t)s * S::kStage + q * S::kSlab;
             const int x = (ks * S::kSub + q) * 64;
-            if (warp == kTmaWarp) {
+            if (warp != kRowWarp) {
               if (l.gated) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) load_gated<CG>(p + j * 4096, &wmap, x, nt * 4 + j, t.group, bar);
+                for (int j = j_lo; j < j_hi; ++j) load_gated<CG>(p + j * 4096, &wmap, x, nt * 4 + j, t.group, bar);
               } else {
                 load_rows<CG>(p, &wmap, x, nt * 128, t.group, bar);
               }
@@ -751,10 +756,12 @@ cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
     return (reinterpret_cast<uintptr_t>(p) & (l.f32 ? 15 : 7)) == 0 && stride % 4 == 0;
   };
   a.wide = whole(l.out, l.out_stride) && whole(l.res, l.res ? l.res_stride : 0);
-  CUtensorMap wm, xm, xa;
+  CUtensorMap wm, xm{}, xa{};
   e = make_weight_map(&wm, l.w, l.gated, l.k, l.n, l.w_stride * 2, l.groups, l.group_stride * 2);
-  if (e == cudaSuccess) e = make_map(&xm, l.x, 2, l.k, l.x_rows, l.x_stride * 2, 32);
-  if (e == cudaSuccess) e = make_map(&xa, l.x, 2, l.k, l.x_rows, l.x_stride * 2, S::kX);
+  if (!l.order) {  // gathered rows need no maps
+    if (e == cudaSuccess) e = make_map(&xm, l.x, 2, l.k, l.x_rows, l.x_stride * 2, 32);
+    if (e == cudaSuccess) e = make_map(&xa, l.x, 2, l.k, l.x_rows, l.x_stride * 2, S::kX);
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const long long teams = most < sms / team ? most : sms / team;
@@ -794,7 +801,8 @@ void consider(const Linear& l, int sms, long long tiles, Cut& best) {
   const int start = CG == 2 && kSub == 2 ? 600 : 0;  // as measured beside the others
   for (int split = 1; split <= split_for(all, nk, CG, sms); split *= 2) {
     const long long per = sms / (CG * split), waves = (all + per - 1) / per;
-    const long long cost = waves * ((nk + split - 1) / split) * kSub * slab + width * 40 + start + (split > 1 ? 3000 + 60 * NT : 0);
+    const long long cost = waves * ((nk + split - 1) / split) * kSub * slab + width * 40 + start +
+                           (split > 1 ? 3000 + 60 * NT : 0);
     if (best.nt == 0 || cost < best.cost) best = {NT, CG, (int)tiles, width, split, cost};
   }
 }
