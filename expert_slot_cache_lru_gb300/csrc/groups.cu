@@ -281,19 +281,16 @@ __device__ __forceinline__ void store_v(__nv_bfloat16* p, const float (&v)[V]) {
 }
 
 // Y, O: types of y and of add and out; V elements per thread.  A CTA takes `rows_per` rows at a time, or 256 of
-// `pieces` pieces of one row; a thread has IT such items at once and U routes of each, all loaded before
-// any is used, and loads the next ones' places and weights while it waits.
-template <typename Y, typename O, int V, int U, int IT>
+// `pieces` pieces of one row; a thread loads U routes of its piece before it uses any, and the next piece's places and
+// weights while it waits.
+template <typename Y, typename O, int V, int U>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int pieces, int rows_per, int chunks) {
   tc::pdl_trigger();
   tc::pdl_wait();
   const int sub = rows_per > 1 ? threadIdx.x / pieces : 0, c0 = threadIdx.x - sub * pieces;
-  const unsigned items = (unsigned)((a.rows + rows_per - 1ll) / rows_per * chunks), step = gridDim.x * IT;
-  int p[IT][U], p_next[IT][U];
-  float f[IT][U], f_next[IT][U];
+  const unsigned items = (unsigned)((a.rows + rows_per - 1ll) / rows_per * chunks);
   struct At {
-    long long b;
-    long long c;
+    long long b, c;
     bool in;
   };
   auto at = [&](unsigned i) {
@@ -302,6 +299,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int p
     const long long b = (long long)g * rows_per + sub;
     return At{b, (long long)piece * V, i < items && sub < rows_per && piece < pieces && b < a.rows};
   };
+  int p[U], p_next[U];
+  float f[U], f_next[U];
   auto places = [&](const At& x, int j0, int (&to)[U], float (&weight)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -310,77 +309,68 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a, int p
       weight[u] = in ? a.w[x.b * a.k + j0 + u] : 0.f;
     }
   };
-  unsigned i = blockIdx.x * IT;
-#pragma unroll
-  for (int t = 0; t < IT; ++t) places(at(i + t), 0, p[t], f[t]);
-  for (; i < items; i += step) {
-    At x[IT];
-    float acc[IT][V] = {};
-#pragma unroll
-    for (int t = 0; t < IT; ++t) x[t] = at(i + t);
+  unsigned i = blockIdx.x;
+  places(at(i), 0, p, f);
+  for (; i < items; i += gridDim.x) {
+    const At x = at(i);
+    float acc[V] = {};
     for (int j0 = 0; j0 < a.k; j0 += U) {
-      Raw<Y, V> v[IT][U];
-      Raw<O, V> r[IT];
+      Raw<Y, V> v[U];
+      Raw<O, V> r;
 #pragma unroll
-      for (int t = 0; t < IT; ++t) {
+      for (int u = 0; u < U; ++u)
+        if ((unsigned)p[u] < (unsigned)a.y_rows) v[u].load(static_cast<const Y*>(a.y) + p[u] * a.y_stride + x.c);
+      const bool add = j0 == 0 && a.add && x.in;
+      if (add) r.load(static_cast<const O*>(a.add) + x.b * a.add_stride + x.c);
+      if (j0 + U < a.k) places(x, j0 + U, p_next, f_next);
+      else places(at(i + gridDim.x), 0, p_next, f_next);
+      if (add)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if ((unsigned)p[t][u] < (unsigned)a.y_rows)
-            v[t][u].load(static_cast<const Y*>(a.y) + p[t][u] * a.y_stride + x[t].c);
-        if (j0 == 0 && a.add && x[t].in) r[t].load(static_cast<const O*>(a.add) + x[t].b * a.add_stride + x[t].c);
-      }
+        for (int e = 0; e < V; ++e) acc[e] = r.at(e);
 #pragma unroll
-      for (int t = 0; t < IT; ++t) {
-        if (j0 + U < a.k) places(x[t], j0 + U, p_next[t], f_next[t]);
-        else places(at(i + step + t), 0, p_next[t], f_next[t]);
-      }
+      for (int u = 0; u < U; ++u) {
+        if ((unsigned)p[u] < (unsigned)a.y_rows)
 #pragma unroll
-      for (int t = 0; t < IT; ++t) {
-        if (j0 == 0 && a.add && x[t].in)
-#pragma unroll
-          for (int e = 0; e < V; ++e) acc[t][e] = r[t].at(e);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if ((unsigned)p[t][u] < (unsigned)a.y_rows)
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[t][e] = fmaf(f[t][u], v[t][u].at(e), acc[t][e]);
-          p[t][u] = p_next[t][u], f[t][u] = f_next[t][u];
-        }
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(f[u], v[u].at(e), acc[e]);
+        p[u] = p_next[u], f[u] = f_next[u];
       }
     }
-#pragma unroll
-    for (int t = 0; t < IT; ++t)
-      if (x[t].in) store_v<V>(static_cast<O*>(a.out) + x[t].b * a.out_stride + x[t].c, acc[t]);
+    if (x.in) store_v<V>(static_cast<O*>(a.out) + x.b * a.out_stride + x.c, acc);
   }
 }
 
-template <typename Y, typename O, int V, int U, int IT>
+template <typename Y, typename O, int V, int U>
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s) {
   tc::DeviceInfo d;
-  const cudaError_t e = tc::device_info(&d);
+  cudaError_t e = tc::device_info(&d);
   if (e != cudaSuccess) return e;
-  const int pieces = a.hidden / V, rows_per = pieces < 256 ? 256 / pieces : 1, chunks = (pieces + 255) / 256;
+  const int pieces = a.hidden / V, rows_per = pieces < 256 ? 256 / pieces : 1, chunks = (int)((pieces + 255ll) / 256);
   const long long items = (a.rows + rows_per - 1ll) / rows_per * chunks;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
-  // two CTAs an SM fill it with 16-byte loads (3 to 12: up to 4 us more of 57 for 8,192 x 8 x 2,048); single elements want
-  // more threads
-  const long long blocks = (items + IT - 1) / IT, most = (V == 1 ? 8ll : 2ll) * d.sms;
-  return tc::launch_early(combine_kernel<Y, O, V, U, IT>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
-                          s, a, pieces, rows_per, chunks);
+  // as many CTAs as run at once (8,192 x 2 x 4,096 of two items a thread: 44 us with the three an SM that fit, 54 with
+  // two, 55 with four; one item a thread is a little better: 43)
+  static std::atomic<int> fit{0};
+  int per_sm = fit.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, combine_kernel<Y, O, V, U>, 256, 0);
+    if (e != cudaSuccess) return e;
+    fit.store(per_sm, std::memory_order_relaxed);
+  }
+  const long long most = (long long)per_sm * d.sms;
+  return tc::launch_early(combine_kernel<Y, O, V, U>, dim3((unsigned)(items < most ? items : most)), dim3(256), 0, s, a,
+                          pieces, rows_per, chunks);
 }
 template <typename Y, typename O>
 cudaError_t combine(const CombineArgs& a, cudaStream_t s) {
   auto whole = [](const void* p, long long stride, size_t e) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * e % 16 == 0;
   };
-  constexpr int N = sizeof(Y) == 4 ? 4 : 8;  // loads of a thread in flight
   if (a.hidden % 8 == 0 && whole(a.y, a.y_stride, sizeof(Y)) &&
       whole(a.add, a.add ? a.add_stride : 0, sizeof(O)) && whole(a.out, a.out_stride, sizeof(O))) {
-    if (a.k <= 2) return launch_combine<Y, O, 8, 2, N / 2>(a, s);
-    if (a.k <= 4) return launch_combine<Y, O, 8, 4, N / 4>(a, s);
-    return launch_combine<Y, O, 8, N, 1>(a, s);
+    if (a.k <= 2) return launch_combine<Y, O, 8, 2>(a, s);
+    return launch_combine<Y, O, 8, 4>(a, s);  // of 8 routes too: 53.2 us for 8,192 x 8 x 2,048, eight at once 55.7
   }
-  return launch_combine<Y, O, 1, 8, 1>(a, s);
+  return launch_combine<Y, O, 1, 8>(a, s);
 }
 
 }  // namespace

@@ -16,7 +16,7 @@ namespace {
 
 using namespace lin;
 
-constexpr int kDotThreads = 128, kDotRows = 2, kDotPlaces = 24;
+constexpr int kDotThreads = 128, kDotRows = 2;
 constexpr int kDotCtas = 8;  // an SM; bounds the registers to 64 (4,096 x 4,096: 7.4 us, with 77 8.0)
 constexpr int kStreamWarps = 16, kStreamRows = 16;
 // Rows of weights of a CTA's part and 256-element pieces of K of a warp, for R rows of x: the best of
@@ -419,7 +419,10 @@ cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool whole = l.k % 8 == 0 && l.x_stride % 8 == 0 && l.w_stride % 8 == 0 && l.group_stride % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
-  if (whole && l.offsets && l.rows <= kDotPlaces) return launch_dots<1>(l, d.sms, s);
+  // Places one by one while they are few, or most have a group to themselves (24 / 48 places over 256 experts of
+  // 2 x 512 x 2,048: 19.6 / 34.2 us, in tiles 23.8 / 35.8; 48 over 64 of 2 x 1,024 x 4,096: 96 and 87).
+  const bool few = l.rows <= 16 || (l.rows <= 48 && 4 * l.rows <= l.groups);
+  if (whole && l.offsets && few) return launch_dots<1>(l, d.sms, s);
   if (whole && !l.offsets && l.rows <= kDotRows)
     return l.rows == 1 ? launch_dots<1>(l, d.sms, s) : launch_dots<2>(l, d.sms, s);
   // The streaming kernel where its CTAs, one per 16 rows of weights, are at most two an SM and K gives each no more than
