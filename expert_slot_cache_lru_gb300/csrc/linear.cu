@@ -157,9 +157,9 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
 // R rows of x (grouped: the place blockIdx.y alone).  A CTA takes NB rows of
 // weights per part of n (of each matrix half as many if gated); `kw` of its warps share a part, each a
 // slice of K at a time, the slices of x in registers.
-template <int R, bool GATED>
-__global__ void __launch_bounds__(kDotThreads, kDotCtas) dot_kernel(const Linear l, int kw) {
-  constexpr int kWarps = kDotThreads / 32, U = Dots<R>::U, NB = Dots<R>::NB, H = GATED ? NB / 2 : NB;  // H results a part
+template <int R, bool GATED, int THREADS>
+__global__ void __launch_bounds__(THREADS, kDotCtas * kDotThreads / THREADS) dot_kernel(const Linear l, int kw) {
+  constexpr int kWarps = THREADS / 32, U = Dots<R>::U, NB = Dots<R>::NB, H = GATED ? NB / 2 : NB;  // H results a part
   __shared__ int found;
   __shared__ float sums[kWarps][NB * R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -175,10 +175,10 @@ __global__ void __launch_bounds__(kDotThreads, kDotCtas) dot_kernel(const Linear
     const int p = blockIdx.y, src = source_row(l, p);
     int below = 0;
     __syncthreads();
-    for (int g0 = threadIdx.x; g0 <= l.groups; g0 += 4 * kDotThreads) {
+    for (int g0 = threadIdx.x; g0 <= l.groups; g0 += 4 * THREADS) {
       int at[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) at[u] = g0 + u * kDotThreads <= l.groups ? l.offsets[g0 + u * kDotThreads] : 0x7fffffff;
+      for (int u = 0; u < 4; ++u) at[u] = g0 + u * THREADS <= l.groups ? l.offsets[g0 + u * THREADS] : 0x7fffffff;
 #pragma unroll
       for (int u = 0; u < 4; ++u) below += at[u] <= p;
     }
@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(kDotThreads, kDotCtas) dot_kernel(const Linear
   });
 }
 
-template <int R>
+template <int R, int THREADS>
 cudaError_t launch_dots(const Linear& l, long long sms, cudaStream_t s) {
-  constexpr int kWarps = kDotThreads / 32;
+  constexpr int kWarps = THREADS / 32;
   // Slices of K as there are whole ones; where a CTA has its group to look up first, as long as all CTAs run at once (two
   // places of 2 x 512 x 2,048: 5.1 us in four slices, 6.5 in two; eight: 9.6 and 8.8).
   const int H = l.gated ? Dots<R>::NB / 2 : Dots<R>::NB;
@@ -269,9 +269,15 @@ cudaError_t launch_dots(const Linear& l, long long sms, cudaStream_t s) {
   while (kw < kWarps && l.k >= 2 * kw * 256 * Dots<R>::U && (!l.offsets || kw < 2 || ctas(2 * kw) <= kDotCtas * sms))
     kw *= 2;
   const long long per = (long long)(kWarps / kw) * H, blocks = (l.n + per - 1) / per;
-  const dim3 grid((unsigned)blocks, l.offsets ? l.rows : 1), block(kDotThreads);
-  if (l.gated) return tc::launch_early(dot_kernel<R, true>, grid, block, 0, s, l, kw);
-  return tc::launch_early(dot_kernel<R, false>, grid, block, 0, s, l, kw);
+  const dim3 grid((unsigned)blocks, l.offsets ? l.rows : 1), block(THREADS);
+  if (l.gated) return tc::launch_early(dot_kernel<R, true, THREADS>, grid, block, 0, s, l, kw);
+  return tc::launch_early(dot_kernel<R, false, THREADS>, grid, block, 0, s, l, kw);
+}
+// Four times the warps, and slices of K, where few results have long sums (1,024 x 8,192: 5.1 us for 8.2).
+template <int R>
+cudaError_t launch_dots(const Linear& l, long long sms, cudaStream_t s) {
+  const bool thin = !l.offsets && l.k >= 4096 && l.n <= 2 * sms * (l.gated ? Dots<R>::NB / 2 : Dots<R>::NB);
+  return thin ? launch_dots<R, 4 * kDotThreads>(l, sms, s) : launch_dots<R, kDotThreads>(l, sms, s);
 }
 
 // Up to 8 TN rows of x (the last again where there are fewer).  A CTA takes 16 rows of weights (8 gate rows and
