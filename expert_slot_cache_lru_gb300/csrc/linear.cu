@@ -18,7 +18,7 @@ using namespace lin;
 
 constexpr int kDotThreads = 128, kDotRows = 2;
 constexpr int kDotCtas = 8;  // an SM; bounds the registers to 64 (4,096 x 4,096: 7.4 us, with 77 8.0)
-constexpr int kStreamWarps = 16, kStreamRows = 16;
+constexpr int kStreamRows = 16;
 // Rows of weights of a CTA's part and 256-element pieces of K of a warp, for R rows of x: the best of
 // 4 and 8 and of 1, 2 and 4 at 4,096 x 4,096 (8.1 and 7.9 us; with more in flight per thread and fewer threads 9
 // to 13).
@@ -284,11 +284,11 @@ cudaError_t launch_dots(const Linear& l, long long sms, cudaStream_t s) {
 // their up rows), its warps 32 of K in turn, from memory to registers in the order of the MMA's operands: which
 // of K an operand's place holds is free as long as it is the same for both, so lane 4 g + t loads 16 bytes of row g,
 // from t * 8 on, and these are its places of two MMAs.
-template <int TN, bool GATED>
-__global__ void __launch_bounds__(kStreamWarps * 32) stream_kernel(const Linear l) {
+template <int TN, bool GATED, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) stream_kernel(const Linear l) {
   constexpr int U = 4, OUT = GATED ? 8 : 16;  // U: steps of K in flight
-  constexpr int kValues = OUT * 8 * TN, kPer = (kValues + kStreamWarps * 32 - 1) / (kStreamWarps * 32);
-  __shared__ float sums[kStreamWarps][TN][16][9];
+  constexpr int kValues = OUT * 8 * TN, kPer = (kValues + WARPS * 32 - 1) / (WARPS * 32);
+  __shared__ float sums[WARPS][TN][16][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   tc::pdl_trigger();
   tc::pdl_wait();
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32) stream_kernel(const Linear 
       mma_16x8(c[j], a.z, b.z, a.w, b.w, v[j].z, v[j].w);
     }
   };
-  constexpr int kStep = 4 * kStreamWarps;
+  constexpr int kStep = 4 * WARPS;
   int i = 4 * warp;
   for (; i + kStep * (U - 1) + 4 <= pieces; i += kStep * U) {
     uint4 a[U], b[U];
@@ -344,12 +344,12 @@ __global__ void __launch_bounds__(kStreamWarps * 32) stream_kernel(const Linear 
   with_act(l.act, [&](auto act) {
 #pragma unroll
     for (int z = 0; z < kPer; ++z) {
-      const int i = threadIdx.x + z * kStreamWarps * 32, r = i % OUT, token = i / OUT;
+      const int i = threadIdx.x + z * WARPS * 32, r = i % OUT, token = i / OUT;
       const long long n = n0 + r;
       if (i >= kValues || token >= l.rows || n >= l.n) continue;
       float y = 0.f, up = 0.f;
 #pragma unroll
-      for (int k = 0; k < kStreamWarps; ++k) {
+      for (int k = 0; k < WARPS; ++k) {
         y += sums[k][token / 8][r][token % 8];
         if (GATED) up += sums[k][token / 8][r + 8][token % 8];
       }
@@ -365,11 +365,12 @@ __global__ void __launch_bounds__(kStreamWarps * 32) stream_kernel(const Linear 
 }
 
 template <int TN>
-cudaError_t launch_stream(const Linear& l, cudaStream_t s) {
+cudaError_t launch_stream(const Linear& l, bool thin, cudaStream_t s) {
   const int per = l.gated ? 8 : 16;
-  const dim3 grid((unsigned)((l.n + (long long)per - 1) / per)), block(kStreamWarps * 32);
-  if (l.gated) return tc::launch_early(stream_kernel<TN, true>, grid, block, 0, s, l);
-  return tc::launch_early(stream_kernel<TN, false>, grid, block, 0, s, l);
+  const dim3 grid((unsigned)((l.n + (long long)per - 1) / per));
+  auto go = [&](auto kern, int warps) { return tc::launch_early(kern, grid, dim3(warps * 32), 0, s, l); };
+  if (thin) return l.gated ? go(stream_kernel<TN, true, 32>, 32) : go(stream_kernel<TN, false, 32>, 32);
+  return l.gated ? go(stream_kernel<TN, true, 16>, 16) : go(stream_kernel<TN, false, 16>, 16);
 }
 
 // A few rows of any layout: a warp per result's weights, an element a lane, four rows of x at a time.
@@ -433,10 +434,12 @@ cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
     return l.rows == 1 ? launch_dots<1>(l, d.sms, s) : launch_dots<2>(l, d.sms, s);
   // The streaming kernel where its CTAs, one per 16 rows of weights, are at most two an SM and K gives each no more than
   // a few rounds (4,096 x 4,096: 9.2 us for 4 rows, 9.9 for 16, and 11.2 and 12.2 in the tiles below; 8 x 2 x 512 x 2,048
-  // gated: 4.2 and 6.5); else the tiles (16 x 16,384 x 2,048: 14.1 us, here 19.3; 16 x 1,024 x 8,192: 11.3 and 13.8).
+  // gated: 4.2 and 6.5), twice the warps where they are at most one and K is long (8 x 1,024 x 8,192: 8.1 us, in the tiles
+  // 11); else the tiles (16 x 16,384 x 2,048: 14.1 us, here 19.3).
   const long long blocks = (l.n + (l.gated ? 7ll : 15ll)) / (l.gated ? 8 : 16);
-  if (whole && !l.offsets && l.rows <= kStreamRows && blocks <= 2ll * d.sms && l.k <= 4096)
-    return l.rows <= 8 ? launch_stream<1>(l, s) : launch_stream<2>(l, s);
+  const bool thin = blocks <= d.sms && l.k >= 4096;
+  if (whole && !l.offsets && l.rows <= kStreamRows && (thin ? l.k <= 8192 : blocks <= 2ll * d.sms && l.k <= 4096))
+    return l.rows <= 8 ? launch_stream<1>(l, thin, s) : launch_stream<2>(l, thin, s);
   // What the tensor-core kernel's copies address: strides below 2^40 bytes, gathered rows in 32 bits of 16-byte
   // pieces; and a tile's K within what its waits allow (512 cycles for 64 of K).
   const long long most = 1ll << 38;
