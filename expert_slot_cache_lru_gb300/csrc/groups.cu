@@ -4,8 +4,8 @@
 // The order is a stable counting sort in one launch of one cluster.  Every counting warp
 // takes a run of consecutive routes: it counts them by expert in its own counters in
 // shared memory (lanes with the same expert find one another by a ballot per bit of the id, the first
-// adds for all, so no order of atomics matters; __match_any_sync took three times as long where
-// the experts differ); prefixes over the warps, the cluster's CTAs (each CTA a slice of the
+// adds for all, so no order of atomics matters; 65,536 routes of 256 experts 16.9 us, by
+// __match_any_sync 21.5); prefixes over the warps, the cluster's CTAs (each CTA a slice of the
 // experts) and the experts turn the counts into each warp's first places; and a second pass
 // over the routes hands the places out.
 //
