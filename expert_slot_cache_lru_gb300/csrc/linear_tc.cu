@@ -19,7 +19,8 @@
 // the cycles (plain 281 us, 1,957 TFLOP/s); experts' gate and up (256 of 2 x 512 x 2,048, 65,536 gathered
 // rows) 255 to 275 us, 11.4 TB/s from L2 to the SMs; down products (4,096 x 1,024) HBM, 96%.
 // Sums: the tensor cores add with truncation, an error that grows with the chain of additions;
-// where the tensor memory has room the sum is taken in up to four parts of K.
+// the sum is taken in as many parts of K, up to four, as leave room for two accumulators.  bf16 results hide what
+// is left; fp32 results of long sums take more parts (kLongSum).
 // Where tiles are few, `split` CTAs (pairs) of a cluster share a tile: each sums its part of K,
 // then its share of the rows over the parts in ascending order.
 // Every wait is bounded; on a timeout the CTA reports it, drains its copies and MMAs, frees
@@ -35,6 +36,11 @@ using namespace lin;
 
 constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kRowWarp = 10, kThreads = 384;
 constexpr long long kLandCycles = 2000 * 1000;
+// fp32 results: K of a part beyond which one accumulator takes the place of both, in twice the parts, and of a sum
+// beyond which no tile has 256 tokens.  Off by, relative to the norm of the sums, at K 1,024 / 2,048 / 4,096:
+// 4.7e-7 / 4.7e-7 / 1.0e-6, without this 1.0e-6 / 2.1e-6 / 4.4e-6 (a plain fp32 form 2.5e-7 / 3.9e-7 / 6.1e-7).
+// 65,536 rows of 256 groups, N 1,024: 158 / 322 us at K 1,024 / 2,048, without 150 / 254; 8,192 x 8,192 x 4,096 380, without 294.
+constexpr int kLongSum = 640;
 constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
 
 template <int NT, int CG>
@@ -353,7 +359,9 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   const int pair = crank % CG, first = crank - pair, part = crank / CG;
   const int team = CG * a.split;
   const int k_lo = (int)((long long)a.nk * part / a.split), k_hi = (int)((long long)a.nk * (part + 1) / a.split);
-  const int n_k = k_hi - k_lo, n_chains = min(S::kChains, n_k);
+  const int n_k = k_hi - k_lo;
+  const bool deep = NT < 256 && l.f32 && n_k * 64 * S::kSub > kLongSum * S::kChains;
+  const int n_chains = min(S::kChains << deep, n_k);
   const int tile0 = blockIdx.x / team, step = gridDim.x / team;
   const uint16_t both = (uint16_t)(((1 << CG) - 1) << first);
 
@@ -459,15 +467,16 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       bool ok = true;
       const uint64_t w_base = desc_tile(sa(stg)), x_base = desc_tile(sa(stg) + 128 * 128);
       for (int i = tile0; ok && more; t = next, more = more_next, ++u) {
-        const int b = u & 1;
-        if (u >= 2 && !warp_wait(&c.acc_empty[b], (u / 2 - 1) & 1, &c.abort_flag, a.l.status)) break;
+        const int b = deep ? 0 : u & 1, use = deep ? u : u / 2;
+        if (use > 0 && !warp_wait(&c.acc_empty[b], (use - 1) & 1, &c.abort_flag, a.l.status)) break;
         const uint32_t id = idesc(128 * CG, half(t.rows) * CG);
         uint32_t d = tmem + b * S::kChains * NT;
-        int chain = 0, first_of = 0;  // the part of K being summed, its first stage
+        int chain = 0, first_of = 0, next_of = n_k / n_chains;  // the part of K being summed, its first stage, the next's
         for (int k = 0; k < n_k; ++k) {
-          if (S::kChains > 1 && k == n_k * (chain + 1) / n_chains) {
+          if (S::kChains > 1 && k == next_of) {
             ++chain;
             first_of = k;
+            next_of = n_k * (chain + 1) / n_chains;
             d += NT;
           }
           if ((l.order && !warp_wait(&c.landed[s], full_par, &c.abort_flag, a.l.status)) ||
@@ -578,7 +587,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     const int quarter = warp & 3;
     Epilogue<W> e(l, sa(stg) + ST * S::kStage + warp * W * 128, lane);
     for (int i = tile0; more; more = walk.seek(i += step, t), ++u) {
-      const int b = u & 1;
+      const int b = deep ? 0 : u & 1, use = deep ? u : u / 2;
       e.start(l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter
                       : ((long long)t.n * CG + pair) * 128 + 32 * quarter,
               t.row, t.group, a.wide);
@@ -592,7 +601,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       uint32_t mask = rows_of(n0);
       if (l.res) e.prefetch(n0, t.rows);
       if (threadIdx.x == 0)
-        c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], (u / 2) & 1, &c.abort_flag, a.l.status);
+        c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], use & 1, &c.abort_flag, a.l.status);
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!c.epi_ok[u & 1]) break;
       fence_after();
@@ -820,17 +829,18 @@ void consider(const Linear& l, int sms, Cut& best) {
 
 cudaError_t launch_linear_tc(const Linear& l, int sms, cudaStream_t s) {
   Cut cut{0, 0, 0, 0, 1, 0};
+  const bool exact = l.f32 && l.k > kLongSum;
   if (l.offsets) {
     // The rows a group has on average decide; ragged sizes fill either tile as they come.  256 experts, gate and up of
     // 512 x 2,048, 32 / 64 / 128 / 256 rows on average: 148 / 166 / 204 / 283 us in tiles of up to 128 tokens, 161 / 175 /
     // 201 / 254 in tiles of 256 (176 to 830 in lone CTAs' of 32, which tie below 8 rows).
-    if (l.rows / l.groups < 100) return launch<128, 2>(l, cut, sms, s);
+    if (l.rows / l.groups < 100 || exact) return launch<128, 2>(l, cut, sms, s);
     return launch<256, 2>(l, cut, sms, s);
   }
   consider<32, 1>(l, sms, cut);
   consider<128, 1>(l, sms, cut);
   consider<128, 2>(l, sms, cut);
-  consider<256, 2>(l, sms, cut);
+  if (!exact) consider<256, 2>(l, sms, cut);
   if (cut.nt == 128 && cut.cg == 2) return launch<128, 2>(l, cut, sms, s);
   if (cut.nt == 32) return launch<32, 1>(l, cut, sms, s);
   if (cut.nt == 128) return launch<128, 1>(l, cut, sms, s);

@@ -314,3 +314,39 @@ def test_captured_on_two_streams(m):  # noqa: F811
     for i in range(2):
         y, dy = ref.product(x[i], w, None, "none", False, chain(K, True))
         ref.check(out[i], y, dy, BF16)
+
+
+# fp32 results of long sums: K in four parts or more, whatever the tile.  A part has K / 64 additions of 16 products
+# or fewer, each truncated: at most 2^-23 of the running sum, half of that on average, and always the same way.  A sum
+# of random products grows with the root of its length, so the running sum is two thirds of the whole on average.
+# One chain of K / 16 additions would be off by up to four times this (4.4e-6 as measured at K 4,096, beyond the bound).
+def long_sum_bound(K):
+    return K / 64 * 2 / 3 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("B,N,K", [(40, 700, 4096), (300, 1024, 4096), (1024, 1024, 4096), (3000, 2048, 4096),
+                                   (5000, 2056, 8192)])
+def test_fp32_results_of_long_sums(m, B, N, K):
+    g = gen(B, N, K)
+    x, w = normal(g, B, K), normal(g, N, K, std=K ** -0.5)
+    out = torch.empty(B, N, device="cuda")
+    m.moe_linear(x, w, None, None, out, B, N, K, dtype=m.MOE_T_F32)
+    y = x.double() @ w.double().T
+    assert ((out.double() - y).norm() / y.norm()).item() < long_sum_bound(K)
+    again = torch.empty_like(out)
+    m.moe_linear(x, w, None, None, again, B, N, K, dtype=m.MOE_T_F32)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("E,mean,N,K", [(6, 30, 512, 4096), (3, 700, 520, 4096), (40, 300, 1024, 4096)])
+def test_fp32_results_of_long_sums_in_groups(m, E, mean, N, K):
+    r = np.random.default_rng([E, mean, K])
+    ends = np.concatenate(([0], np.cumsum(r.poisson(mean, E))))
+    rows = int(ends[-1])
+    g = gen(E, mean, N, K)
+    offsets = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    x, w = normal(g, rows, K), normal(g, E, N, K, std=K ** -0.5)
+    out = torch.empty(rows, N, device="cuda")
+    m.moe_grouped_linear(x, rows, None, 1, offsets, E, w, None, out, rows, N, K, dtype=m.MOE_T_F32)
+    y = torch.cat([x[a:b].double() @ w[e].double().T for e, (a, b) in enumerate(zip(ends[:-1], ends[1:]))])
+    assert ((out.double() - y).norm() / y.norm()).item() < long_sum_bound(K)
