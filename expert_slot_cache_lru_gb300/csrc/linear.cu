@@ -40,7 +40,8 @@ __device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1
 
 // Operands of any layout: tiles of 128 rows x 128 rows of weights (gated: 64 results, their gate and up rows in turns of
 // eight, which puts a result's halves into one lane), 32 of K at a time, loaded an element a lane (the next 32 into
-// registers while these are multiplied) and from shared memory into the warps' MMAs, 32 x 64 a warp.
+// registers while these are multiplied) and from shared memory into the warps' MMAs, 32 x 64 a warp.  The MMAs truncate
+// their additions, so each 16 of K is a sum of its own, added to the others in fp32, rounded to nearest.
 constexpr int kPitch = 40;  // elements; rows 20 banks apart keep a fragment's 32 words apart
 template <bool GATED>
 __global__ void __launch_bounds__(256) tile_kernel(const Linear l, int tn) {
@@ -94,7 +95,12 @@ __global__ void __launch_bounds__(256) tile_kernel(const Linear l, int tn) {
           const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&ws[wn + 8 * n + g][k + 2 * t4]);
           const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&ws[wn + 8 * n + g][k + 2 * t4 + 8]);
 #pragma unroll
-          for (int m = 0; m < 2; ++m) mma_16x8(acc[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b0, b1);
+          for (int m = 0; m < 2; ++m) {
+            float part[4] = {};
+            mma_16x8(part, a[m][0], a[m][1], a[m][2], a[m][3], b0, b1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[m][n][q] += part[q];
+          }
         }
       }
       __syncthreads();

@@ -1,0 +1,76 @@
+"""fp32 results of the bf16 products over long sums: no error that grows with K as one chain of
+the tensor cores' truncated additions does, whichever kernel takes the call."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_linear import gen, m, normal, padded  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def sum_bound(K):
+    """Off by, relative to the norm of the results.  A chain takes 16 products an addition, at most 512 of K:
+    32 additions, each truncated, by at most 2^-23 of the running sum, half of that on average, always the same
+    way.  A sum of random products grows with the root of its length, so the running sum is two thirds of the
+    chain's on average.  Chains are independent of one another: their errors grow with the root of their number,
+    as the whole sum does, so K does not enter.  They (as sums of 16 products, where these are chains) are added
+    in fp32, rounded to nearest: an error spread evenly over half of 2^-23 of the running sum either way, 2^-24 / sqrt 3 on
+    average, at random signs; the running sum's square is half of the whole's on average: sqrt(n / 6) 2^-24 for n.
+    Chains of 1,024 would be off by up to twice the first term, one of 4,096 by eight times."""
+    return 512 / 16 * 2 / 3 * 2.0 ** -24 + (K / 16 / 6) ** 0.5 * 2.0 ** -24
+
+
+def off_by(out, y):
+    return ((out.double() - y).norm() / y.norm()).item()
+
+
+def dense(m, B, N, K, gated=False, pad=0, off=0):  # noqa: F811
+    g = gen(B, N, K, gated)
+    x = padded(normal(g, B, K), pad, off)
+    w = padded(normal(g, N * (1 + gated), K, std=K ** -0.5), pad, off)
+    outs = [torch.full((B, N), float("nan"), device="cuda") for _ in range(2)]
+    st = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for out in outs:
+        m.moe_linear(x, w, None, None, out, B, N, K, gated=gated, dtype=m.MOE_T_F32, x_stride=K + pad,
+                     w_stride=K + pad, d_status=st)
+    z = x.double() @ w.double().T
+    y = z[:, :N] * z[:, N:] if gated else z
+    assert st.item() == 0
+    # a gated result is a product of two sums
+    assert off_by(outs[0], y) < sum_bound(K) * (1 + gated)
+    assert torch.equal(*outs)
+
+
+# rows that are no whole 16-byte pieces; gated widths that are no multiple of 16
+@pytest.mark.parametrize("B,N,K,gated,pad,off", [
+    (17, 40, 4097, False, 0, 0), (200, 300, 4097, False, 0, 0), (200, 300, 8191, False, 0, 0),
+    (150, 130, 16384, False, 1, 0), (150, 130, 16384, False, 0, 1), (300, 100, 4097, True, 0, 0),
+    (300, 1000, 4096, True, 0, 0), (40, 33, 32768, True, 0, 0)])
+def test_long_sums_of_any_layout(m, B, N, K, gated, pad, off):  # noqa: F811
+    dense(m, B, N, K, gated, pad, off)
+
+
+# few rows, whole and not
+@pytest.mark.parametrize("B", [1, 2, 5, 16])
+@pytest.mark.parametrize("N,K,pad", [(64, 4096, 0), (300, 8192, 0), (64, 65536, 0), (64, 8191, 0), (48, 65536, 1)])
+def test_long_sums_of_few_rows(m, B, N, K, pad):  # noqa: F811
+    dense(m, B, N, K, pad=pad)
+
+
+@pytest.mark.parametrize("E,mean,N,K,gated,gather", [
+    (6, 30, 100, 4097, False, True), (6, 90, 100, 8191, False, False), (5, 60, 200, 4096, True, True)])
+def test_long_sums_in_groups(m, E, mean, N, K, gated, gather):  # noqa: F811
+    r = np.random.default_rng([E, mean, K])
+    ends = np.concatenate(([0], np.cumsum(r.poisson(mean, E))))
+    rows = int(ends[-1])
+    g = gen(E, mean, N, K)
+    offsets = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    x, w = normal(g, rows, K), normal(g, E, N * (1 + gated), K, std=K ** -0.5)
+    order = torch.randperm(rows, generator=g, device="cuda").int() if gather else None
+    out = torch.full((rows, N), float("nan"), device="cuda")
+    m.moe_grouped_linear(x, rows, order, 1, offsets, E, w, None, out, rows, N, K, gated=gated, dtype=m.MOE_T_F32)
+    src = x[order.long()] if gather else x
+    z = torch.cat([src[a:b].double() @ w[e].double().T for e, (a, b) in enumerate(zip(ends[:-1], ends[1:]))])
+    y = z[:, :N] * z[:, N:] if gated else z
+    assert off_by(out, y) < sum_bound(K) * (1 + gated)
