@@ -19,8 +19,8 @@
 // the cycles (plain 281 us, 1,957 TFLOP/s); experts' gate and up (256 of 2 x 512 x 2,048, 65,536 gathered
 // rows) 255 to 275 us, 11.4 TB/s from L2 to the SMs; down products (4,096 x 1,024) HBM, 96%.
 // Sums: the tensor cores add with truncation, an error that grows with the chain of additions;
-// the sum is taken in as many parts of K, up to four, as leave room for two accumulators.  bf16 results hide what
-// is left; fp32 results of long sums take more parts (kLongSum).
+// the sum is taken in as many parts of K, up to four, as leave room for two accumulators.  Where these are too long
+// (kPart) the parts go through three accumulators in turn, and the epilogue's warps add each to a sum of their own.
 // Where tiles are few, `split` CTAs (pairs) of a cluster share a tile: each sums its part of K,
 // then its share of the rows over the parts in ascending order.
 // Every wait is bounded; on a timeout the CTA reports it, drains its copies and MMAs, frees
@@ -36,11 +36,11 @@ using namespace lin;
 
 constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kRowWarp = 10, kThreads = 384;
 constexpr long long kLandCycles = 2000 * 1000;
-// fp32 results: K of a part beyond which one accumulator takes the place of both, in twice the parts, and of a sum
-// beyond which no tile has 256 tokens.  Off by, relative to the norm of the sums, at K 1,024 / 2,048 / 4,096:
-// 4.7e-7 / 4.7e-7 / 1.0e-6, without this 1.0e-6 / 2.1e-6 / 4.4e-6 (a plain fp32 form 2.5e-7 / 3.9e-7 / 6.1e-7).
-// 65,536 rows of 256 groups, N 1,024: 158 / 322 us at K 1,024 / 2,048, without 150 / 254; 8,192 x 8,192 x 4,096 380, without 294.
-constexpr int kLongSum = 640;
+// K of one chain at most, for results of fp32 and of bf16.  Chains of 512 are off by 4.7e-7 of the norm of the sums, whatever
+// the whole K, one of 4,096 by 4.4e-6 (a plain fp32 form at K 1,024 / 4,096 / 16,384: 2.5e-7 / 6.1e-7 / 1.5e-6); the rounding to
+// bf16 is off by 1.7e-3.  65,536 rows of 256 groups, N 1,024, fp32: 175 / 300 us at K 1,024 / 2,048 (one chain in tiles of
+// 256 tokens 150 / 254); 8,192 x 8,192 x 4,096 338 (294).
+constexpr int kPart = 512, kPartBf16 = 65536;
 constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
 
 template <int NT, int CG>
@@ -59,6 +59,7 @@ struct Shape {
   static constexpr int kSmem = kStages * kStage + kTurn + 1024;
   static constexpr int kPitch = NT + 4;                  // of a split's sums
   static_assert(kCols <= 512 && (kCols & (kCols - 1)) == 0 && kStage % 1024 == 0, "tile shape");
+  static_assert(NT == 256 || kCols >= 4 * NT, "room for a long sum");
   static_assert(kStages * kStage + kTurn >= 128 * kPitch * 4 * (CG == 1 ? 7 : 6) / 4, "room for a split's sums");
 };
 
@@ -69,15 +70,16 @@ struct Args {
   int shift;  // a group's tiles have up to 1 << shift tokens
   int nk;     // stages of K
   int split;  // parts of K
+  int part;   // stages of K of a chain at most
   int wide;   // four neighbouring results of out and res are one aligned access
 };
 
 template <int ST>
 struct Ctl {
   uint64_t full[ST], empty[ST], landed[ST];  // landed: gathered rows of x
-  uint64_t acc_full[2], acc_empty[2], drain, sums;
+  uint64_t acc_full[3], acc_empty[3], drain, sums;
   uint32_t tmem;
-  int abort_flag, epi_ok[2];  // epi_ok: the epilogue's wait, by tile parity
+  int abort_flag, epi_ok[2];  // epi_ok: the epilogue's waits in turn
 };
 
 #define MOE_LIN_LOAD(cg, dim, coords)                                                             \
@@ -137,22 +139,32 @@ __device__ __forceinline__ uint32_t idesc(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// W tokens of the warp's lanes, the sums of n_chains parts of K added up in order
-template <int NT, int W>
-__device__ __forceinline__ void read_sums(uint32_t at, int n_chains, uint32_t (&v)[W]) {
+// W tokens of the warp's lanes, the sums of n chains added up in order: the first at `at`, the others `step` on each
+template <int W>
+__device__ __forceinline__ void read_sums(uint32_t at, uint32_t step, int n, uint32_t (&v)[W]) {
   uint32_t u[W];
   tmem_ld(at, v);
-  if (n_chains > 1) tmem_ld(at + NT, u);
+  if (n > 1) tmem_ld(at + step, u);
   tmem_wait_ld();
-  for (int k = 1; k < n_chains; ++k) {
+  for (int k = 1; k < n; ++k) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
-    if (k + 1 < n_chains) {
-      tmem_ld(at + (k + 1) * NT, u);
+    if (k + 1 < n) {
+      tmem_ld(at + (k + 1) * step, u);
       tmem_wait_ld();
     }
   }
 }
+
+// The accumulators in turn, as the MMAs fill them and the epilogue takes them.
+template <int N>
+struct Turn {
+  int b = 0, par = 0;  // par: of this round
+  __device__ __forceinline__ void next() {
+    b = b + 1 == N ? 0 : b + 1;
+    par ^= b == 0;
+  }
+};
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -342,7 +354,10 @@ struct Epilogue {
   }
 };
 
-template <int NT, int CG>
+// LONG: sums of more chains than an accumulator has.  Three accumulators of one chain each then, and the sum of the
+// chains so far as a fourth, which the epilogue alone uses; else two of up to kChains.  (By a branch in one
+// kernel: 8,192 x 8,192 x 1,024 fp32 113 us, so 108.)
+template <int NT, int CG, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
               const __grid_constant__ CUtensorMap xmap_all, const __grid_constant__ Args a) {
@@ -360,8 +375,8 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   const int team = CG * a.split;
   const int k_lo = (int)((long long)a.nk * part / a.split), k_hi = (int)((long long)a.nk * (part + 1) / a.split);
   const int n_k = k_hi - k_lo;
-  const bool deep = NT < 256 && l.f32 && n_k * 64 * S::kSub > kLongSum * S::kChains;
-  const int n_chains = min(S::kChains << deep, n_k);
+  constexpr int kAccs = LONG ? 3 : 2, kAcc = LONG ? NT : S::kChains * NT;  // accumulators, columns of one
+  const int n_chains = S::kChains == 1 ? 1 : min(S::kChains, n_k), n_parts = LONG ? (n_k + a.part - 1) / a.part : 1;
   const int tile0 = blockIdx.x / team, step = gridDim.x / team;
   const uint16_t both = (uint16_t)(((1 << CG) - 1) << first);
 
@@ -371,7 +386,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     mbar_init(&c.full[i], l.order ? CG : 1);  // with the second CTA's gathered rows handed on
     mbar_init(&c.empty[i], 1);
     mbar_init(&c.landed[i], 64);
-    if (i < 2) {
+    if (i < 3) {
       mbar_init(&c.acc_full[i], 1);
       mbar_init(&c.acc_empty[i], kEpiWarps * CG);
     }
@@ -462,22 +477,37 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     __syncwarp();
   } else if (warp == kMmaWarp) {
     if (pair == 0) {
-      int u = 0, s = 0;
+      int s = 0;
       uint32_t full_par = 0;
       bool ok = true;
       const uint64_t w_base = desc_tile(sa(stg)), x_base = desc_tile(sa(stg) + 128 * 128);
-      for (int i = tile0; ok && more; t = next, more = more_next, ++u) {
-        const int b = deep ? 0 : u & 1, use = deep ? u : u / 2;
-        if (use > 0 && !warp_wait(&c.acc_empty[b], (use - 1) & 1, &c.abort_flag, a.l.status)) break;
+      Turn<kAccs> acc;
+      // an accumulator of the first round is free: the phase before a barrier's first one counts as over
+      auto take = [&] { return warp_wait(&c.acc_empty[acc.b], acc.par ^ 1, &c.abort_flag, a.l.status); };
+      for (int i = tile0; ok && more; t = next, more = more_next) {
+        if (!take()) break;
         const uint32_t id = idesc(128 * CG, half(t.rows) * CG);
-        uint32_t d = tmem + b * S::kChains * NT;
-        int chain = 0, first_of = 0, next_of = n_k / n_chains;  // the part of K being summed, its first stage, the next's
+        uint32_t d = tmem + acc.b * kAcc;
+        // the part of K being summed, its first stage, the next's
+        int chain = 0, first_of = 0, next_of = LONG ? a.part : n_k / n_chains;
         for (int k = 0; k < n_k; ++k) {
-          if (S::kChains > 1 && k == next_of) {
-            ++chain;
+          if ((LONG || S::kChains > 1) && k == next_of) {
             first_of = k;
-            next_of = n_k * (chain + 1) / n_chains;
-            d += NT;
+            if constexpr (LONG) {
+              if (elect_one()) mma_commit<CG>(&c.acc_full[acc.b], both);
+              __syncwarp();
+              acc.next();
+              if (!take()) {
+                ok = false;
+                break;
+              }
+              next_of += a.part;
+              d = tmem + acc.b * kAcc;
+            } else {
+              ++chain;
+              next_of = n_k * (chain + 1) / n_chains;
+              d += NT;
+            }
           }
           if ((l.order && !warp_wait(&c.landed[s], full_par, &c.abort_flag, a.l.status)) ||
               !warp_wait(&c.full[s], full_par, &c.abort_flag, a.l.status)) {
@@ -503,8 +533,9 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
           if (k == 0) more_next = walk.seek(i += step, next);
         }
         if (!ok) break;
-        if (elect_one()) mma_commit<CG>(&c.acc_full[b], both);
+        if (elect_one()) mma_commit<CG>(&c.acc_full[acc.b], both);
         __syncwarp();
+        acc.next();
       }
       if (elect_one()) mma_commit<CG>(&c.drain, both);
       __syncwarp();
@@ -579,54 +610,82 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       copies_wait();
     }
     __syncwarp();
-  } else if (a.split > 1) {
-    if (threadIdx.x == 0) c.epi_ok[0] = wait_bar(&c.acc_full[0], 0, &c.abort_flag, a.l.status);
-    __syncwarp();
   } else {
-    int u = 0;
     const int quarter = warp & 3;
-    Epilogue<W> e(l, sa(stg) + ST * S::kStage + warp * W * 128, lane);
-    for (int i = tile0; more; more = walk.seek(i += step, t), ++u) {
-      const int b = deep ? 0 : u & 1, use = deep ? u : u / 2;
-      e.start(l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter
-                      : ((long long)t.n * CG + pair) * 128 + 32 * quarter,
-              t.row, t.group, a.wide);
-      auto rows_of = [&](int n0) {  // which of W tokens have a row
-        const int left = t.rows - n0;
-        const uint32_t in = left >= W ? 0xffffffffu >> (32 - W) : left > 0 ? (1u << left) - 1 : 0u;
-        if (!l.order) return in;
-        return __ballot_sync(kAll, (in >> lane & 1) && source_row(l, t.row + n0 + lane) >= 0);
-      };
-      int n0 = (warp >> 2) * W;
-      uint32_t mask = rows_of(n0);
-      if (l.res) e.prefetch(n0, t.rows);
-      if (threadIdx.x == 0)
-        c.epi_ok[u & 1] = wait_bar(&c.acc_full[b], use & 1, &c.abort_flag, a.l.status);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16), run = lanes + 3 * NT;
+    Turn<kAccs> acc;
+    int waits = 0;
+    // the accumulator is full, told by one thread to all
+    auto filled = [&] {
+      if (threadIdx.x == 0) c.epi_ok[waits & 1] = wait_bar(&c.acc_full[acc.b], acc.par, &c.abort_flag, a.l.status);
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (!c.epi_ok[u & 1]) break;
-      fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16) + b * S::kChains * NT;
-#pragma unroll 1
-      for (; n0 < t.rows; n0 += 2 * W) {
-        uint32_t r[W / 4][4];
-        if (l.res) e.fetch(n0, mask, r);
-        const uint32_t next = rows_of(n0 + 2 * W);
-        uint32_t v[W];
-        read_sums<NT>(acc + n0, n_chains, v);
-        __syncwarp();
-        e.turn(v);
-        __syncwarp();
-        with_act(l.act, [&](auto act) {
-          if (e.gated) e.template finish<true>(act, n0, mask, r);
-          else e.template finish<false>(act, n0, mask, r);
-        });
-        mask = next;
-      }
+      return c.epi_ok[waits++ & 1] != 0;
+    };
+    auto release = [&] {
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 1) mbar_arrive(&c.acc_empty[b]);
-        else mbar_arrive_at(peer_addr(sa(&c.acc_empty[b]), first));
+        if (CG == 1) mbar_arrive(&c.acc_empty[acc.b]);
+        else mbar_arrive_at(peer_addr(sa(&c.acc_empty[acc.b]), first));
+      }
+      acc.next();
+    };
+    // a long sum's parts but the last, for `cols` tokens: a warp's lanes and blocks of tokens are its own here and below
+    auto add_parts = [&](int cols) {
+      for (int k = 1; k < n_parts; ++k) {
+        if (!filled()) return false;
+        fence_after();
+        const uint32_t at = lanes + acc.b * kAcc;
+#pragma unroll 1
+        for (int n0 = (warp >> 2) * W; n0 < cols; n0 += 2 * W) {
+          uint32_t v[W];
+          if (k == 1) read_sums(at + n0, 0, 1, v);
+          else read_sums(run + n0, at - run, 2, v);
+          tmem_st_all<W, 0>(run + n0, v);
+        }
+        tmem_wait_st();
+        release();
+      }
+      return true;
+    };
+    if (a.split > 1) {  // one tile; its sums are exchanged below
+      if (add_parts(NT)) filled();
+    } else {
+      Epilogue<W> e(l, sa(stg) + ST * S::kStage + warp * W * 128, lane);
+      for (int i = tile0; more; more = walk.seek(i += step, t)) {
+        e.start(l.gated ? ((long long)t.n * CG + pair) * 64 + 16 * quarter
+                        : ((long long)t.n * CG + pair) * 128 + 32 * quarter,
+                t.row, t.group, a.wide);
+        auto rows_of = [&](int n0) {  // which of W tokens have a row
+          const int left = t.rows - n0;
+          const uint32_t in = left >= W ? 0xffffffffu >> (32 - W) : left > 0 ? (1u << left) - 1 : 0u;
+          if (!l.order) return in;
+          return __ballot_sync(kAll, (in >> lane & 1) && source_row(l, t.row + n0 + lane) >= 0);
+        };
+        int n0 = (warp >> 2) * W;
+        uint32_t mask = rows_of(n0);
+        if (l.res) e.prefetch(n0, t.rows);
+        if (!add_parts(t.rows) || !filled()) break;
+        fence_after();
+        const uint32_t sums = lanes + acc.b * kAcc;
+#pragma unroll 1
+        for (; n0 < t.rows; n0 += 2 * W) {
+          uint32_t r[W / 4][4];
+          if (l.res) e.fetch(n0, mask, r);
+          const uint32_t next = rows_of(n0 + 2 * W);
+          uint32_t v[W];
+          if constexpr (LONG) read_sums(run + n0, sums - run, 2, v);
+          else read_sums(sums + n0, NT, n_chains, v);
+          __syncwarp();
+          e.turn(v);
+          __syncwarp();
+          with_act(l.act, [&](auto act) {
+            if (e.gated) e.template finish<true>(act, n0, mask, r);
+            else e.template finish<false>(act, n0, mask, r);
+          });
+          mask = next;
+        }
+        release();
       }
     }
     __syncwarp();
@@ -659,11 +718,13 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     if (warp < kEpiWarps) {
       fence_after();
       const int pr = 32 * (warp & 3) + lane;
-      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16), run = acc + 3 * NT;
+      const uint32_t last = acc + (n_parts - 1) % 3 * NT;  // of a long sum's parts
 #pragma unroll 1
       for (int n0 = (warp >> 2) * W; n0 < NT; n0 += 2 * W) {
         uint32_t v[W];
-        read_sums<NT>(acc + n0, n_chains, v);
+        if constexpr (LONG) read_sums(run + n0, last - run, 2, v);
+        else read_sums(acc + n0, NT, n_chains, v);
 #pragma unroll
         for (int i = 0; i < W; i += 4)
           *reinterpret_cast<uint4*>(own + pr * kPitch + n0 + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -742,10 +803,13 @@ long long tiles_n(const Linear& l, int cg) {
   return (l.n + (long long)per - 1) / per;
 }
 
-template <int NT, int CG>
+// K of a chain at most.
+int longest(const Linear& l) { return l.f32 ? kPart : kPartBf16; }
+
+template <int NT, int CG, bool LONG>
 cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
   using S = Shape<NT, CG>;
-  auto kern = linear_kernel<NT, CG>;
+  auto kern = linear_kernel<NT, CG, LONG>;
   static Once once;
   cudaError_t e = raise_smem(once, kern, S::kSmem);
   if (e != cudaSuccess) return e;
@@ -760,6 +824,7 @@ cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
   a.tn = (int)tn;
   a.nk = (int)((l.k + 64ll * S::kSub - 1) / (64 * S::kSub));
   a.split = cut.split;
+  a.part = longest(l) / (64 * S::kSub);
   const int team = CG * a.split;
   auto whole = [&](const void* p, long long stride) {  // 4 results
     return (reinterpret_cast<uintptr_t>(p) & (l.f32 ? 15 : 7)) == 0 && stride % 4 == 0;
@@ -786,6 +851,17 @@ cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, wm, xm, xa, a);
+}
+
+template <int NT, int CG>
+cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
+  if constexpr (NT < 256) {
+    // of the largest part of K; the smallest is a stage less, two chains at least
+    constexpr int kStageK = 64 * Shape<NT, CG>::kSub;
+    const long long nk = (l.k + kStageK - 1ll) / kStageK, most = (nk + cut.split - 1) / cut.split;
+    if (most * kStageK > (long long)Shape<NT, CG>::kChains * longest(l)) return launch<NT, CG, true>(l, cut, sms, s);
+  }
+  return launch<NT, CG, false>(l, cut, sms, s);
 }
 
 // Parts of K that give every SM a CTA where tiles are few.
@@ -829,7 +905,7 @@ void consider(const Linear& l, int sms, Cut& best) {
 
 cudaError_t launch_linear_tc(const Linear& l, int sms, cudaStream_t s) {
   Cut cut{0, 0, 0, 0, 1, 0};
-  const bool exact = l.f32 && l.k > kLongSum;
+  const bool exact = l.k > longest(l);  // tiles of 256 tokens keep one chain
   if (l.offsets) {
     // The rows a group has on average decide; ragged sizes fill either tile as they come.  256 experts, gate and up of
     // 512 x 2,048, 32 / 64 / 128 / 256 rows on average: 148 / 166 / 204 / 283 us in tiles of up to 128 tokens, 161 / 175 /

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_linear import gen, m, normal, padded  # noqa: F401
+from tests.test_gpu_linear import gen, linear_case, m, normal, padded  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -42,6 +42,24 @@ def dense(m, B, N, K, gated=False, pad=0, off=0):  # noqa: F811
     assert torch.equal(*outs)
 
 
+# tiles of 32, 128 and a pair's 128 tokens; K cut over clusters and not; one and several tiles a CTA; widths that end inside
+@pytest.mark.parametrize("B,N,K", [(20, 128, 16384), (30, 4096, 16384), (64, 512, 65536), (100, 20000, 2048),
+                                   (300, 300, 16384), (300, 1024, 4096), (1000, 5000, 1280), (1000, 5000, 1344),
+                                   (2000, 2500, 2048), (2000, 2500, 2056), (3000, 4096, 16384), (5000, 2056, 8192)])
+def test_long_sums(m, B, N, K):  # noqa: F811
+    dense(m, B, N, K)
+
+
+@pytest.mark.parametrize("B,N,K", [(30, 512, 16384), (200, 96, 8192), (1500, 1024, 4096), (1500, 1024, 16384)])
+def test_long_sums_gated(m, B, N, K):  # noqa: F811
+    dense(m, B, N, K, gated=True)
+
+
+@pytest.mark.parametrize("B,N,K,gated", [(300, 300, 131072, False), (300, 300, 65600, True), (20, 128, 1 << 21, False)])
+def test_the_longest_sums_of_bf16_results(m, B, N, K, gated):  # noqa: F811
+    linear_case(m, B, N, K, gated=gated, kind="silu" if gated else "none", bias=True, res=True)
+
+
 # rows that are no whole 16-byte pieces; gated widths that are no multiple of 16
 @pytest.mark.parametrize("B,N,K,gated,pad,off", [
     (17, 40, 4097, False, 0, 0), (200, 300, 4097, False, 0, 0), (200, 300, 8191, False, 0, 0),
@@ -59,7 +77,10 @@ def test_long_sums_of_few_rows(m, B, N, K, pad):  # noqa: F811
 
 
 @pytest.mark.parametrize("E,mean,N,K,gated,gather", [
-    (6, 30, 100, 4097, False, True), (6, 90, 100, 8191, False, False), (5, 60, 200, 4096, True, True)])
+    (6, 30, 512, 16384, False, True), (3, 700, 520, 16384, False, False), (40, 300, 1024, 4096, False, True),
+    (40, 300, 1024, 2048, True, True), (64, 40, 1024, 1344, False, False), (100, 150, 512, 8192, False, True),
+    (6, 30, 100, 4097, False, True), (6, 90, 100, 8191, False, False), (5, 60, 200, 4096, True, True),
+    (8, 1, 128, 32768, False, True)])
 def test_long_sums_in_groups(m, E, mean, N, K, gated, gather):  # noqa: F811
     r = np.random.default_rng([E, mean, K])
     ends = np.concatenate(([0], np.cumsum(r.poisson(mean, E))))
