@@ -433,8 +433,14 @@ cudaError_t launch_linear(const Linear& call, cudaStream_t s) {
   const bool whole = l.k % 8 == 0 && l.x_stride % 8 == 0 && l.w_stride % 8 == 0 && l.group_stride % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(l.x) | reinterpret_cast<uintptr_t>(l.w)) & 15) == 0;
   // Places one by one while they are few, or most have a group to themselves (24 / 48 places over 256 experts of
-  // 2 x 512 x 2,048: 19.6 / 34.2 us, in tiles 23.8 / 35.8; 48 over 64 of 2 x 1,024 x 4,096: 96 and 87).
-  const bool few = l.rows <= 16 || (l.rows <= 48 && 4 * l.rows <= l.groups);
+  // 2 x 512 x 2,048: 19.6 / 34.2 us, in tiles 23.8 / 35.8; 48 over 64 of 2 x 1,024 x 4,096: 96 and 87).  Each place reads
+  // its whole matrix: more places than groups read some again, from L2 or not, and no more than 64 MiB of it (over one group,
+  // dot products / tiles: 16 places of 2 x 512 x 2,048 9.2 / 9.6 us, of 4,096 x 1,024 20.1 / 7.3; 4 and 16 of 2 x 1,024 x 4,096
+  // 8.5 / 15.0 and 21.9 / 15.1; 2 and 16 of 4,096 x 8,192 15.5 / 24.6 and 69.2 / 24.6, of 16,384 x 8,192 80 / 45 and 581 / 46;
+  // over 16 groups of 2 x 1,024 x 4,096: 8 places 24.0 / 24.1, 16 45.3 / 42.9).
+  const long long read = (long long)l.n * (l.gated ? 2 : 1) * l.k * 2;  // by a place
+  const bool few = l.rows <= 16 ? l.rows <= l.groups || read <= (1ll << 26) / (l.rows - 1)
+                                : l.rows <= 48 && 4 * l.rows <= l.groups;
   if (whole && l.offsets && few) return launch_dots<1>(l, d.sms, s);
   if (whole && !l.offsets && l.rows <= kDotRows)
     return l.rows == 1 ? launch_dots<1>(l, d.sms, s) : launch_dots<2>(l, d.sms, s);

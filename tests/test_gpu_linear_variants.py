@@ -37,3 +37,12 @@ def test_places_of_many_groups(m, kw, places, E):  # noqa: F811
     for N, K in ((96, 256), (64, 4096)):
         grouped_case(m, counts, N, K, spare=0, **kw)
     grouped_case(m, counts[:-1] + [counts[-1] - 1], 96, 256, spare=1, **kw)
+
+
+# more places than groups, either side of what the matrices read again may amount to
+@pytest.mark.parametrize("kw", [dict(kind="silu", gated=True, bias=True), dict(f32=True), dict(gather=False)])
+@pytest.mark.parametrize("counts,N,K", [([16], 1024, 2176), ([16], 1024, 2240), ([0, 7, 0, 9], 1200, 2048),
+                                        ([1, 1, 1, 0], 4096, 4096), ([2], 4096, 8192), ([2], 4104, 8192),
+                                        ([3, 2], 2048, 4096), ([1], 8192, 8192)])
+def test_more_places_than_groups(m, kw, counts, N, K):  # noqa: F811
+    grouped_case(m, counts, N // 2 if kw.get("gated") else N, K, spare=0, **kw)
