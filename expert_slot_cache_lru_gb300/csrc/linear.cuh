@@ -16,7 +16,8 @@ __device__ __forceinline__ float sigmoid(float z) {
 }
 // z Phi(z) by the upper tail Q(a) = e^(-a^2 / 2) R(a), a = |z|: no cancellation in Phi's lower tail.  R is the
 // smooth scaled tail erfcx(a / sqrt 2) / 2, here t times a polynomial of degree 8 in t = 1 / (1 + 0.35 a), fitted for least
-// relative error over 0 .. 16 (2^-25; 5 2^-24 in fp32 steps); the exponent's rounding a^2 - fl(a^2) is put back.
+// relative error over 0 .. 16 (2^-24); the exponent's rounding a^2 - fl(a^2) is put back.  All of it is at most 7.8 2^-24
+// off, over 6 million fp32 z of -12.5 .. 6.
 // 8,192 x 8,192 x 512 with a residual 232 us, by normcdff (67 cycles a lane) 291.
 __device__ __forceinline__ float gelu(float z) {
   const float a = fminf(fabsf(z), 16.f);  // Q(16) is below fp32; a NaN comes back with z

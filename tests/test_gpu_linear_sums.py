@@ -16,7 +16,8 @@ def sum_bound(K):
     chain's on average.  Chains are independent of one another: their errors grow with the root of their number,
     as the whole sum does, so K does not enter.  They (as sums of 16 products, where these are chains) are added
     in fp32, rounded to nearest: an error spread evenly over half of 2^-23 of the running sum either way,
-    2^-24 / sqrt 3 on average, at random signs; the running sum's square is half of the whole's on average: sqrt(n / 6) 2^-24 for n.
+    2^-24 / sqrt 3 on average, at random signs; the running sum's square is half of the whole's on average:
+    sqrt(n / 6) 2^-24 for n.
     Chains of 1,024 would be off by up to twice the first term, one of 4,096 by eight times."""
     return 512 / 16 * 2 / 3 * 2.0 ** -24 + (K / 16 / 6) ** 0.5 * 2.0 ** -24
 

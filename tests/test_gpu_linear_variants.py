@@ -1,7 +1,10 @@
-"""Each form of the bf16 products of few rows that the sizes choose."""
+"""Each form of the bf16 products of few rows that the sizes choose, and GELU at arguments that
+are no bf16 numbers."""
 import pytest
+import torch
 
-from tests.test_gpu_linear import grouped_case, linear_case, m  # noqa: F401
+from tests import linear_ref as ref
+from tests.test_gpu_linear import BF16, grouped_case, linear_case, m  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +49,26 @@ def test_places_of_many_groups(m, kw, places, E):  # noqa: F811
                                         ([3, 2], 2048, 4096), ([1], 8192, 8192)])
 def test_more_places_than_groups(m, kw, counts, N, K):  # noqa: F811
     grouped_case(m, counts, N // 2 if kw.get("gated") else N, K, spare=0, **kw)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 20])
+def test_gelu_of_fp32_arguments(m, rows):  # noqa: F811
+    """z is any fp32 number: three bf16 weights of which each holds what the ones before leave, times one.  They are
+    one lane's or one addition's products, no more than 24 bits together: z is exact."""
+    g = torch.Generator().manual_seed(3)
+    z = torch.cat([torch.rand(300000, generator=g) * 6 - 3, torch.rand(300000, generator=g) * 30 - 15,
+                   torch.rand(100000, generator=g) * 0.01 - 0.005]).cuda()
+    N, K = z.numel(), 8
+    w = torch.zeros(N, K, dtype=BF16, device="cuda")
+    left = z.clone()
+    for j in range(3):
+        w[:, j] = (left.view(torch.int32) & -65536).view(torch.float32).to(BF16)  # the upper half of its bits
+        left -= w[:, j].float()
+    assert (left == 0).all() and (w.double().sum(1) == z.double()).all()
+    x = torch.ones(rows, K, dtype=BF16, device="cuda")
+    plain, out = (torch.empty(rows, N, device="cuda") for _ in range(2))
+    m.moe_linear(x, w, None, None, plain, rows, N, K, dtype=m.MOE_T_F32)
+    m.moe_linear(x, w, None, None, out, rows, N, K, act=m.MOE_ACT_GELU, dtype=m.MOE_T_F32)
+    assert (plain == z).all()
+    y, e = ref.act(z.double(), "gelu")
+    assert ((out.double() - y).abs() <= e).all()
