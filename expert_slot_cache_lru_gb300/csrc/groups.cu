@@ -379,7 +379,7 @@ cudaError_t launch_group_routes(const int32_t* ids, int routes, int experts, int
                                 int32_t* order, int32_t* pos, cudaStream_t s) {
   GroupArgs a{ids, offsets, order, pos, routes, experts, 1, 32, 1, experts, 0};
   while ((experts - 1) >> a.bits) ++a.bits;
-  // a CTA holds 32 warps of counters where they fit, at least 3 (16,384 experts in 16 bits)
+  // a CTA holds 32 warps of counters where they fit; of 16,384 experts 5 in 16 bits, 2 in 32
   const int room = 224 * 1024 - 4 * experts;
   auto plan = [&](int bytes) {
     const int most = room / (bytes * experts) < 32 ? room / (bytes * experts) : 32;

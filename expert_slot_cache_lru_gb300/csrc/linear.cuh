@@ -98,7 +98,6 @@ inline void division_of(int d, unsigned& mul, int& shift) {
 // are loaded ahead.
 struct Tile {
   int group, row, rows, n;  // rows: of this tile; n: which tile of n
-  int width;                // rows of the group's tiles
 };
 struct Walk {
   const int32_t* offsets;
@@ -172,7 +171,6 @@ struct Walk {
   // tile r of T by tn tiles of `width` rows from lo to hi
   __device__ __forceinline__ void place(int r, int T, int width, int lo_, int hi_, Tile& out) const {
     const int per = 8 * T, strip = r / per, in = r - strip * per, w = min(8, tn - strip * 8);
-    out.width = width;
     out.n = strip * 8 + in % w;
     out.row = lo_ + in / w * width;
     out.rows = min(width, hi_ - out.row);

@@ -379,11 +379,12 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   const int n_chains = S::kChains == 1 ? 1 : min(S::kChains, n_k), n_parts = LONG ? (n_k + a.part - 1) / a.part : 1;
   const int tile0 = blockIdx.x / team, step = gridDim.x / team;
   const uint16_t both = (uint16_t)(((1 << CG) - 1) << first);
+  const bool gather = CG == 2 && l.order;  // groups take pairs
 
   pdl_trigger();
   if (threadIdx.x < ST) {
     const int i = threadIdx.x;
-    mbar_init(&c.full[i], l.order ? CG : 1);  // with the second CTA's gathered rows handed on
+    mbar_init(&c.full[i], gather ? CG : 1);  // with the second CTA's gathered rows handed on
     mbar_init(&c.empty[i], 1);
     mbar_init(&c.landed[i], 64);
     if (i < 3) {
@@ -399,7 +400,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   }
   if (warp == kTmaWarp && elect_one()) {  // the maps are on their way when the first copy reads them
     prefetch_map(&wmap);
-    prefetch_map(l.order ? &wmap : &xmap_all);
+    prefetch_map(gather ? &wmap : &xmap_all);
   }
   if (warp == kMmaWarp) tmem_alloc<CG>(&c.tmem, S::kCols);
   fence_before();
@@ -422,17 +423,17 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
   }
   if (!l.offsets) pdl_wait();
 
-  if (warp == kTmaWarp || (warp >= kRowWarp && !l.order && (warp == kRowWarp || l.gated))) {
+  if (warp == kTmaWarp || (warp >= kRowWarp && !gather && (warp == kRowWarp || l.gated))) {
     // Two or three warps, since an instruction takes one about 100 cycles: the weights' copies, the tokens', and half of
     // a gated tile's weights.
-    const int j_lo = warp == kTmaWarp ? 0 : 2, j_hi = warp == kTmaWarp && !l.order ? 2 : 4;
+    const int j_lo = warp == kTmaWarp ? 0 : 2, j_hi = warp == kTmaWarp && !gather ? 2 : 4;
     int it = 0, s = 0;
     bool ok = true;
     for (int i = tile0; ok && more; t = next, more = more_next) {
       // boxes of 32 rows, or all the CTA has room for at once
       const int hx = half(t.rows);
       const bool all = hx > S::kX - 32;
-      const int boxes = l.order ? 0 : all ? S::kX / 32 : (hx + 31) / 32;
+      const int boxes = gather ? 0 : all ? S::kX / 32 : (hx + 31) / 32;
       const int bytes = CG * S::kSub * (128 * 128 + boxes * 4096);
       const int x0 = t.row + pair * hx, nt = t.n * CG + pair;
       for (int ks = k_lo; ks < k_hi; ++ks, ++it) {
@@ -509,12 +510,12 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
               d += NT;
             }
           }
-          if ((l.order && !warp_wait(&c.landed[s], full_par, &c.abort_flag, a.l.status)) ||
+          if ((gather && !warp_wait(&c.landed[s], full_par, &c.abort_flag, a.l.status)) ||
               !warp_wait(&c.full[s], full_par, &c.abort_flag, a.l.status)) {
             ok = false;
             break;
           }
-          if (l.order) {
+          if (gather) {
             fence_async_smem();
             __syncwarp();
           }
@@ -539,7 +540,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
       }
       if (elect_one()) mma_commit<CG>(&c.drain, both);
       __syncwarp();
-    } else if (l.order) {
+    } else if (gather) {
       // The second CTA's gathered rows, fenced and handed on to the first.  The arrival is the default one:
       // with .release.cluster it took 2,000 cycles beside copies in flight, four times a stage
       // (65,536 x 1,024 x 2,048 in 256 groups: 564 us, so 284); the rows are in this CTA's shared memory, in order
@@ -564,7 +565,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
     // copies' swizzle.  A thread's copies arrive at `landed` by themselves; the warp that waits
     // there fences them for the MMAs.  (TMA's four-row gathers took about 70 cycles each, 2,200 a
     // stage of 128 rows; a fence by the copying threads waits for all their copies in flight.)
-    if (l.order) {
+    if (gather) {
       constexpr int kPer = S::kX / 8;  // rows of a lane
       const int gw = warp - kRowWarp, chunk = lane & 7, r0 = 4 * gw + (lane >> 3);
       int it = 0, s = 0;
@@ -659,7 +660,7 @@ linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ 
         auto rows_of = [&](int n0) {  // which of W tokens have a row
           const int left = t.rows - n0;
           const uint32_t in = left >= W ? 0xffffffffu >> (32 - W) : left > 0 ? (1u << left) - 1 : 0u;
-          if (!l.order) return in;
+          if (!gather) return in;
           return __ballot_sync(kAll, (in >> lane & 1) && source_row(l, t.row + n0 + lane) >= 0);
         };
         int n0 = (warp >> 2) * W;
@@ -816,7 +817,7 @@ cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
   Args a{};
   a.l = l;
   const long long tn = tiles_n(l, CG);
-  a.shift = NT == 32 ? 5 : NT == 128 ? 7 : 8;
+  a.shift = NT == 128 ? 7 : 8;  // a dense product is cut beforehand
   a.tiles = cut.tiles;
   a.width = cut.width;
   const long long most = l.offsets ? most_tiles(l, a.shift, tn) : cut.tiles * tn;
