@@ -306,6 +306,7 @@ int moe_combine(const void* d_y, int y_dtype, long long y_stride, int y_rows, co
       (y_dtype == MOE_T_F32 && dtype != MOE_T_F32) || !take_stride(y_stride, hidden) ||
       !take_stride(add_stride, hidden) || !take_stride(out_stride, hidden))
     return MOE_ERR_INVALID_ARG;
+  if (k > 1 << 30) return MOE_ERR_UNSUPPORTED;  // the kernel counts routes past the last in 32 bits
   if (n_rows == 0) return MOE_OK;
   const size_t e = size_of(dtype);
   if ((!d_y && y_rows > 0) || !d_pos || !d_w || !d_out || !aligned(d_y, size_of(y_dtype)) ||

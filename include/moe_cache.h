@@ -686,7 +686,7 @@ MOE_API int moe_grouped_linear(const void* d_x, long long x_stride, int x_rows,
 /* out[b] = add[b] + sum_j w[b][j] * y[pos[b][j]],  j ascending from add (NULL = 0), fp32 sums;
  * a pos outside [0, y_rows) adds nothing, whatever its weight.  y [y_rows][hidden] of y_dtype (fp32 only
  * into an fp32 out), pos int32 and w float32 [n_rows][k], add and out [n_rows][hidden] of dtype.
- * d_out may equal d_add, with equal strides; no other overlap. */
+ * k 1 .. 2^30.  d_out may equal d_add, with equal strides; no other overlap. */
 MOE_API int moe_combine(const void* d_y, int y_dtype, long long y_stride, int y_rows,
                         const int32_t* d_pos, const float* d_w, const void* d_add,
                         long long add_stride, int n_rows, int k, int hidden, void* d_out, int dtype,
