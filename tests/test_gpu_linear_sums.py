@@ -43,15 +43,19 @@ def dense(m, B, N, K, gated=False, pad=0, off=0):  # noqa: F811
     assert torch.equal(*outs)
 
 
-# tiles of 32, 128 and a pair's 128 tokens; K cut over clusters and not; one and several tiles a CTA; widths that end inside
+# tiles of 32, 128 and a pair's 128 tokens; K cut over clusters and not; one and several tiles a CTA; widths that end
+# inside one
 @pytest.mark.parametrize("B,N,K", [(20, 128, 16384), (30, 4096, 16384), (64, 512, 65536), (100, 20000, 2048),
                                    (300, 300, 16384), (300, 1024, 4096), (1000, 5000, 1280), (1000, 5000, 1344),
-                                   (2000, 2500, 2048), (2000, 2500, 2056), (3000, 4096, 16384), (5000, 2056, 8192)])
+                                   (2000, 2500, 2048), (2000, 2500, 2056), (3000, 4096, 16384), (5000, 2056, 8192),
+                                   (20, 8192, 2112), (2000, 64, 8192), (2000, 300, 1280), (40, 2500, 8192),
+                                   (500, 1024, 16384), (40, 12000, 1280), (200, 12000, 1280), (40, 8192, 8192)])
 def test_long_sums(m, B, N, K):  # noqa: F811
     dense(m, B, N, K)
 
 
-@pytest.mark.parametrize("B,N,K", [(30, 512, 16384), (200, 96, 8192), (1500, 1024, 4096), (1500, 1024, 16384)])
+@pytest.mark.parametrize("B,N,K", [(30, 512, 16384), (200, 96, 8192), (1500, 1024, 4096), (1500, 1024, 16384),
+                                   (40, 2048, 8192), (40, 4096, 8192)])
 def test_long_sums_gated(m, B, N, K):  # noqa: F811
     dense(m, B, N, K, gated=True)
 

@@ -29,6 +29,15 @@ def test_few_results_of_three_to_sixteen_rows(m, form, B, N, K, gated):  # noqa:
     linear_case(m, B, N, K, gated=gated, **form)
 
 
+# tiles of 32, of 128, of a pair's 128 and 256 tokens, K in one, two and four parts, one and several tiles a CTA
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("B,N,K", [(20, 64, 1280), (40, 2500, 2048), (20, 64, 2048), (2000, 300, 1280), (40, 2500, 8192),
+                                   (40, 12000, 1280), (300, 12000, 1280), (40, 8192, 8192), (100, 12000, 1280),
+                                   (2000, 2500, 1280), (300, 4096, 16384)])
+def test_tiles_and_parts(m, form, B, N, K):  # noqa: F811
+    linear_case(m, B, N, K, **form)
+
+
 # more groups than four times the places: 17 to 48 of them one by one, and the sizes next to these
 @pytest.mark.parametrize("kw", [dict(kind="silu", gated=True), dict(bias=True, f32=True), dict(gather=False),
                                 dict(bad=3, top=8)])
