@@ -804,8 +804,8 @@ long long tiles_n(const Linear& l, int cg) {
   return (l.n + (long long)per - 1) / per;
 }
 
-// K of a chain at most.
-int longest(const Linear& l) { return l.f32 ? kPart : kPartBf16; }
+// K of a chain at most, in tiles that have room for a long sum.  Groups' tiles of 128 tokens wait for HBM and hide its additions.
+int longest(const Linear& l) { return l.f32 || l.offsets ? kPart : kPartBf16; }
 
 template <int NT, int CG, bool LONG>
 cudaError_t launch(const Linear& l, const Cut& cut, int sms, cudaStream_t s) {
@@ -906,7 +906,7 @@ void consider(const Linear& l, int sms, Cut& best) {
 
 cudaError_t launch_linear_tc(const Linear& l, int sms, cudaStream_t s) {
   Cut cut{0, 0, 0, 0, 1, 0};
-  const bool exact = l.k > longest(l);  // tiles of 256 tokens keep one chain
+  const bool exact = l.k > (l.f32 ? kPart : kPartBf16);  // tiles of 256 tokens keep one chain
   if (l.offsets) {
     // The rows a group has on average decide; ragged sizes fill either tile as they come.  256 experts, gate and up of
     // 512 x 2,048, 32 / 64 / 128 / 256 rows on average: 148 / 166 / 204 / 283 us in tiles of up to 128 tokens, 161 / 175 /

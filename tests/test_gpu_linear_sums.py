@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_linear import gen, linear_case, m, normal, padded  # noqa: F401
+from tests.test_gpu_linear import BF16, gen, linear_case, m, normal, padded  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,22 @@ def test_long_sums_in_groups(m, E, mean, N, K, gated, gather):  # noqa: F811
     z = torch.cat([src[a:b].double() @ w[e].double().T for e, (a, b) in enumerate(zip(ends[:-1], ends[1:]))])
     y = z[:, :N] * z[:, N:] if gated else z
     assert off_by(out, y) < sum_bound(K) * (1 + gated)
+
+
+@pytest.mark.parametrize("E,mean,N,K,gated,gather", [(300, 2, 512, 2048, True, True), (40, 60, 520, 4096, False, False),
+                                                     (30, 90, 256, 1344, True, True)])
+def test_bf16_results_of_short_groups(m, E, mean, N, K, gated, gather):  # noqa: F811
+    """The sums of fp32 results, rounded: the same chains whatever the type."""
+    r = np.random.default_rng([E, mean, K])
+    ends = np.concatenate(([0], np.cumsum(r.poisson(mean, E))))
+    rows = int(ends[-1])
+    assert 48 < rows < 100 * E
+    g = gen(E, mean, N, K)
+    offsets = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    x, w = normal(g, rows, K), normal(g, E, N * (1 + gated), K, std=K ** -0.5)
+    order = torch.randperm(rows, generator=g, device="cuda").int() if gather else None
+    wide, out = (torch.full((rows, N), float("nan"), dtype=t, device="cuda") for t in (torch.float32, BF16))
+    for o, t in ((wide, m.MOE_T_F32), (out, m.MOE_T_BF16)):
+        m.moe_grouped_linear(x, rows, order, 1, offsets, E, w, None, o, rows, N, K, act=m.MOE_ACT_SILU, gated=gated,
+                             dtype=t)
+    assert torch.equal(out, wide.to(BF16))
