@@ -119,3 +119,41 @@ def test_bf16_results_of_short_groups(m, E, mean, N, K, gated, gather):  # noqa:
         m.moe_grouped_linear(x, rows, order, 1, offsets, E, w, None, o, rows, N, K, act=m.MOE_ACT_SILU, gated=gated,
                              dtype=t)
     assert torch.equal(out, wide.to(BF16))
+
+
+def test_long_sums_captured_on_two_streams(m):  # noqa: F811
+    """Graphs of dense products, cut over clusters and not, and of groups, replayed at once and again."""
+    def calls(side):
+        g = gen("two", side)
+        offsets = torch.tensor([0, 40, 40, 300, 411], dtype=torch.int32, device="cuda")
+        some = [(normal(g, B, K), normal(g, N, K, std=K ** -0.5)) for B, N, K in ((40, 2500, 8192), (700, 1000, 4096))]
+        x, w = normal(g, 411, 4096), normal(g, 4, 256, 4096, std=1 / 64)
+        outs = [torch.empty(a.shape[0], b.shape[0], device="cuda") for a, b in some] + [torch.empty(411, 256, device="cuda")]
+
+        def go():
+            for (a, b), o in zip(some, outs):
+                m.moe_linear(a, b, None, None, o, a.shape[0], b.shape[0], a.shape[1], dtype=m.MOE_T_F32)
+            m.moe_grouped_linear(x, 411, None, 1, offsets, 4, w, None, outs[2], 411, 256, 4096, dtype=m.MOE_T_F32)
+
+        go()
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go()
+            go()
+        return graph, outs, want
+
+    sides = [calls(i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in sides]
+    for _, outs, _ in sides:
+        for o in outs:
+            o.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (graph, _, _), s in zip(sides, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, outs, want in sides:
+        assert all(torch.equal(o, a) for o, a in zip(outs, want))
