@@ -128,7 +128,7 @@ def test_long_sums_captured_on_two_streams(m):  # noqa: F811
         offsets = torch.tensor([0, 40, 40, 300, 411], dtype=torch.int32, device="cuda")
         some = [(normal(g, B, K), normal(g, N, K, std=K ** -0.5)) for B, N, K in ((40, 2500, 8192), (700, 1000, 4096))]
         x, w = normal(g, 411, 4096), normal(g, 4, 256, 4096, std=1 / 64)
-        outs = [torch.empty(a.shape[0], b.shape[0], device="cuda") for a, b in some] + [torch.empty(411, 256, device="cuda")]
+        outs = [torch.empty(a.shape[0], b.shape[0], device="cuda") for a, b in (*some, (x, w[0]))]
 
         def go():
             for (a, b), o in zip(some, outs):
@@ -142,18 +142,18 @@ def test_long_sums_captured_on_two_streams(m):  # noqa: F811
         with torch.cuda.graph(graph):
             go()
             go()
-        return graph, outs, want
+        return graph, outs, want, (some, offsets, x, w)  # the graph's inputs live as long as it
 
     sides = [calls(i) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in sides]
-    for _, outs, _ in sides:
+    for _, outs, _, _ in sides:
         for o in outs:
             o.fill_(float("nan"))
     torch.cuda.synchronize()
     for _ in range(5):
-        for (graph, _, _), s in zip(sides, streams):
+        for (graph, *_), s in zip(sides, streams):
             with torch.cuda.stream(s):
                 graph.replay()
     torch.cuda.synchronize()
-    for _, outs, want in sides:
+    for _, outs, want, _ in sides:
         assert all(torch.equal(o, a) for o, a in zip(outs, want))
