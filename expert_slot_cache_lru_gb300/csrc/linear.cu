@@ -18,7 +18,11 @@ namespace {
 using namespace lin;
 
 constexpr int kDotThreads = 128, kDotRows = 2;
-constexpr int kDotCtas = 8;  // an SM; bounds the registers to 64 (4,096 x 4,096: 7.4 us, with 77 8.0)
+// CTAs an SM, which bound the registers.  Eight, 64 registers (4,096 x 4,096: 7.4 us, with 77 8.0); seven, 72, for a row with a
+// gate, which spills with 64 (8 / 24 places over 256 of 2 x 512 x 2,048: 7.7 / 18.7 us, of eight CTAs 8.1 / 19.4, of six 9.0 /
+// 19.0; one row of 2 x 1,024 x 4,096 5.0, 5.4 and 4.6), but not as 16 warps (2 x 512 x 8,192: 4.8 us, with more registers 6.4).
+template <int R, bool GATED, int THREADS>
+constexpr int kDotCtas = R == 1 && GATED && THREADS == kDotThreads ? 7 : 8 * kDotThreads / THREADS;
 constexpr int kStreamRows = 16;
 // Rows of weights of a CTA's part and 256-element pieces of K of a warp, for R rows of x: the best of
 // 4 and 8 and of 1, 2 and 4 at 4,096 x 4,096 (8.1 and 7.9 us; with more in flight per thread and fewer threads 9
@@ -165,7 +169,7 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
 // weights per part of n (of each matrix half as many if gated); `kw` of its warps share a part, each a
 // slice of K at a time, the slices of x in registers.
 template <int R, bool GATED, int THREADS>
-__global__ void __launch_bounds__(THREADS, kDotCtas * kDotThreads / THREADS) dot_kernel(const Linear l, int kw) {
+__global__ void __launch_bounds__(THREADS, kDotCtas<R, GATED, THREADS>) dot_kernel(const Linear l, int kw) {
   constexpr int kWarps = THREADS / 32, U = Dots<R>::U, NB = Dots<R>::NB, H = GATED ? NB / 2 : NB;  // H results a part
   __shared__ int found;
   __shared__ float sums[kWarps][NB * R];
@@ -272,8 +276,9 @@ cudaError_t launch_dots(const Linear& l, long long sms, cudaStream_t s) {
   // places of 2 x 512 x 2,048: 5.1 us in four slices, 6.5 in two; eight: 9.6 and 8.8).
   const int H = l.gated ? Dots<R>::NB / 2 : Dots<R>::NB;
   auto ctas = [&](int k) { return (l.n + (long long)(kWarps / k) * H - 1) / ((kWarps / k) * H) * l.rows; };
+  const long long at_once = sms * (l.gated ? kDotCtas<R, true, THREADS> : kDotCtas<R, false, THREADS>);
   int kw = 1;
-  while (kw < kWarps && l.k >= 2 * kw * 256 * Dots<R>::U && (!l.offsets || kw < 2 || ctas(2 * kw) <= kDotCtas * sms))
+  while (kw < kWarps && l.k >= 2 * kw * 256 * Dots<R>::U && (!l.offsets || kw < 2 || ctas(2 * kw) <= at_once))
     kw *= 2;
   const long long per = (long long)(kWarps / kw) * H, blocks = (l.n + per - 1) / per;
   const dim3 grid((unsigned)blocks, l.offsets ? l.rows : 1), block(THREADS);
