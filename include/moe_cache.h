@@ -638,7 +638,7 @@ MOE_API int moe_fp4_linear(int wfmt, const uint8_t* d_x_codes, const uint8_t* d_
  *   moe_grouped_linear   one product per expert over its own rows (gate and up, then down);
  *   moe_combine          the routes' outputs, weighted, back into their rows.
  * Operands bf16, exact products, fp32 sums; sums of the tensor cores truncate their additions, as
- * moe_fp4_linear's do, for fp32 results over no more than 512 of K before an fp32 addition.
+ * moe_fp4_linear's do, for fp32 results over no more than 256 of K before an fp32 addition.
  * act(z):  NONE z;  SILU z / (1 + e^-z);  GELU z Phi(z), Phi the normal distribution function;
  *   GELU_TANH (z / 2) (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)));  RELU max(z, 0).  In fp32, a NaN
  *   stays NaN, and -inf is NaN but for NONE and RELU. */

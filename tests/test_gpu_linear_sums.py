@@ -10,16 +10,16 @@ pytestmark = pytest.mark.gpu
 
 
 def sum_bound(K):
-    """Off by, relative to the norm of the results.  A chain takes 16 products an addition, at most 512 of K:
-    32 additions, each truncated, by at most 2^-23 of the running sum, half of that on average, always the same
+    """Off by, relative to the norm of the results.  A chain takes 16 products an addition, at most 256 of K:
+    16 additions, each truncated, by at most 2^-23 of the running sum, half of that on average, always the same
     way.  A sum of random products grows with the root of its length, so the running sum is two thirds of the
     chain's on average.  Chains are independent of one another: their errors grow with the root of their number,
     as the whole sum does, so K does not enter.  They (as sums of 16 products, where these are chains) are added
     in fp32, rounded to nearest: an error spread evenly over half of 2^-23 of the running sum either way,
     2^-24 / sqrt 3 on average, at random signs; the running sum's square is half of the whole's on average:
     sqrt(n / 6) 2^-24 for n.
-    Chains of 1,024 would be off by up to twice the first term, one of 4,096 by eight times."""
-    return 512 / 16 * 2 / 3 * 2.0 ** -24 + (K / 16 / 6) ** 0.5 * 2.0 ** -24
+    Chains of 512 would be off by up to twice the first term, one of 4,096 by sixteen times."""
+    return 256 / 16 * 2 / 3 * 2.0 ** -24 + (K / 16 / 6) ** 0.5 * 2.0 ** -24
 
 
 def off_by(out, y):
