@@ -39,7 +39,7 @@ constexpr long long kLandCycles = 2000 * 1000;
 // K of one chain at most, for results of fp32 and of bf16.  Chains of 256 are off by 2.4e-7 of the norm of the sums, whatever
 // the whole K, one of 4,096 by 4.4e-6 (a plain fp32 form at K 1,024 / 4,096 / 16,384: 2.5e-7 / 6.1e-7 / 1.5e-6); the rounding to
 // bf16 is off by 1.7e-3.  Chains of 256 / 512 / one in tiles of 256 tokens: 65,536 rows of 256 groups, N 1,024, at K 1,024
-// 188 / 175 / 150 us, at 2,048 318 / 300 / 254; 8,192 x 8,192 at K 512 97 / 76 / 76 (which is 512's), at 4,096 350 / 338 / 294.
+// 188 / 175 / 150 us, at 2,048 318 / 300 / 254; 8,192 x 8,192 at K 4,096 350 / 338 / 294, at 512 97 / 76.
 constexpr int kPart = 256, kPartBf16 = 65536;
 constexpr int kMaxCluster = 4;  // CTAs; eights do not all find room at once
 
